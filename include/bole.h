@@ -471,6 +471,92 @@ BOLE_API bole_status_t bole_tree_accept(const float *p_ctx, const float *p_node,
                                int32_t *accepted_len, int32_t *bonus, int32_t *tree_status,
                                bole_stream_t stream);
 
+/*
+ * Gated delta rule: the recurrence whose update subtracts what the state already returns
+ * for a key before it adds the key's new value. For one head, state H [d_k][d_v], token
+ * with key k, value v, query q, decay a and strength b:
+ *     H' = a H,   u = b (v - H'^T k),   H <- H' + k u^T,   o = H^T q.
+ * Value head h reads key head h / (heads / key_heads). q is used as given: a scale, and a
+ * normalisation of q or k, are the caller's.
+ *
+ * Layouts, row-major and contiguous in device memory:
+ *   H0    float [B][H][d_k][d_v]   state of each sequence and value head
+ *   q, k  [T][H_k][d_k]            factor_dtype (bf16 or fp32)
+ *   v     [T][H][d_v]              factor_dtype
+ *   gate  float [T][H]             the decay a itself: finite and >= 0, typically in (0, 1]
+ *   beta  float [T][H]             the strength b
+ *   out   [T][H][d_v]              factor_dtype: what the layer's next product reads. Its
+ *                                  rounding is the only one to that type on a row's way to
+ *                                  H0; states are fp32 throughout
+ * Values must be finite: a NaN or an infinity in one token reaches every token of its
+ * sequence (its head alone), earlier ones of the same 64 tokens among them. Gates are not
+ * checked. Buffers that a call writes must not overlap any other buffer of that call.
+ * Rows that belong to no sequence are neither read nor written.
+ */
+typedef struct {
+    int32_t batch;        /* B >= 0 sequences */
+    int32_t heads;        /* H >= 1 value heads */
+    int32_t key_heads;    /* H_k >= 1, a divisor of heads */
+    int32_t d_k;          /* key width = state rows, 1..256 */
+    int32_t d_v;          /* value width = state columns, 1..256 */
+    int32_t total_tokens; /* T >= 0, rows of the packed arrays */
+    int32_t max_path;     /* commit: row stride of accepted_idx, 0..64 */
+    int32_t factor_dtype; /* bole_dtype_t of q, k, v and out */
+    int32_t flags;        /* 0 or BOLE_FLAG_FORCE_GENERIC */
+} bole_delta_dims_t;
+
+/* Host-only check of the dims, the same check every entry point below runs first. `op` is
+ * 0 for prefill, 1 for step, 2 for tree verify, 3 for commit. */
+BOLE_API bole_status_t bole_delta_check_dims(const bole_delta_dims_t *dims, int32_t op);
+
+/*
+ * Prompts: every token of every sequence, in order, from the state H0 of the sequence,
+ * which is replaced by the state after its last token. seq_offsets int32 [B + 1]: sequence
+ * b owns rows seq_offsets[b] .. seq_offsets[b+1]-1 (any number of them; none leaves its
+ * state as it is). Offsets have to be ordered and inside [0, T]: if any are not, every
+ * sequence is reported BOLE_TREE_BAD_SIZE and nothing is written. seq_status int32 [B]
+ * may be NULL. workspace: at least bole_delta_prefill_workspace_size(dims) bytes, 16-byte
+ * aligned, owned by the caller (NULL where that is 0); contents on entry do not matter,
+ * and calls that may overlap (other streams, graphs that replay at once) need one each.
+ */
+BOLE_API size_t bole_delta_prefill_workspace_size(const bole_delta_dims_t *dims);
+BOLE_API bole_status_t bole_delta_prefill(float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, const float *beta,
+                               const int32_t *seq_offsets, void *out, void *workspace,
+                               size_t workspace_bytes, const bole_delta_dims_t *dims,
+                               int32_t *seq_status, bole_stream_t stream);
+
+/* One token a sequence: row b belongs to sequence b (total_tokens has to equal batch). */
+BOLE_API bole_status_t bole_delta_step(float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, const float *beta, void *out,
+                               const bole_delta_dims_t *dims, bole_stream_t stream);
+
+/*
+ * Tree verification: out[i] = H_i^T q_i for every node of every draft tree, all nodes in
+ * parallel, H0 read once per (sequence, value head) and never written. With D_i the product
+ * of the decays on the root-to-i path and D_{j->i} = D_i / D_j, the updates of a tree solve
+ *     u_i = b_i (v_i - D_i H0^T k_i - sum_{j above i} D_{j->i} (k_i . k_j) u_j),
+ *     o_i = D_i H0^T q_i + sum_{j on path(i)} D_{j->i} (q_i . k_j) u_j.
+ * Trees, statuses and their errors follow bole_tree_verify (at most 64 nodes a tree; rows
+ * of a bad-parent tree become NaN; a tree of bad size is not touched).
+ */
+BOLE_API bole_status_t bole_delta_tree_verify(const float *H0, const void *q, const void *k,
+                               const void *v, const float *gate, const float *beta,
+                               const int32_t *parent, const int32_t *node_offsets, void *out,
+                               const bole_delta_dims_t *dims, int32_t *tree_status,
+                               bole_stream_t stream);
+
+/*
+ * Accepted-path commit: H0 becomes the state after the tokens of each tree's accepted path,
+ * in place. Paths, path_nodes, statuses and errors follow bole_commit_path (a bad tree
+ * keeps its state; a length of 0 leaves it untouched).
+ */
+BOLE_API bole_status_t bole_delta_commit_path(float *H0, const void *k, const void *v,
+                               const float *gate, const float *beta, const int32_t *parent,
+                               const int32_t *node_offsets, const int32_t *accepted_idx,
+                               const int32_t *accepted_len, const bole_delta_dims_t *dims,
+                               int32_t *path_nodes, int32_t *tree_status, bole_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,149 @@
+"""CPU checks of the gated delta rule: the fp64 oracle against what the recurrence fixes by
+itself, and the refusals of the C ABI and the binding (nothing is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from oracle import delta as O
+from tree_speculative_decoding_02_amd import bole, delta
+
+
+def make(seed=1, **kw):
+    a = dict(sizes=[5, 9, 1], heads=4, key_heads=2, d_k=6, d_v=3, factor_dtype=torch.float32)
+    a.update(kw)
+    return W.make_delta(seed, **a)
+
+
+def factors(w):
+    return w.q, w.k, w.v, w.gate, w.beta
+
+
+def test_full_strength_stores_the_value():
+    """With b = 1 and a unit key the state returns exactly the new value for that key."""
+    w = make(strength=1.0)
+    k = w.k.double().numpy()
+    k /= np.linalg.norm(k, axis=-1, keepdims=True)
+    S, _ = O.token(w.H0[0].double().numpy(), None, k[0], w.v[0].double().numpy(),
+                   w.gate[0].double().numpy(), w.beta[0].double().numpy())
+    got = np.einsum("hkv,hk->hv", S, np.repeat(k[0], 2, axis=0))
+    assert np.abs(got - w.v[0].double().numpy()).max() < 1e-12
+
+
+def test_no_strength_is_pure_decay():
+    w = make(strength=0.0)
+    _, S = O.prefill(w.H0, *factors(w), w.offsets)
+    for b in range(3):
+        d = np.prod(w.gate[w.offsets[b]:w.offsets[b + 1]].double().numpy(), axis=0)
+        assert np.abs(S[b] - d[:, None, None] * w.H0[b].double().numpy()).max() < 1e-13
+
+
+def test_orthogonal_keys_add_up():
+    """Over orthonormal keys without decay nothing is subtracted twice: H = H0 + sum of
+    b k (v - H0^T k)^T."""
+    w = make(sizes=[4], key_heads=4, gate_value=1.0)
+    k = np.broadcast_to(np.eye(6)[:4, None], (4, 4, 6))
+    _, S = O.prefill(w.H0, w.q, k, w.v, w.gate, w.beta, w.offsets)
+    H0, v, b = (x.double().numpy() for x in (w.H0, w.v, w.beta))
+    want = H0[0].copy()
+    for t in range(4):
+        want += b[t, :, None, None] * k[t][:, :, None] * (v[t] - H0[0][:, t])[:, None, :]
+    assert np.abs(S[0] - want).max() < 1e-13
+
+
+def test_tree_path_is_a_prompt():
+    """A chain-shaped tree gives the outputs of the same tokens as a prompt, every node of a
+    tree those of its own path, and a commit the state after the path."""
+    w = make(sizes=[12, 7], kind="random", max_path=12)
+    out = O.verify(w.H0, *factors(w), w.parent, w.offsets)
+    for b in range(2):
+        lo = w.offsets[b]
+        for i in range(w.offsets[b + 1] - lo):
+            path, j = [], i
+            while j >= 0:
+                path.insert(0, lo + j)
+                j = w.parent[lo + j]
+            o, S = O.prefill(w.H0[b:b + 1], *(x[path] for x in factors(w)), np.array([0, len(path)]))
+            assert np.abs(out[lo + i] - o[-1]).max() < 1e-13
+            idx = np.array([[p - lo for p in path]])
+            C = O.commit(w.H0[b:b + 1], w.k, w.v, w.gate, w.beta, [lo], idx, [len(path)])
+            assert np.abs(C - S).max() == 0.0
+
+
+def test_key_heads_are_shared_in_order():
+    w = make(heads=6, key_heads=3)
+    out, S = O.prefill(w.H0, *factors(w), w.offsets)
+    k = w.k.repeat_interleave(2, 1)
+    q = w.q.repeat_interleave(2, 1)
+    out2, S2 = O.prefill(w.H0, q, k, w.v, w.gate, w.beta, w.offsets)
+    assert np.array_equal(out, out2) and np.array_equal(S, S2)
+
+
+# ---- refusals
+
+def dims(**kw):
+    d = bole.bole_delta_dims_t(4, 8, 4, 128, 64, 100, 8, bole.BOLE_DTYPE_BF16, 0)
+    for n, x in kw.items():
+        setattr(d, n, x)
+    return d
+
+
+@pytest.mark.parametrize("field,value,op,want", [
+    ("batch", -1, 0, 1), ("heads", 0, 0, 1), ("key_heads", 0, 0, 1), ("key_heads", 3, 2, 1),
+    ("d_k", 0, 0, 1), ("d_v", 0, 3, 1), ("d_k", 257, 0, 2), ("d_v", 257, 2, 2),
+    ("total_tokens", -1, 0, 1), ("total_tokens", 5, 1, 1), ("factor_dtype", 2, 0, 1),
+    ("flags", 2, 0, 1), ("max_path", -1, 3, 1), ("max_path", 65, 3, 2), ("batch", 1 << 28, 2, 2),
+])
+def test_check_dims_refuses(field, value, op, want):
+    assert bole.lib.bole_delta_check_dims(ctypes.byref(dims(**{field: value})), op) == want
+
+
+def test_check_dims_takes_valid():
+    L = bole.lib
+    for op in (0, 2, 3):
+        assert L.bole_delta_check_dims(ctypes.byref(dims()), op) == bole.BOLE_OK
+        assert L.bole_delta_check_dims(ctypes.byref(dims(flags=1)), op) == bole.BOLE_OK
+    assert L.bole_delta_check_dims(ctypes.byref(dims(total_tokens=4)), 1) == bole.BOLE_OK
+    assert L.bole_delta_check_dims(ctypes.byref(dims()), 4) == bole.BOLE_ERR_INVALID_VALUE
+    assert L.bole_delta_check_dims(None, 0) == bole.BOLE_ERR_INVALID_VALUE
+
+
+def test_null_pointers_refused_before_any_launch():
+    L = bole.lib
+    d, bad = ctypes.byref(dims()), bole.BOLE_ERR_INVALID_VALUE
+    one = ctypes.byref(dims(total_tokens=4))
+    P = 0x1000
+    assert L.bole_delta_prefill(*[None] * 9, 0, d, None, None) == bad
+    assert L.bole_delta_prefill(P, P, P, P, P, None, P, P, P, 1 << 40, d, None, None) == bad
+    assert L.bole_delta_step(P, P, P, P, P, P, None, one, None) == bad
+    assert L.bole_delta_step(P, P, P, P, P, P, P, d, None) == bad         # T is not B
+    assert L.bole_delta_tree_verify(P, P, P, P, P, P, None, P, P, d, None, None) == bad
+    assert L.bole_delta_commit_path(P, P, P, P, P, P, P, None, P, d, None, None, None) == bad
+    empty = ctypes.byref(dims(batch=0, total_tokens=0))
+    assert L.bole_delta_prefill(*[None] * 9, 0, empty, None, None) == bole.BOLE_OK
+    assert L.bole_delta_step(*[None] * 7, empty, None) == bole.BOLE_OK
+    assert L.bole_delta_tree_verify(*[None] * 9, empty, None, None) == bole.BOLE_OK
+    assert L.bole_delta_commit_path(*[None] * 9, empty, None, None, None) == bole.BOLE_OK
+
+
+def test_prefill_workspace_is_checked():
+    L = bole.lib
+    d = dims(total_tokens=1000, batch=3)
+    need = L.bole_delta_prefill_workspace_size(ctypes.byref(d))
+    assert L.bole_delta_prefill_workspace_size(ctypes.byref(dims(d_k=0))) == 0
+    assert L.bole_delta_prefill_workspace_size(ctypes.byref(dims(flags=1))) == 0
+    P = 0x1000
+    if need:
+        for ws, size in ((None, need), (P + 8, need), (P, need - 1)):
+            assert L.bole_delta_prefill(P, P, P, P, P, P, P, P, ws, size, ctypes.byref(d), None,
+                                        None) == bole.BOLE_ERR_INVALID_VALUE
+
+
+def test_binding_refuses_host_tensors_and_shapes():
+    w = make()
+    with pytest.raises(ValueError, match="GPU tensor"):
+        delta.bole_delta_step(w.H0, *factors(w))
+    with pytest.raises(TypeError):
+        delta.bole_delta_prefill(w.H0.double(), *factors(w), torch.from_numpy(w.offsets))

@@ -29,7 +29,9 @@ EXPORTED = ("bole_max_tree_nodes", "bole_status_string", "bole_check_dims",
             "bole_tree_verify_lazy_commit_layers", "bole_tree_verify_naive", "bole_commit_path",
             "bole_tree_prepare", "bole_build_tree_workspace_size", "bole_build_tree",
             "bole_build_tree_noalloc",
-            "bole_tree_accept")
+            "bole_tree_accept", "bole_delta_check_dims", "bole_delta_prefill_workspace_size",
+            "bole_delta_prefill", "bole_delta_step", "bole_delta_tree_verify",
+            "bole_delta_commit_path")
 BOLE_ACCEPT_GREEDY, BOLE_ACCEPT_SAMPLE = 0, 1
 BOLE_BUILD_FIXED_BUDGET = 1
 
@@ -61,6 +63,13 @@ class bole_build_dims_t(ctypes.Structure):
 class bole_accept_dims_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("total_nodes", ctypes.c_int32),
                 ("vocab", ctypes.c_int32), ("max_path", ctypes.c_int32), ("mode", ctypes.c_int32)]
+
+
+class bole_delta_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("key_heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("max_path", ctypes.c_int32),
+                ("factor_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 class BoleError(RuntimeError):
@@ -112,6 +121,19 @@ def _load():
     lib.bole_commit_path.argtypes = [P, ctypes.POINTER(bole_factors_t), P, P, D, P, P, P]
     lib.bole_tree_prepare.restype = ctypes.c_int
     lib.bole_tree_prepare.argtypes = [P, P, P, D, P, P, P, P, P]
+    SZ, ND = ctypes.c_size_t, ctypes.POINTER(bole_delta_dims_t)
+    lib.bole_delta_check_dims.restype = ctypes.c_int
+    lib.bole_delta_check_dims.argtypes = [ND, I32]
+    lib.bole_delta_prefill_workspace_size.restype = SZ
+    lib.bole_delta_prefill_workspace_size.argtypes = [ND]
+    lib.bole_delta_prefill.restype = ctypes.c_int
+    lib.bole_delta_prefill.argtypes = [P] * 9 + [SZ, ND, P, P]
+    lib.bole_delta_step.restype = ctypes.c_int
+    lib.bole_delta_step.argtypes = [P] * 7 + [ND, P]
+    lib.bole_delta_tree_verify.restype = ctypes.c_int
+    lib.bole_delta_tree_verify.argtypes = [P] * 9 + [ND, P, P]
+    lib.bole_delta_commit_path.restype = ctypes.c_int
+    lib.bole_delta_commit_path.argtypes = [P] * 9 + [ND, P, P, P]
     return lib
 
 

@@ -1,0 +1,114 @@
+// delta_device.h - device helpers shared by the gated delta rule's kernels: cumulative
+// log-decays in fp64, sequence offsets, accepted paths.
+//
+// Gated delta rule, one head, state H [d_k][d_v]:
+//     H' = a H,   u = b (v - H'^T k),   H <- H' + k u^T,   o = H^T q.
+#pragma once
+
+#include "bole_device.h"
+#include "mfma_util.h"
+
+namespace bole {
+
+struct DeltaShape {
+    int B, H, HK, DK, DV, T;  // sequences, value heads, key heads, widths, packed rows
+};
+
+// log2 of a decay. A decay of 0 (a reset) becomes 2^-10000: every product across it is 0 in
+// fp32, and no difference of logarithms is infinity minus infinity. A NaN stays one.
+__device__ __forceinline__ float log2_decay(float a) {
+    const float l = log2f(a);
+    return l < -10000.f ? -10000.f : l;
+}
+
+// Topology and cumulative log2-decay of a tree whose node i has parent p_loaded in lane i
+// (as wave_topology_cumlog), the sum in fp64: pair weights are exponentials of differences
+// of these sums, and after strong decays the sums are large while later differences are
+// small (in fp32 a sum of 600 leaves an error of 3e-5 in every later pair weight).
+struct WaveTopoD {
+    uint64_t mask;
+    int bad;
+    double L;
+};
+
+__device__ __forceinline__ double shfl_f64(double x, int src) {
+    const long long v = __double_as_longlong(x);
+    return __longlong_as_double((long long)shfl_u64((uint64_t)v, src));
+}
+
+__device__ __forceinline__ WaveTopoD wave_topology_cumlog_f64(int p_loaded, float lg, int n) {
+    const int lane = lane_id();
+    const int p = lane < n ? p_loaded : -1;
+    const bool bad_lane = lane < n && (p < -1 || p >= lane);
+    WaveTopoD t;
+    t.bad = __any(bad_lane) ? BOLE_TREE_BAD_PARENT : BOLE_TREE_OK;
+    const bool live = lane < n && !t.bad;
+    uint64_t m = live ? (1ull << lane) : 0ull;
+    double acc = live ? (double)lg : 0.0;
+    int anc = live ? p : -1;
+    for (int r = 0; r < 6 && __any(anc >= 0); ++r) {
+        const int src = anc < 0 ? lane : anc;
+        const uint64_t m_up = shfl_u64(m, src);
+        const double acc_up = shfl_f64(acc, src);
+        const int anc_up = __shfl(anc, src, 64);
+        if (anc >= 0) {
+            m |= m_up;
+            acc += acc_up;
+            anc = anc_up;
+        }
+    }
+    t.mask = m;
+    t.L = acc;
+    return t;
+}
+
+// Whether all B + 1 offsets are ordered and inside [0, T] (wave-uniform; all lanes active).
+__device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off, int B, int T) {
+    bool bad = false;
+    for (int b = lane_id(); b < B; b += 64) {
+        const int lo = off[b], hi = off[b + 1];
+        bad |= lo < 0 || hi < lo || hi > T;
+    }
+    return !__any(bad);
+}
+
+// The accepted path of tree b, validated by one wavefront with the rules of commit_kernel:
+// lane m gets the packed row of path node m (-1 past the path), len is 0 for a bad tree.
+struct WavePath {
+    int row, len, status;
+};
+
+__device__ __forceinline__ WavePath wave_path(const int32_t *__restrict__ parent,
+                                              const int32_t *__restrict__ node_offsets,
+                                              const int32_t *__restrict__ accepted_idx,
+                                              const int32_t *__restrict__ accepted_len, int b,
+                                              int T, int max_path) {
+    const int lane = lane_id();
+    const TreeRange tr = tree_range(node_offsets, b, T);
+    const int len_raw = accepted_len[b];
+    int st = tr.status, len = 0, x = -1;
+    if (st == BOLE_TREE_OK) {
+        const int n = tr.n;
+        const int p = lane < n ? parent[tr.lo + lane] : -1;
+        const bool len_ok = len_raw >= 0 && len_raw <= max_path && len_raw <= n;
+        x = (len_ok && lane < len_raw) ? accepted_idx[(size_t)b * max_path + lane] : -1;
+        if (__any(lane < n && (p < -1 || p >= lane))) {
+            st = BOLE_TREE_BAD_PARENT;
+        } else if (!len_ok) {
+            st = BOLE_TREE_BAD_PATH;
+        } else {
+            len = len_raw;
+            const int px = __shfl(p, (x >= 0 && x < n) ? x : 0, 64);
+            const int before = __shfl(x, lane > 0 ? lane - 1 : 0, 64);
+            const int prev = lane == 0 ? -1 : before;
+            if (__any(lane < len && (x < 0 || x >= n || px != prev))) st = BOLE_TREE_BAD_PATH;
+        }
+    }
+    WavePath w;
+    w.status = st;
+    w.len = st == BOLE_TREE_OK ? len : 0;
+    w.row = lane < w.len ? tr.lo + x : -1;
+    return w;
+}
+
+}  // namespace bole

@@ -112,4 +112,28 @@ hipError_t launch_tree_accept(const float *p_ctx, const float *p_node, const flo
                               int32_t *accepted_len, int32_t *bonus, int32_t *tree_status,
                               hipStream_t stream);
 
+// Gated delta rule (delta_walk.hip, delta_verify.hip, delta_prefill.hip).
+hipError_t launch_delta_step(float *H0, const void *q, const void *k, const void *v,
+                             const float *gate, const float *beta, void *out,
+                             const bole_delta_dims_t &d, hipStream_t stream);
+hipError_t launch_delta_commit(float *H0, const void *k, const void *v, const float *gate,
+                               const float *beta, const int32_t *parent,
+                               const int32_t *node_offsets, const int32_t *accepted_idx,
+                               const int32_t *accepted_len, const bole_delta_dims_t &d,
+                               int32_t *path_nodes, int32_t *tree_status, hipStream_t stream);
+hipError_t launch_delta_prefill_walk(float *H0, const void *q, const void *k, const void *v,
+                                     const float *gate, const float *beta,
+                                     const int32_t *seq_offsets, void *out,
+                                     const bole_delta_dims_t &d, int32_t *seq_status,
+                                     hipStream_t stream);
+hipError_t launch_delta_verify(const float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, const float *beta, const int32_t *parent,
+                               const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
+                               int32_t *tree_status, hipStream_t stream);
+size_t delta_prefill_workspace(const bole_delta_dims_t &d);
+hipError_t launch_delta_prefill(float *H0, const void *q, const void *k, const void *v,
+                                const float *gate, const float *beta, const int32_t *seq_offsets,
+                                void *out, void *workspace, const bole_delta_dims_t &d,
+                                int32_t *seq_status, hipStream_t stream);
+
 }  // namespace bole

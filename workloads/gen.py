@@ -344,3 +344,53 @@ def make_random(seed: int, batch: int, heads: int, d_k: int, d_v: int,
     return Workload(f"random_{kind}_{seed}", batch, heads, d_k, d_v, vector_gate, factor_dtype,
                     parent, offs, np.concatenate(rhos) if rhos else np.zeros(0), acc_idx,
                     acc_len, [lay], f"random {kind} trees, seed {seed}")
+
+
+@dataclass
+class DeltaWorkload:
+    """Inputs of the gated delta rule's operators: packed rows of prompts or draft trees."""
+    H0: torch.Tensor           # float32 [B, H, d_k, d_v]
+    q: torch.Tensor            # [T, H_k, d_k], bf16 or fp32
+    k: torch.Tensor            # [T, H_k, d_k]
+    v: torch.Tensor            # [T, H, d_v]
+    gate: torch.Tensor         # float32 [T, H]
+    beta: torch.Tensor         # float32 [T, H]
+    offsets: np.ndarray        # int32 [B + 1]
+    parent: np.ndarray         # int32 [T]
+    accepted_idx: np.ndarray   # int32 [B, max_path], -1 padded
+    accepted_len: np.ndarray   # int32 [B]
+
+
+def make_delta(seed: int, sizes: Sequence[int], heads: int, key_heads: int, d_k: int, d_v: int,
+               factor_dtype: torch.dtype = torch.bfloat16, kind: str = "random",
+               max_path: int = 16, gate_value: Optional[float] = None, key_std: float = 1.0,
+               strength: Optional[float] = None, spare_rows: int = 0) -> DeltaWorkload:
+    """Seeded gated-delta inputs for sequences of ``sizes`` tokens: keys of length
+    ``key_std`` and queries of length d_k^-1/2, decays exp(-softplus(N(0,1))) or
+    ``gate_value``, strengths sigmoid(N(0,1)) or ``strength``. Sizes of at most 64 carry a
+    draft tree of the given kind (random_tree) and an accepted path. ``spare_rows`` rows
+    follow the last sequence."""
+    rng = np.random.default_rng(np.random.SeedSequence([seed, 0xde17a]))
+    B = len(sizes)
+    parents = [random_tree(rng, int(n), kind if n <= 64 else "chain") for n in sizes]
+    _, offs = _pack(parents)
+    parent = np.concatenate(parents + [np.full(spare_rows, -1, np.int32)]).astype(np.int32)
+    T = int(offs[-1]) + spare_rows
+    acc_idx = np.full((B, max_path), -1, np.int32)
+    acc_len = np.zeros(B, np.int32)
+    for b, p in enumerate(parents):
+        branch = greedy_branch(p, rng.random(len(p))) if 0 < len(p) <= 64 else []
+        acc_len[b] = rng.integers(0, min(len(branch), max_path) + 1)
+        acc_idx[b, :acc_len[b]] = branch[:acc_len[b]]
+    unit = lambda x, s: s * x / np.maximum(np.linalg.norm(x, axis=-1, keepdims=True), 1e-30)
+    q = _cast(unit(rng.standard_normal((T, key_heads, d_k)), d_k ** -0.5), factor_dtype)
+    k = _cast(unit(rng.standard_normal((T, key_heads, d_k)), key_std), factor_dtype)
+    v = _cast(rng.standard_normal((T, heads, d_v)), factor_dtype)
+    gate = _cast(np.exp(-softplus(rng.standard_normal((T, heads)))), torch.float32)
+    if gate_value is not None:
+        gate = torch.full((T, heads), float(gate_value), dtype=torch.float32)
+    beta = _cast(1.0 / (1.0 + np.exp(-rng.standard_normal((T, heads)))), torch.float32)
+    if strength is not None:
+        beta = torch.full((T, heads), float(strength), dtype=torch.float32)
+    H0 = _cast(rng.standard_normal((B, heads, d_k, d_v)) * 0.3, torch.float32)
+    return DeltaWorkload(H0, q, k, v, gate, beta, offs, parent, acc_idx, acc_len)
