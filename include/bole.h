@@ -557,6 +557,75 @@ BOLE_API bole_status_t bole_delta_commit_path(float *H0, const void *k, const vo
                                const int32_t *accepted_len, const bole_delta_dims_t *dims,
                                int32_t *path_nodes, int32_t *tree_status, bole_stream_t stream);
 
+/*
+ * Attention with a sliding window and visible first tokens over a paged cache: the
+ * attention layers between a hybrid model's linear-recurrence layers, for single tokens,
+ * draft trees and prompts.
+ *
+ * Sequence b has cache_len[b] tokens in the cache, at positions 0 .. cache_len[b] - 1, and
+ * rows node_offsets[b] .. node_offsets[b+1]-1 of q, k and v in this call, whose keys and
+ * values are not in the cache:
+ *  - with a parent array, a draft tree (at most 64 nodes, parents as bole_tree_verify takes
+ *    them): node i is at position cache_len[b] + (nodes on its path) - 1;
+ *  - with parent NULL, the sequence's next tokens, any number of them: row i is at position
+ *    cache_len[b] + i (a prompt, a piece of one, or a single token).
+ * A row at position p sees a key at position s if the key is cached, or the row's own, or a
+ * row's on its path (before it), and p - s < window or s < sinks. Then
+ *     out = sum_s w_s v_s,   w = softmax over the seen keys of scale (q . k_s).
+ * Every row sees itself. Query head h reads key head h / (heads / kv_heads).
+ *
+ * Layouts, row-major and contiguous in device memory:
+ *   q, out   [T][H][d]        dtype (bf16 or fp32)
+ *   k, v     [T][H_kv][d]     dtype
+ *   k_cache, v_cache  [num_pages][H_kv][page_size][d]   dtype
+ *   page_table int32 [B][max_pages]  position s of sequence b is row s % page_size of page
+ *              page_table[b][s / page_size]. Entries of pages none of whose positions any
+ *              row of the call sees are not used and may hold anything
+ *   cache_len  int32 [B]
+ * The softmax's statistics and sums are fp32; bf16 weights are rounded to bf16 before
+ * their product with v, as v is. A NaN or an infinity in a key or value that a row does not
+ * see does not reach that row.
+ *
+ * Offsets have to be ordered and inside [0, T]: if any are not, every sequence is reported
+ * BOLE_TREE_BAD_SIZE and nothing is written. A tree of more than 64 nodes is reported
+ * BOLE_TREE_BAD_SIZE and not touched; rows become NaN of a tree with a bad parent
+ * (BOLE_TREE_BAD_PARENT), and of a sequence whose cache_len lies outside
+ * [0, max_pages page_size] or for which a page that some row sees is not in [0, num_pages)
+ * (BOLE_TREE_BAD_CACHE). seq_status int32 [B] may be NULL.
+ *
+ * workspace: at least bole_window_workspace_size(dims) bytes, 16-byte aligned, owned by the
+ * caller (NULL where that is 0); contents on entry do not matter, and calls that may
+ * overlap need one each. out must not overlap any other buffer of the call.
+ */
+enum { BOLE_TREE_BAD_CACHE = 6 };
+
+typedef struct {
+    int32_t batch;       /* B >= 0 sequences */
+    int32_t heads;       /* H >= 1 query heads */
+    int32_t kv_heads;    /* H_kv >= 1, a divisor of heads */
+    int32_t head_dim;    /* d, 1..256 */
+    int32_t total_rows;  /* T >= 0, rows of the packed arrays */
+    int32_t num_pages;   /* pages of the cache, >= 0 */
+    int32_t page_size;   /* positions a page, a power of two from 1 to 1024 */
+    int32_t max_pages;   /* row stride of page_table, >= 0 */
+    int32_t window;      /* >= 1 */
+    int32_t sinks;       /* >= 0 */
+    int32_t dtype;       /* bole_dtype_t */
+    int32_t flags;       /* 0 or BOLE_FLAG_FORCE_GENERIC */
+    float scale;         /* finite */
+} bole_window_dims_t;
+
+/* Host-only check of the dims, the same check the entry point runs first. */
+BOLE_API bole_status_t bole_window_check_dims(const bole_window_dims_t *dims);
+BOLE_API size_t bole_window_workspace_size(const bole_window_dims_t *dims);
+BOLE_API bole_status_t bole_window_attention(const void *q, const void *k, const void *v,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, const int32_t *cache_len,
+                               const int32_t *parent, const int32_t *node_offsets, void *out,
+                               void *workspace, size_t workspace_bytes,
+                               const bole_window_dims_t *dims, int32_t *seq_status,
+                               bole_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,8 +10,11 @@ from .bole import (bind_build_tree, bole_build_tree, bind_tree_accept, bole_tree
 from .delta import (bind_delta_commit_path, bind_delta_prefill, bind_delta_step,
                     bind_delta_tree_verify, bole_delta_commit_path, bole_delta_prefill,
                     bole_delta_prefill_workspace_size, bole_delta_step, bole_delta_tree_verify)
+from .window import (bind_window_attention, bole_window_attention,
+                     bole_window_workspace_size)
 
-__all__ = ["bind_delta_commit_path", "bind_delta_prefill", "bind_delta_step",
+__all__ = ["bind_window_attention", "bole_window_attention", "bole_window_workspace_size",
+           "bind_delta_commit_path", "bind_delta_prefill", "bind_delta_step",
            "bind_delta_tree_verify", "bole_delta_commit_path", "bole_delta_prefill",
            "bole_delta_prefill_workspace_size", "bole_delta_step", "bole_delta_tree_verify",
            "bind_build_tree", "bole_build_tree", "bind_tree_accept", "bole_tree_accept", "bind_commit_path", "bind_commit_path_layers", "bind_tree_verify",

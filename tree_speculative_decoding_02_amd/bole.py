@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libbole.so")
 
 BOLE_OK, BOLE_ERR_INVALID_VALUE, BOLE_ERR_UNSUPPORTED, BOLE_ERR_HIP, BOLE_ERR_BAD_TREE = 0, 1, 2, 3, 4
 BOLE_TREE_OK, BOLE_TREE_BAD_SIZE, BOLE_TREE_BAD_PARENT, BOLE_TREE_BAD_PATH = 0, 1, 2, 3
-BOLE_TREE_BAD_TOKEN, BOLE_TREE_BAD_GATE = 4, 5
+BOLE_TREE_BAD_TOKEN, BOLE_TREE_BAD_GATE, BOLE_TREE_BAD_CACHE = 4, 5, 6
 BOLE_DTYPE_BF16, BOLE_DTYPE_F32 = 0, 1
 BOLE_GATE_SCALAR, BOLE_GATE_VECTOR = 0, 1
 BOLE_FLAG_FORCE_GENERIC = 1
@@ -31,7 +31,8 @@ EXPORTED = ("bole_max_tree_nodes", "bole_status_string", "bole_check_dims",
             "bole_build_tree_noalloc",
             "bole_tree_accept", "bole_delta_check_dims", "bole_delta_prefill_workspace_size",
             "bole_delta_prefill", "bole_delta_step", "bole_delta_tree_verify",
-            "bole_delta_commit_path")
+            "bole_delta_commit_path", "bole_window_check_dims", "bole_window_workspace_size",
+            "bole_window_attention")
 BOLE_ACCEPT_GREEDY, BOLE_ACCEPT_SAMPLE = 0, 1
 BOLE_BUILD_FIXED_BUDGET = 1
 
@@ -70,6 +71,15 @@ class bole_delta_dims_t(ctypes.Structure):
                 ("key_heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("total_tokens", ctypes.c_int32), ("max_path", ctypes.c_int32),
                 ("factor_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class bole_window_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("total_rows", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class BoleError(RuntimeError):
@@ -134,6 +144,13 @@ def _load():
     lib.bole_delta_tree_verify.argtypes = [P] * 9 + [ND, P, P]
     lib.bole_delta_commit_path.restype = ctypes.c_int
     lib.bole_delta_commit_path.argtypes = [P] * 9 + [ND, P, P, P]
+    WD = ctypes.POINTER(bole_window_dims_t)
+    lib.bole_window_check_dims.restype = ctypes.c_int
+    lib.bole_window_check_dims.argtypes = [WD]
+    lib.bole_window_workspace_size.restype = SZ
+    lib.bole_window_workspace_size.argtypes = [WD]
+    lib.bole_window_attention.restype = ctypes.c_int
+    lib.bole_window_attention.argtypes = [P] * 11 + [SZ, WD, P, P]
     return lib
 
 

@@ -136,4 +136,12 @@ hipError_t launch_delta_prefill(float *H0, const void *q, const void *k, const v
                                 void *out, void *workspace, const bole_delta_dims_t &d,
                                 int32_t *seq_status, hipStream_t stream);
 
+// Windowed attention (window_attention.hip).
+size_t window_workspace(const bole_window_dims_t &d);
+hipError_t launch_window(const void *q, const void *k, const void *v, const void *k_cache,
+                         const void *v_cache, const int32_t *page_table, const int32_t *cache_len,
+                         const int32_t *parent, const int32_t *node_offsets, void *out,
+                         void *workspace, const bole_window_dims_t &d, int32_t *seq_status,
+                         hipStream_t stream);
+
 }  // namespace bole

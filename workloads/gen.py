@@ -394,3 +394,61 @@ def make_delta(seed: int, sizes: Sequence[int], heads: int, key_heads: int, d_k:
         beta = torch.full((T, heads), float(strength), dtype=torch.float32)
     H0 = _cast(rng.standard_normal((B, heads, d_k, d_v)) * 0.3, torch.float32)
     return DeltaWorkload(H0, q, k, v, gate, beta, offs, parent, acc_idx, acc_len)
+
+
+@dataclass
+class WindowWorkload:
+    """Inputs of windowed attention: packed rows, a paged cache and its tables."""
+    q: torch.Tensor            # [T, H, d], bf16 or fp32
+    k: torch.Tensor            # [T, H_kv, d]
+    v: torch.Tensor            # [T, H_kv, d]
+    k_cache: torch.Tensor      # [num_pages, H_kv, page_size, d]
+    v_cache: torch.Tensor
+    page_table: torch.Tensor   # int32 [B, max_pages]
+    cache_len: torch.Tensor    # int32 [B]
+    offsets: np.ndarray        # int32 [B + 1]
+    parent: np.ndarray         # int32 [T]
+
+
+def make_window(seed: int, sizes: Sequence[int], cached: Sequence[int], heads: int, kv_heads: int,
+                d: int, page_size: int, window: int, sinks: int,
+                dtype: torch.dtype = torch.bfloat16, kind: str = "random", spread: float = 1.0,
+                spare_rows: int = 0, poison: bool = True) -> WindowWorkload:
+    """Seeded windowed-attention inputs: sizes[b] rows behind cached[b] cached tokens, keys,
+    queries (times ``spread``) and values N(0, 1). Pages lie in the cache in random order.
+    With ``poison``, everything that no row may read is NaN or an invalid page: cache slots
+    past a sequence's end, slots outside every row's view, spare pages, entries of pages that
+    nobody sees."""
+    rng = np.random.default_rng(np.random.SeedSequence([seed, 0x817d0]))
+    B = len(sizes)
+    parents = [random_tree(rng, int(n), kind if n <= 64 else "chain") for n in sizes]
+    _, offs = _pack(parents)
+    parent = np.concatenate(parents + [np.full(spare_rows, -1, np.int32)]).astype(np.int32)
+    T = int(offs[-1]) + spare_rows
+    most = max(1, max((-(-int(c) // page_size) for c in cached), default=1) + 1)
+    table = np.full((B, most), -1 if poison else 0, np.int64)
+    used = []
+    for b in range(B):
+        for i in range(-(-int(cached[b]) // page_size)):
+            near = (i + 1) * page_size > max(0, cached[b] - window + 1) and window > 1
+            if not poison or near or i * page_size < min(sinks, cached[b]):
+                used.append((b, i))
+    pages = len(used) + 2
+    order = rng.permutation(pages)
+    kc = rng.standard_normal((pages, kv_heads, page_size, d))
+    vc = rng.standard_normal((pages, kv_heads, page_size, d))
+    seen = np.zeros((pages, page_size), bool)
+    for m, (b, i) in enumerate(used):
+        table[b, i] = order[m]
+        s = i * page_size + np.arange(page_size)
+        seen[order[m]] = (s < cached[b]) & ((s < sinks) | (s > cached[b] - window))
+    if poison:
+        hide = ~seen[:, None, :, None] & np.ones(kc.shape, bool)
+        kc[hide] = np.nan
+        vc[hide] = np.nan
+        table[(table < 0) & (rng.random(table.shape) < 0.5)] = pages + 12345
+    q = _cast(rng.standard_normal((T, heads, d)) * spread, dtype)
+    k, v = (_cast(rng.standard_normal((T, kv_heads, d)), dtype) for _ in range(2))
+    return WindowWorkload(q, k, v, _cast(kc, dtype), _cast(vc, dtype),
+                          torch.from_numpy(table.astype(np.int32)),
+                          torch.tensor(list(map(int, cached)), dtype=torch.int32), offs, parent)
