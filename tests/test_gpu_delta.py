@@ -192,6 +192,21 @@ def test_prefill_bad_offsets_touch_nothing(lib):
         assert (out == -7.0).all() and torch.equal(t["H0"].cpu(), w.H0)
 
 
+def test_prefill_rows_before_the_first_sequence(lib):
+    """Sequences that start behind rows of nobody: those rows are not read."""
+    w = make(27, [70, 0, 129], SHAPES[0])
+    t = on_gpu(w)
+    H = t.pop("H0")
+    u = {n: torch.cat([torch.full((150, *x.shape[1:]), float("nan"), dtype=x.dtype, device=dev()), x])
+         for n, x in t.items()}
+    out, status = torch.full_like(u["v"], -7.0), torch.full((3,), -1, dtype=torch.int32, device=dev())
+    lib.bole_delta_prefill(H, **u, seq_offsets=g(w.offsets) + 150, out=out, seq_status=status)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(H, S, w)
+    check_out(out[150:], ref, w, column_norms(w))
+    assert (out[:150] == -7.0).all() and status.tolist() == [0] * 3
+
+
 TREES = [([1], "random"), ([64, 33, 0, 5, 16, 17], "random"), ([32, 31], "bestfirst"),
          ([64, 50], "chain"), ([64, 20], "star"), ([48], "deep")]
 

@@ -214,6 +214,22 @@ def test_no_cache_and_no_rows(lib):
     assert status.tolist() == [0, 0]
 
 
+def test_rows_before_the_first_sequence(lib):
+    """Sequences that start behind rows of nobody: those rows stay as they are."""
+    for lead, sizes, tree in ((70, [40, 0, 3], False), (5, [1, 1, 1], False), (300, [64, 9, 1], True)):
+        w = make(55, sizes, [100, 33, 7], SHAPES[0], 64, 4)
+        t = on_gpu(w)
+        pad = lambda x: torch.cat([torch.full((lead, *x.shape[1:]), float("nan"), dtype=x.dtype, device=dev()), x])
+        u = dict(t, node_offsets=t["node_offsets"] + lead, **{n: pad(t[n]) for n in ("q", "k", "v")})
+        par = torch.cat([torch.full((lead,), 99, dtype=torch.int32, device=dev()), g(w.parent)]) if tree else None
+        out, status = torch.full_like(u["q"], -7.0), torch.full((3,), -1, dtype=torch.int32, device=dev())
+        for force in (False, True):
+            lib.bole_window_attention(**u, window=64, sinks=4, out=out, parent=par, seq_status=status,
+                                      force_generic=force)
+            assert (out[:lead] == -7.0).all() and status.tolist() == [0] * 3
+            check(out[lead:], oracle_of(w, 64, 4, tree), w, 140)
+
+
 def test_unaligned_buffers(lib):
     w = make(53, [20, 1, 40], [100, 33, 7], SHAPES[0], 64, 4)
     t = on_gpu(w)

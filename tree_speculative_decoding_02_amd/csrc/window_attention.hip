@@ -98,22 +98,17 @@ __global__ __launch_bounds__(64) void window_generic_kernel(const WindowArgs a) 
         if (lane + 64 * j < s.D) o[lane + 64 * j] = (T)(acc[j] / sum);
 }
 
-size_t window_workspace(const bole_window_dims_t &d) {
-    (void)d;
-    return 0;
-}
-
 hipError_t launch_window(const void *q, const void *k, const void *v, const void *k_cache,
                          const void *v_cache, const int32_t *page_table, const int32_t *cache_len,
                          const int32_t *parent, const int32_t *node_offsets, void *out,
                          void *workspace, const bole_window_dims_t &d, int32_t *seq_status,
                          hipStream_t stream) {
-    (void)workspace;
     const WindowArgs a = {q, k, v, k_cache, v_cache, page_table, cache_len, parent, node_offsets, out,
                           seq_status,
                           {d.batch, d.heads, d.kv_heads, d.head_dim, d.total_rows, d.num_pages,
                            __builtin_ctz((unsigned)d.page_size), d.max_pages, d.window, d.sinks,
                            d.scale}};
+    if (window_mfma_applies(d, a)) return launch_window_mfma(a, d, workspace, stream);
     const dim3 grid((unsigned)(d.total_rows > 0 ? d.total_rows : 1), (unsigned)d.heads);
     if (d.dtype == BOLE_DTYPE_F32)
         window_generic_kernel<float><<<grid, dim3(64), 0, stream>>>(a);

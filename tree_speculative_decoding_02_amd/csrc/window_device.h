@@ -21,6 +21,11 @@ struct WindowArgs {
     WindowShape s;
 };
 
+// The matrix-core kernels (window_mfma.hip).
+bool window_mfma_applies(const bole_window_dims_t &d, const WindowArgs &a);
+hipError_t launch_window_mfma(const WindowArgs &a, const bole_window_dims_t &d, void *workspace,
+                              hipStream_t stream);
+
 // The last sequence whose first row is at or before `row` (ordered offsets): the one that
 // owns the row, if any does. B >= 1.
 __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int B, int row) {
