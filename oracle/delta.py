@@ -38,6 +38,28 @@ def prefill(H0, q, k, v, gate, beta, offsets):
     return out, S
 
 
+def pair_terms(H0, q, k, v, gate, beta, offsets, chunk=64):
+    """[T, H, d_v]: sum over the tokens j of i's chunk, up to i, of D_{j->i} |q_i . k_j| |u_j|,
+    the magnitude of an output's terms that a weight per token pair stands before."""
+    H0, q, k, v, gate, beta = map(_f64, (H0, q, k, v, gate, beta))
+    H = v.shape[1]
+    q, k = (np.repeat(x, H // x.shape[1], axis=1) for x in (q, k))
+    mag = np.zeros(v.shape)
+    for b in range(H0.shape[0]):
+        S = H0[b].copy()
+        for t in range(offsets[b], offsets[b + 1]):
+            if (t - offsets[b]) % chunk == 0:
+                us, ks, D = [], [], []
+            S = gate[t][:, None, None] * S
+            u = beta[t][:, None] * (v[t] - np.einsum("hkv,hk->hv", S, k[t]))
+            S = S + k[t][:, :, None] * u[:, None, :]
+            D = [d * gate[t] for d in D] + [np.ones(H)]
+            us.append(np.abs(u)), ks.append(k[t])
+            for d, kk, uu in zip(D, ks, us):
+                mag[t] += (d * np.abs((q[t] * kk).sum(-1)))[:, None] * uu
+    return mag
+
+
 def verify(H0, q, k, v, gate, beta, parent, offsets):
     """out [T, H, d_v] of every node of every tree."""
     H0, q, k, v, gate, beta = map(_f64, (H0, q, k, v, gate, beta))

@@ -8,7 +8,9 @@ Tolerances, set from the arithmetic:
     nothing decays;
   - outputs: the same relative to |q| |H| (the largest sum a product with the state can have),
     rounded once: half a step of the output type relative to the value. bf16 factors take
-    products with the state as sums of two bf16 terms, 2^-16 each of |q| |H|, four of them.
+    products with the state as sums of two bf16 terms, 2^-16 each of |q| |H|, four of them;
+  - prompts in bf16 round each token pair's weight once to bf16 for the output (not for the
+    state): half a step of each such term.
 """
 import numpy as np
 import pytest
@@ -53,14 +55,21 @@ def check_states(got, ref, w, many=1.0):
     assert np.isfinite(got).all() and d.max() <= state_tol(w, many), d.max()
 
 
-def check_out(got, ref, w, states, many=1.0):
+def check_prompt(got, ref, w, states, many=1.0):
+    extra = 0.0
+    if w.q.dtype == BF16:
+        extra = 2.0 ** -8 * O.pair_terms(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_out(got, ref, w, states, many, extra)
+
+
+def check_out(got, ref, w, states, many=1.0, extra=0.0):
     """states: an upper bound of |H| by column, [H] (the largest over tokens)."""
     half = 2.0 ** -8 if w.q.dtype == BF16 else 2.0 ** -24
     alg = state_tol(w, many) + (4 * 2.0 ** -16 if w.q.dtype == BF16 else 0.0)
     qn = np.linalg.norm(w.q.double().numpy(), axis=-1)
     qn = np.repeat(qn, w.v.shape[1] // qn.shape[1], axis=1)          # [T, H]
     rows = np.isfinite(ref).all(axis=(1, 2))
-    lim = half * np.abs(ref) + (alg * qn * states[None])[:, :, None]
+    lim = half * np.abs(ref) + (alg * qn * states[None])[:, :, None] + extra
     e = np.abs(got.double().cpu().numpy() - ref)[rows]
     assert (e <= lim[rows]).all(), float((e / lim[rows]).max())
 
@@ -110,7 +119,7 @@ def test_prefill(lib, shape, sizes):
     lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out, seq_status=status)
     ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
     check_states(t["H0"], S, w)
-    check_out(out, ref, w, column_norms(w))
+    check_prompt(out, ref, w, column_norms(w))
     assert (out[-3:] == -7.0).all() and status.tolist() == [0] * len(sizes)
     for b, n in enumerate(sizes):  # no token: the state keeps its bits
         if n == 0:
@@ -132,7 +141,7 @@ def test_prefill_gates_and_strengths(lib, shape, kw):
     if kw.get("gate_value") == 1.02:
         many *= 1.02 ** 90
     check_states(t["H0"], S, w, many)
-    check_out(out, ref, w, column_norms(w) * (1.02 ** 90 if many > 100 else 1.0), many)
+    check_prompt(out, ref, w, column_norms(w) * (1.02 ** 90 if many > 100 else 1.0), many)
 
 
 @pytest.mark.parametrize("shape", SHAPES[:4], ids=IDS[:4])
@@ -146,7 +155,7 @@ def test_prefill_after_strong_decays(lib, shape):
     out = lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets))
     ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
     check_states(t["H0"], S, w, 10.0)
-    check_out(out, ref, w, column_norms(w), 10.0)
+    check_prompt(out, ref, w, column_norms(w), 10.0)
 
 
 @pytest.mark.parametrize("shape", SHAPES[:4], ids=IDS[:4])
@@ -158,7 +167,7 @@ def test_prefill_with_repeated_keys(lib, shape):
     out = lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets))
     ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
     check_states(t["H0"], S, w, 2.0)
-    check_out(out, ref, w, column_norms(w), 2.0)
+    check_prompt(out, ref, w, column_norms(w), 2.0)
 
 
 def test_prefill_is_step_by_step_and_resumable(lib):
@@ -203,7 +212,7 @@ def test_prefill_rows_before_the_first_sequence(lib):
     lib.bole_delta_prefill(H, **u, seq_offsets=g(w.offsets) + 150, out=out, seq_status=status)
     ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
     check_states(H, S, w)
-    check_out(out[150:], ref, w, column_norms(w))
+    check_prompt(out[150:], ref, w, column_norms(w))
     assert (out[:150] == -7.0).all() and status.tolist() == [0] * 3
 
 
@@ -338,7 +347,7 @@ def test_unaligned_and_sliced_buffers(lib):
         out = off(torch.zeros_like(t["v"]), 3)
         lib.bole_delta_prefill(**u, seq_offsets=g(w.offsets), out=out)
         check_states(u["H0"], S, w)
-        check_out(out, ref, w, column_norms(w))
+        check_prompt(out, ref, w, column_norms(w))
 
 
 def test_prefill_then_verify_then_commit(lib):
@@ -391,7 +400,7 @@ def test_prefill_on_two_streams_at_once(lib):
     for w, t, out in zip(ws, ts, outs):
         ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
         check_states(t["H0"], S, w)
-        check_out(out, ref, w, column_norms(w))
+        check_prompt(out, ref, w, column_norms(w))
     # a stream given by hand: outputs and workspace belong to it
     t = on_gpu(ws[0])
     torch.cuda.synchronize()

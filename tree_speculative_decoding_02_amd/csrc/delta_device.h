@@ -10,6 +10,22 @@
 
 namespace bole {
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Transposing LDS read: of each 16 lanes, lane i gets column i, rows 0..3, of the 4 x 16 block
+// whose row r, columns 4c .. 4c + 3 lane 4r + c points to (8 bytes a lane).
+__device__ __forceinline__ bf16x4 read_transposed(const __bf16 *p) {
+    const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4 *)(__attribute__((address_space(3))) void *)p);
+    return __builtin_bit_cast(bf16x4, r);
+}
+
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 struct DeltaShape {
     int B, H, HK, DK, DV, T;  // sequences, value heads, key heads, widths, packed rows
 };
@@ -70,6 +86,30 @@ __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off,
         bad |= lo < 0 || hi < lo || hi > T;
     }
     return !__any(bad);
+}
+
+// Tile `slot` of the packed rows (MT packed rows a tile): sequence b owns slots from
+// floor(off[b] G / MT) + b, at least one each (slots before the first sequence's are nobody's).
+// `ordered`: whether the offsets are.
+__device__ __forceinline__ bool locate(const int32_t *__restrict__ off, int B, int T, int G, int MT,
+                                       int slot, int &b, int &slot0, bool &ordered) {
+    bool bad = false;
+    int before = 0;
+    for (int c = 0; c < B; c += 64) {
+        const int x = c + lane_id();
+        bool at = false;
+        if (x < B) {
+            const int lo = off[x], hi = off[x + 1];
+            bad |= lo < 0 || hi < lo || hi > T;
+            at = (int64_t)lo * G / MT + x <= slot;
+        }
+        before += (int)__popcll(__ballot(at));
+    }
+    b = __builtin_amdgcn_readfirstlane(before - 1);
+    ordered = !__any(bad);
+    if (!ordered || b < 0) return false;
+    slot0 = __builtin_amdgcn_readfirstlane((int)((int64_t)off[b] * G / MT) + b);
+    return true;
 }
 
 // The accepted path of tree b, validated by one wavefront with the rules of commit_kernel:

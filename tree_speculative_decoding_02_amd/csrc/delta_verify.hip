@@ -7,7 +7,7 @@
 // a unit lower triangular system in the updates, the same for every column of the state.
 #include <type_traits>
 
-#include "delta_device.h"
+#include "delta_mfma.h"
 #include "launch.h"
 
 namespace bole {
@@ -100,6 +100,199 @@ __global__ __launch_bounds__(256) void delta_verify_generic_kernel(
     }
 }
 
+// bf16, d_k 64 or 128, d_v a multiple of 16: one workgroup of four wavefronts per (sequence,
+// value head, 64 NT columns). The loads of its state columns are in flight while it forms the
+// tree's system (delta_mfma.h); then every wavefront carries its 16 NT columns through
+//     R = V - diag(2^L) K H0,   U = X diag(b) R,   O = diag(2^L) Q H0 + P U
+// in registers, each product's results being the next one's operand. H0, X, R, P and U are
+// taken as two bf16 terms (2^-17 left), so that the output's own rounding is the one that
+// counts.
+//
+// NT = 2: lane c of 16 holds columns 2c and 2c + 1, and a state row's 32 columns are one
+// 128-byte read.
+template <int DK, int NT>
+__global__ __launch_bounds__(256, 2) void delta_verify_kernel(
+    const float *__restrict__ H0, const __bf16 *__restrict__ q, const __bf16 *__restrict__ k,
+    const __bf16 *__restrict__ v, const float *__restrict__ gate, const float *__restrict__ beta,
+    const int32_t *__restrict__ parent, const int32_t *__restrict__ node_offsets,
+    __bf16 *__restrict__ out, int32_t *__restrict__ tree_status, const DeltaShape s) {
+    typedef float hvec __attribute__((ext_vector_type(NT)));
+    typedef __bf16 vvec __attribute__((ext_vector_type(NT)));
+    constexpr int KS = DK / 32;
+    __shared__ DeltaTokens t;
+    const int unit = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    const int col = lane & 15, g = lane >> 4;
+    const int b = unit / s.H, h = unit - b * s.H, hk = h / (s.H / s.HK);
+    const bool first = h == 0 && blockIdx.y == 0 && tid == 0 && tree_status;
+    const TreeRange tr = tree_range(node_offsets, b, s.T);
+    if (tr.status != BOLE_TREE_OK) {
+        if (first) tree_status[b] = tr.status;
+        return;
+    }
+    const int lo = tr.lo, n = tr.n;
+    const size_t sk = (size_t)s.HK * DK, sv = (size_t)s.H * s.DV;
+    const __bf16 *kb = k + (size_t)lo * sk + (size_t)hk * DK, *qb = q + (size_t)lo * sk + (size_t)hk * DK;
+    const int c0 = (blockIdx.y * 4 + wave) * 16 * NT + NT * col;  // the lane's columns
+    const bool live = c0 < s.DV && n > 0;                         // wave-uniform: 16 NT divides d_v
+    const float *Hu = H0 + (size_t)unit * DK * s.DV + c0;
+    hvec hr[KS][8];
+    if (live) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                hr[ks][e] = __builtin_nontemporal_load(
+                    reinterpret_cast<const hvec *>(Hu + (size_t)(32 * ks + 8 * g + e) * s.DV));
+    }
+    if (tid < 64) {
+        const bool in = tid < n;
+        const float lg = in ? log2_decay(gate[(size_t)(lo + tid) * s.H + h]) : 0.f;
+        const WaveTopoD w = wave_topology_cumlog_f64(in ? parent[lo + tid] : -1, lg, n);
+        t.mask[tid] = w.mask;
+        t.L[tid] = w.L;
+        t.start[tid] = __builtin_amdgcn_exp2f((float)w.L);
+        t.beta[tid] = in ? beta[(size_t)(lo + tid) * s.H + h] : 0.f;
+        if (tid == 0) t.bad = w.bad;
+    }
+    __syncthreads();
+    if (first) tree_status[b] = t.bad;
+    const size_t v0 = (size_t)lo * sv + (size_t)h * s.DV;
+    if (t.bad) {
+        for (int e = tid; e < n * s.DV; e += 256)
+            out[v0 + (size_t)(e / s.DV) * sv + e % s.DV] = (__bf16)__builtin_nanf("");
+        return;
+    }
+    if (n == 0) return;
+    delta_system<DK>(t, kb, qb, sk, n);
+    // row tile m has tokens of the tree
+    auto used = [&](int m) { return tile_token(m, 0) < n; };
+    if (!live) return;
+    const size_t vc = v0 + c0;
+    f32x4 r[4][NT], o[4][NT];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) r[m][c] = o[m][c] = (f32x4)0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        bf16x8 hb[NT][2];
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            f32x4 x, y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = hr[ks][e][c];
+                y[e] = hr[ks][4 + e][c];
+            }
+            split_terms8<2>(x, y, hb[c]);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if (!used(m)) continue;
+            const int row = tile_token(m, col);
+            bf16x8 ka = (bf16x8)(__bf16)0.f, qa = (bf16x8)(__bf16)0.f;
+            if (row < n) {
+                ka = load16(kb + (size_t)row * sk + 32 * ks + 8 * g);
+                qa = load16(qb + (size_t)row * sk + 32 * ks + 8 * g);
+            }
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int e = 1; e >= 0; --e) {
+                    r[m][c] = mfma16_bf16(ka, hb[c][e], r[m][c]);
+                    o[m][c] = mfma16_bf16(qa, hb[c][e], o[m][c]);
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // rows of one step at a time in registers
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (!used(m)) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = tile_token(m, 4 * g + e);
+            const float d = t.start[i];
+            vvec vv = (vvec)(__bf16)0.f;
+            if (i < n) vv = *reinterpret_cast<const vvec *>(v + vc + (size_t)i * sv);
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                r[m][c][e] = (float)vv[c] - d * r[m][c][e];
+                o[m][c][e] *= d;
+            }
+        }
+    }
+    // U from R, then O, 32 tokens (two row tiles) of the right operand at a time
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+        bf16x8 rb[2][NT][2];
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) split_terms8<2>(r[2 * sb][c], r[2 * sb + 1][c], rb[sb][c]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if (!used(m)) continue;
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                if (step == 0) r[m][c] = (f32x4)0.f;
+#pragma unroll
+            for (int sb = 0; sb <= (m >> 1); ++sb) {
+                f32x4 x, y;
+                bf16x8 a[2];
+                if (step == 0) x_piece(t, tile_token(m, col), sb, g, x, y);
+                else p_piece(t, tile_token(m, col), sb, g, x, y);
+                split_terms8<2>(x, y, a);
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    if (step == 0) r[m][c] = mfma_terms<2>(a, rb[sb][c], r[m][c]);
+                    else o[m][c] = mfma_terms<2>(a, rb[sb][c], o[m][c]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = tile_token(m, 4 * g + e);
+            vvec y;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) y[c] = (__bf16)o[m][c][e];
+            if (i < n) *reinterpret_cast<vvec *>(out + vc + (size_t)i * sv) = y;
+        }
+}
+
+static bool verify_covers(const bole_delta_dims_t &d, const void *H0, const void *q, const void *k,
+                          const void *v, const void *out) {
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k);
+    const uintptr_t wide = reinterpret_cast<uintptr_t>(H0) | 2 * reinterpret_cast<uintptr_t>(v) |
+                           2 * reinterpret_cast<uintptr_t>(out);
+    return d.factor_dtype == BOLE_DTYPE_BF16 && !(d.flags & BOLE_FLAG_FORCE_GENERIC) &&
+           (d.d_k == 64 || d.d_k == 128) && d.d_v % 16 == 0 && rows % 16 == 0 && wide % 8 == 0;
+}
+
+template <int DK>
+static hipError_t launch_mfma(const float *H0, const void *q, const void *k, const void *v,
+                              const float *gate, const float *beta, const int32_t *parent,
+                              const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
+                              int32_t *tree_status, hipStream_t stream) {
+    const DeltaShape s = {d.batch, d.heads, d.key_heads, d.d_k, d.d_v, d.total_tokens};
+    const unsigned units = (unsigned)d.batch * (unsigned)d.heads;
+    const dim3 block(256);
+    const __bf16 *qb = static_cast<const __bf16 *>(q), *kb = static_cast<const __bf16 *>(k),
+                 *vb = static_cast<const __bf16 *>(v);
+    __bf16 *ob = static_cast<__bf16 *>(out);
+    // 32 columns a wavefront where that still gives each of the four some
+    if (d.d_v % 32 == 0 && d.d_v > 64)
+        delta_verify_kernel<DK, 2><<<dim3(units, (d.d_v + 127) / 128), block, 0, stream>>>(H0, qb, kb, vb, gate, beta, parent,
+                                                               node_offsets, ob, tree_status, s);
+    else
+        delta_verify_kernel<DK, 1><<<dim3(units, (d.d_v + 63) / 64), block, 0, stream>>>(H0, qb, kb, vb, gate, beta, parent,
+                                                               node_offsets, ob, tree_status, s);
+    return hipGetLastError();
+}
+
 template <typename TF>
 static hipError_t launch_generic(const float *H0, const void *q, const void *k, const void *v,
                                  const float *gate, const float *beta, const int32_t *parent,
@@ -118,6 +311,11 @@ hipError_t launch_delta_verify(const float *H0, const void *q, const void *k, co
                                const float *gate, const float *beta, const int32_t *parent,
                                const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
                                int32_t *tree_status, hipStream_t stream) {
+    if (verify_covers(d, H0, q, k, v, out))
+        return d.d_k == 64 ? launch_mfma<64>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
+                                             tree_status, stream)
+                           : launch_mfma<128>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
+                                              tree_status, stream);
     return d.factor_dtype == BOLE_DTYPE_F32
                ? launch_generic<float>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
                                        tree_status, stream)
