@@ -26,6 +26,12 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Barrier for data in LDS alone. __syncthreads also waits for every global load in flight, and
+// with it a prefetch for the next step would end at the first barrier of this one.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 struct DeltaShape {
     int B, H, HK, DK, DV, T;  // sequences, value heads, key heads, widths, packed rows
 };

@@ -78,7 +78,7 @@ __device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[N], const bf16x8 (
 }
 
 // Fills t (A, P, X) for the n tokens at rows 0 .. n - 1 of k and q; t.L, t.beta and t.mask are
-// set and a barrier passed. Four wavefronts; ends with a barrier. From n on, rows and columns
+// set and a barrier passed; n >= 1. Four wavefronts; ends with a barrier. From n on, rows and columns
 // are those of the identity (X) and zero (A, P).
 template <int DK>
 __device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__restrict__ k,
@@ -86,8 +86,8 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__res
     const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
     constexpr int KS = DK / 32;
     // ---- pair products: row tile `wave` (tokens 16 wave ..), column tiles up to it
-    auto piece = [&](const __bf16 *p, int row, int ks) {
-        return row < n ? load16(p + (size_t)row * stride + 32 * ks + 8 * g) : (bf16x8)(__bf16)0.f;
+    auto piece = [&](const __bf16 *p, int row, int ks) {  // rows past the last repeat it
+        return load16(p + (size_t)min(row, n - 1) * stride + 32 * ks + 8 * g);
     };
     bf16x8 ka[KS], qa[KS];
 #pragma unroll
@@ -146,7 +146,7 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__res
 #pragma unroll
             for (int r = 0; r < 4; ++r) t.X[square_at(base + 4 * g + r, 16 * jt + col)] = 0.f;
     }
-    __syncthreads();
+    lds_barrier();
     // ---- column `wave` of the blocks below the diagonal, downwards: each needs the diagonal
     // blocks (above) and the blocks over it, which this wavefront wrote
     const int j = wave;
@@ -168,7 +168,7 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__res
 #pragma unroll
         for (int r = 0; r < 4; ++r) t.X[square_at(16 * i + 4 * g + r, 16 * j + col)] = y[r];
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 // Row `token`, columns 32 s + 8 g .. + 7 of X diag(b).

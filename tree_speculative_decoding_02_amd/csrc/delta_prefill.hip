@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
         w.start[tid] = in ? __builtin_amdgcn_exp2f((float)c.L) : 0.f;
         w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - c.L)) : 0.f;
     }
-    __syncthreads();
+    lds_barrier();
     const size_t sk = (size_t)s.HK * DK, at = (size_t)lo * sk + (size_t)hk * DK;
     delta_system<DK>(t, a.k + at, a.q + at, sk, n);
 #pragma unroll
@@ -141,29 +141,29 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
         for (int i = 0; i < N; ++i)
             *reinterpret_cast<bf16x4 *>(&dst[i][c][m >> 1][lane][4 * (m & 1)]) = y[i];
     };
-    // the next chunk's loads
+    // The next chunk's loads, raw: nothing waits for them before they are used. Rows past the
+    // last token repeat it: their columns of X diag(b) and their `end` are zero, and their
+    // outputs are not stored.
     bf16x8 kr[PER], qn[KS], pn[2];
     f32x4 xn[2][2];
-    float vn[4][NT], startn[4], endn[4], decayn;
+    __bf16 vn[4][NT];
+    float startn[4], endn[4], decayn;
     const int my_row = tile_token(wave, col);
     auto fetch = [&](int chunk) {
-        const int t0 = chunk * kChunk, left = n - t0;
+        const int t0 = chunk * kChunk, last = min(kChunk, n - t0) - 1;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = tid + 256 * j, row = e / CH, c = e % CH;
-            kr[j] = (bf16x8)(__bf16)0.f;
-            if (row < left) kr[j] = load16(kb + (size_t)(t0 + row) * sk + 8 * c);
+            const int e = tid + 256 * j;
+            kr[j] = load16(kb + (size_t)(t0 + min(e / CH, last)) * sk + 8 * (e % CH));
         }
+        const __bf16 *qrow = qb + (size_t)(t0 + min(my_row, last)) * sk + 8 * g;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            qn[ks] = (bf16x8)(__bf16)0.f;
-            if (my_row < left) qn[ks] = load16(qb + (size_t)(t0 + my_row) * sk + 32 * ks + 8 * g);
-        }
+        for (int ks = 0; ks < KS; ++ks) qn[ks] = load16(qrow + 32 * ks);
         const ChunkSystem &w = ws[(size_t)chunk * s.H];
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
-            if (sb > (wave >> 1)) continue;
-            const int f = piece_of(wave, sb);
+            // the first two wavefronts have one piece: they load it twice
+            const int f = piece_of(wave, min(sb, wave >> 1));
             xn[sb][0] = *reinterpret_cast<const f32x4 *>(&w.x[f][lane][0]);
             xn[sb][1] = *reinterpret_cast<const f32x4 *>(&w.x[f][lane][4]);
             pn[sb] = *reinterpret_cast<const bf16x8 *>(&w.p[f][lane][0]);
@@ -174,10 +174,9 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
             startn[e] = w.start[i];
             endn[e] = w.end[i];
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-                vn[e][c] = i < left ? (float)a.v[v0 + (size_t)(t0 + i) * sv + 16 * c] : 0.f;
+            for (int c = 0; c < NT; ++c) vn[e][c] = a.v[v0 + (size_t)(t0 + min(i, last)) * sv + 16 * c];
         }
-        decayn = w.start[min(left, kChunk) - 1];
+        decayn = w.start[last];
     };
     auto stage = [&](int buf) {
 #pragma unroll
@@ -195,7 +194,7 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
     fetch(0);
     stage(0);
     put_state();
-    __syncthreads();
+    lds_barrier();
     for (int chunk = 0; chunk < chunks; ++chunk) {
         const int buf = chunk & 1, t0 = chunk * kChunk;
         bf16x8 q[KS], p[2];
@@ -206,7 +205,6 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
         for (int ks = 0; ks < KS; ++ks) q[ks] = qn[ks];
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
-            if (sb > (wave >> 1)) continue;
             p[sb] = pn[sb];
             split_terms8<3>(xn[sb][0], xn[sb][1], x[sb]);
         }
@@ -214,7 +212,7 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
         for (int e = 0; e < 4; ++e) {
             start[e] = startn[e], end[e] = endn[e];
 #pragma unroll
-            for (int c = 0; c < NT; ++c) v[e][c] = vn[e][c];
+            for (int c = 0; c < NT; ++c) v[e][c] = (float)vn[e][c];
         }
         if (chunk + 1 < chunks) fetch(chunk + 1);
 
@@ -246,7 +244,7 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
             }
             put(r[c], wave, s_r, c);
         }
-        __syncthreads();
+        lds_barrier();
         // ---- U = X diag(b) R
         f32x4 u[NT];
 #pragma unroll
@@ -268,7 +266,7 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
             for (int e = 0; e < 4; ++e) ue[e] = end[e] * u[c][e];
             put(ue, wave, s_e, c);
         }
-        __syncthreads();
+        lds_barrier();
         // ---- S <- decay S + K^T (end U): K^T through the transposing read
 #pragma unroll
         for (int j = 0; j < TILES; ++j) {
@@ -306,7 +304,7 @@ __global__ __launch_bounds__(256, 2) void delta_scan_kernel(const PrefillArgs a,
         if (chunk + 1 < chunks) {
             stage(buf ^ 1);
             put_state();
-            __syncthreads();
+            lds_barrier();
         }
     }
 #pragma unroll

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void delta_verify_generic_kernel(
 //     R = V - diag(2^L) K H0,   U = X diag(b) R,   O = diag(2^L) Q H0 + P U
 // in registers, each product's results being the next one's operand. H0, X, R, P and U are
 // taken as two bf16 terms (2^-17 left), so that the output's own rounding is the one that
-// counts.
+// counts. Row slots past the last node repeat it: their columns of X diag(b) are zero.
 //
 // NT = 2: lane c of 16 holds columns 2c and 2c + 1, and a state row's 32 columns are one
 // 128-byte read.
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         t.beta[tid] = in ? beta[(size_t)(lo + tid) * s.H + h] : 0.f;
         if (tid == 0) t.bad = w.bad;
     }
-    __syncthreads();
+    lds_barrier();
     if (first) tree_status[b] = t.bad;
     const size_t v0 = (size_t)lo * sv + (size_t)h * s.DV;
     if (t.bad) {
@@ -189,12 +189,8 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if (!used(m)) continue;
-            const int row = tile_token(m, col);
-            bf16x8 ka = (bf16x8)(__bf16)0.f, qa = (bf16x8)(__bf16)0.f;
-            if (row < n) {
-                ka = load16(kb + (size_t)row * sk + 32 * ks + 8 * g);
-                qa = load16(qb + (size_t)row * sk + 32 * ks + 8 * g);
-            }
+            const size_t row = (size_t)min(tile_token(m, col), n - 1) * sk + 32 * ks + 8 * g;
+            const bf16x8 ka = load16(kb + row), qa = load16(qb + row);
 #pragma unroll
             for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -212,8 +208,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         for (int e = 0; e < 4; ++e) {
             const int i = tile_token(m, 4 * g + e);
             const float d = t.start[i];
-            vvec vv = (vvec)(__bf16)0.f;
-            if (i < n) vv = *reinterpret_cast<const vvec *>(v + vc + (size_t)i * sv);
+            const vvec vv = *reinterpret_cast<const vvec *>(v + vc + (size_t)min(i, n - 1) * sv);
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
                 r[m][c][e] = (float)vv[c] - d * r[m][c][e];

@@ -11,7 +11,8 @@
 // The keys a tile of rows can see are one virtual list: the cached first tokens, the cached
 // window behind the tile's first row, the call's own first tokens, the call's own rows. Tiles
 // of 64 keys that every row sees are taken without tests; the others test each key. Slots
-// past the end are loaded as zeros, so nothing that no row of the sequence sees is read.
+// past the end repeat the last key, so nothing that no row of the sequence sees is read, and
+// no load depends on a branch.
 //
 // Two shapes of workgroup:
 //  - rows: 128 rows, 32 a wavefront, keys and values staged in LDS for all four wavefronts
@@ -123,6 +124,7 @@ __device__ __forceinline__ int own_row(const RowTile &t, int x) {
 // Page of key x, -1 for the call's own rows and past the end.
 __device__ __forceinline__ int key_page(const WindowShape &s, const int32_t *__restrict__ table,
                                         const RowTile &t, int x) {
+    x = min(x, t.total - 1);
     return x < t.n1 + t.n2 ? table[cached_position(t, x) >> s.page_shift] : -1;
 }
 
@@ -221,18 +223,14 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     int page = -1;
     bf16x8 kr[PER], vr[PER];
     auto fetch = [&](int tile) {
-        const uint32_t mine = key_row(s, t, hk, tile * kKeys + lane, page);
+        const uint32_t mine = key_row(s, t, hk, min(tile * kKeys + lane, t.total - 1), page);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = tid + 256 * j, x = tile * kKeys + e / CH, c = e % CH;
+            const int e = tid + 256 * j, x = min(tile * kKeys + e / CH, t.total - 1), c = e % CH;
             const size_t off = (size_t)(uint32_t)__shfl((int)mine, e / CH, 64) * D + 8 * c;
             const bool own = x >= t.n1 + t.n2;
-            kr[j] = (bf16x8)(__bf16)0.f;
-            vr[j] = (bf16x8)(__bf16)0.f;
-            if (x < t.total) {
-                kr[j] = load16(static_cast<const __bf16 *>(own ? a.k : a.k_cache) + off);
-                vr[j] = load16(static_cast<const __bf16 *>(own ? a.v : a.v_cache) + off);
-            }
+            kr[j] = load16(static_cast<const __bf16 *>(own ? a.k : a.k_cache) + off);
+            vr[j] = load16(static_cast<const __bf16 *>(own ? a.v : a.v_cache) + off);
         }
     };
     auto stage = [&](int buf) {
@@ -253,7 +251,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         fetch(first);
         page = key_page(s, table, t, (first + 1) * kKeys + lane);
         stage(0);
-        __syncthreads();
+        lds_barrier();
     }
     for (int tile = first; tile < last; ++tile) {
         const int buf = (tile - first) & 1;
@@ -321,7 +319,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                 }
             }
         if (tile + 1 < last) stage(buf ^ 1);
-        __syncthreads();
+        lds_barrier();
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
@@ -410,24 +408,20 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
     int page = -1;
     auto fetch = [&](int tile) {
         const int x0 = tile * kKeys, cached = t.n1 + t.n2;
-        const uint32_t mine = key_row(s, t, hk, x0 + lane, page);
+        const uint32_t mine = key_row(s, t, hk, min(x0 + lane, t.total - 1), page);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int x = x0 + 16 * r + col;
+            const int x = min(x0 + 16 * r + col, t.total - 1);
             const size_t off = (size_t)(uint32_t)__shfl((int)mine, 16 * r + col, 64) * D + 8 * g;
             const __bf16 *p = static_cast<const __bf16 *>(x >= cached ? a.k : a.k_cache) + off;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) {
-                kf[r][ks] = (bf16x8)(__bf16)0.f;
-                if (x < t.total) kf[r][ks] = load16(p + 32 * ks);
-            }
+            for (int ks = 0; ks < D / 32; ++ks) kf[r][ks] = load16(p + 32 * ks);
         }
 #pragma unroll
         for (int j = 0; j < VPER; ++j) {
-            const int e = lane + 64 * j, x = x0 + e / CH;
+            const int e = lane + 64 * j, x = min(x0 + e / CH, t.total - 1);
             const size_t off = (size_t)(uint32_t)__shfl((int)mine, e / CH, 64) * D + 8 * (e % CH);
-            vr[j] = (bf16x8)(__bf16)0.f;
-            if (x < t.total) vr[j] = load16(static_cast<const __bf16 *>(x >= cached ? a.v : a.v_cache) + off);
+            vr[j] = load16(static_cast<const __bf16 *>(x >= cached ? a.v : a.v_cache) + off);
         }
     };
     f32x4 acc[D / 16];
@@ -507,7 +501,7 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
     l += __shfl_xor(l, 32, 64);
 
     // the four wavefronts' parts: O^T as [wave][row][D + 4]
-    __syncthreads();
+    lds_barrier();
     float *s_o = reinterpret_cast<float *>(s_mem);
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt)
@@ -516,7 +510,7 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
         s_ml[wave][col][0] = m;
         s_ml[wave][col][1] = l;
     }
-    __syncthreads();
+    lds_barrier();
     const int r = tid >> 4, d0 = (tid & 15) * (D / 16);  // a row's 16 threads
     if (t.tile * kTokenTile + r >= rows) return;
     float mm = -INFINITY, ll = 0.f;
