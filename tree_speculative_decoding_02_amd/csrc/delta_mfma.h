@@ -43,28 +43,32 @@ __device__ __forceinline__ int tile_token(int m, int r) {
     return 32 * (m >> 1) + 8 * (r >> 2) + 4 * (m & 1) + (r & 3);
 }
 
-// fp32 x as bf16 terms of falling size: two leave 2^-17 of it, three 2^-25.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// fp32 x as bf16 terms of falling size: two leave 2^-17 of it, three 2^-25. In pairs, for the
+// packed conversion.
 template <int N>
-__device__ __forceinline__ void split_terms(float x, __bf16 (&y)[N]) {
+__device__ __forceinline__ void split_terms2(f32x2 x, bf16x2 (&y)[N]) {
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-        y[t] = (__bf16)x;
-        x -= (float)y[t];
+        y[t] = __builtin_convertvector(x, bf16x2);
+        if (t + 1 < N) x -= __builtin_convertvector(y[t], f32x2);
     }
 }
 
 template <int N>
 __device__ __forceinline__ void split_terms8(const f32x4 &a, const f32x4 &b, bf16x8 (&y)[N]) {
+    bf16x2 p[4][N];
+    split_terms2<N>(__builtin_shufflevector(a, a, 0, 1), p[0]);
+    split_terms2<N>(__builtin_shufflevector(a, a, 2, 3), p[1]);
+    split_terms2<N>(__builtin_shufflevector(b, b, 0, 1), p[2]);
+    split_terms2<N>(__builtin_shufflevector(b, b, 2, 3), p[3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        __bf16 t[N];
-        split_terms<N>(a[e], t);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i][e] = t[i];
-        split_terms<N>(b[e], t);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i][4 + e] = t[i];
-    }
+    for (int i = 0; i < N; ++i)
+        y[i] = __builtin_shufflevector(__builtin_shufflevector(p[0][i], p[1][i], 0, 1, 2, 3),
+                                       __builtin_shufflevector(p[2][i], p[3][i], 0, 1, 2, 3), 0, 1, 2,
+                                       3, 4, 5, 6, 7);
 }
 
 // c += a b with a and b in N terms each, leaving out the products below the last term.
