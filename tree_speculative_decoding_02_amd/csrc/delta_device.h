@@ -84,6 +84,17 @@ __device__ __forceinline__ WaveTopoD wave_topology_cumlog_f64(int p_loaded, floa
     return t;
 }
 
+// Inclusive sum over lanes 0 .. lane, in fp64.
+__device__ __forceinline__ double wave_sum_up_f64(double x) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double y = shfl_f64(x, lane >= d ? lane - d : lane);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
 // Whether all B + 1 offsets are ordered and inside [0, T] (wave-uniform; all lanes active).
 __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off, int B, int T) {
     bool bad = false;

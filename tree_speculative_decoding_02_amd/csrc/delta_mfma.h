@@ -8,8 +8,8 @@
 //     P_ij = 2^{L_i - L_j} (q_i . k_j)       for j on the path of i, else 0,
 //     U = X diag(b) (V - diag(2^L) K H0),   X = (I + A)^-1,   O = diag(2^L) Q H0 + P U.
 // X is formed once and serves every state column: the four 16 x 16 diagonal blocks by forward
-// substitution, the blocks below them by fp32 matrix products
-//     X_ij = -X_ii sum_{k=j}^{i-1} A_ik X_kj.
+// substitution, what lies below them by fp32 matrix products, first within the two 32 x 32
+// diagonal blocks, then between them:   X_ij = -X_ii A_ij X_jj   (blocks of either size).
 // Products of k and q are bf16 products with fp32 sums, exact but for those sums; decays and
 // everything after them are fp32.
 #pragma once
@@ -24,7 +24,7 @@ struct DeltaTokens {           // LDS of one workgroup, 50 KB
     float A[kChunk * kChunk];  // A, X, P: element (i, j) at square_at(i, j)
     float X[kChunk * kChunk];
     float P[kChunk * kChunk];
-    double L[kChunk];
+    float L[kChunk], Lrest[kChunk];      // cumulative log2-decay (fp64) as two fp32 terms
     float beta[kChunk], start[kChunk];   // strengths, 2^L
     uint64_t mask[kChunk];
     int bad;
@@ -81,54 +81,107 @@ __device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[N], const bf16x8 (
     return c;
 }
 
-// Fills t (A, P, X) for the n tokens at rows 0 .. n - 1 of k and q; t.L, t.beta and t.mask are
-// set and a barrier passed; n >= 1. Four wavefronts; ends with a barrier. From n on, rows and columns
-// are those of the identity (X) and zero (A, P).
+// A wavefront's own rows of k and q (row tile `wave`, tokens 16 wave ..) as operands; rows past
+// the last repeat it. Loaded early, they are in flight while the decays are summed up.
 template <int DK>
-__device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__restrict__ k,
-                                             const __bf16 *__restrict__ q, size_t stride, int n) {
+struct SystemRows {
+    bf16x8 k[DK / 32], q[DK / 32];
+    __device__ __forceinline__ void load(const __bf16 *kp, const __bf16 *qp, size_t stride, int n) {
+        const int row = 16 * (threadIdx.x >> 6) + (lane_id() & 15);
+        const size_t at = (size_t)min(row, n - 1) * stride + 8 * (lane_id() >> 4);
+#pragma unroll
+        for (int ks = 0; ks < DK / 32; ++ks) {
+            k[ks] = load16(kp + at + 32 * ks);
+            q[ks] = load16(qp + at + 32 * ks);
+        }
+    }
+};
+
+// c + A B for 16 x 16 blocks of squares in LDS: block (ai, aj) of a, block (bi, bj) of b.
+__device__ __forceinline__ f32x4 block_product(const float *a, int ai, int aj, const float *b, int bi,
+                                               int bj, f32x4 c) {
+    const int col = lane_id() & 15, g = lane_id() >> 4;
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[square_at(16 * ai + col, 16 * aj + 4 * g)]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)  // k index 4 g + r on both sides
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], b[square_at(16 * bi + 4 * g + r, 16 * bj + col)], c, 0,
+                                                 0, 0);
+    return c;
+}
+
+// c - A B with B in registers as products leave it (row 4 g + r, column col).
+__device__ __forceinline__ f32x4 block_product_reg(const float *a, int ai, int aj, const f32x4 &b, f32x4 c) {
+    const int col = lane_id() & 15, g = lane_id() >> 4;
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[square_at(16 * ai + col, 16 * aj + 4 * g)]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], -b[r], c, 0, 0, 0);
+    return c;
+}
+
+__device__ __forceinline__ void put_block(float *a, int ai, int aj, const f32x4 &v) {
+    const int col = lane_id() & 15, g = lane_id() >> 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[square_at(16 * ai + 4 * g + r, 16 * aj + col)] = v[r];
+}
+
+// Fills t (X, P) for the n tokens at rows 0 .. n - 1 of k; t.L, t.beta and (TREE) t.mask are set
+// for all 64 tokens, those from n on with their predecessor's decay and no strength, and a
+// barrier passed; n >= 1. Four wavefronts; ends with a barrier. What the pieces below read is
+// defined: X's columns from n on are those of the identity (times no strength), P's rows from n
+// on belong to no token. Every other element right of the 32 x 32 diagonal blocks is not.
+template <int DK, bool TREE>
+__device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<DK> &rows,
+                                             const __bf16 *__restrict__ k, size_t stride, int n) {
     const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
     constexpr int KS = DK / 32;
-    // ---- pair products: row tile `wave` (tokens 16 wave ..), column tiles up to it
-    auto piece = [&](const __bf16 *p, int row, int ks) {  // rows past the last repeat it
-        return load16(p + (size_t)min(row, n - 1) * stride + 32 * ks + 8 * g);
-    };
-    bf16x8 ka[KS], qa[KS];
+    const f32x4 zero = (f32x4)0.f;
+    // ---- pair products: row tile `wave`, column tiles up to it
+    {
+        const int i0 = 16 * wave + 4 * g;
+        const f32x4 li = *reinterpret_cast<const f32x4 *>(&t.L[i0]);
+        const f32x4 lr = *reinterpret_cast<const f32x4 *>(&t.Lrest[i0]);
+        const f32x4 bi = *reinterpret_cast<const f32x4 *>(&t.beta[i0]);
+        uint32_t mask[4][2];
+        if (TREE) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        ka[ks] = piece(k, 16 * wave + col, ks);
-        qa[ks] = piece(q, 16 * wave + col, ks);
-    }
+            for (int r = 0; r < 4; ++r) {
+                mask[r][0] = (uint32_t)t.mask[i0 + r];
+                mask[r][1] = (uint32_t)(t.mask[i0 + r] >> 32);
+            }
+        }
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-        f32x4 kk = (f32x4)0.f, qk = (f32x4)0.f;
-        if (jt <= wave && 16 * wave < n) {
+        for (int jt = 0; jt < 4; ++jt) {
+            if (jt > wave) break;
+            f32x4 kk = zero, qk = zero;
+            const size_t at = (size_t)min(16 * jt + col, n - 1) * stride + 8 * g;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const bf16x8 b = jt == wave ? ka[ks] : piece(k, 16 * jt + col, ks);
-                kk = mfma16_bf16(ka[ks], b, kk);
-                qk = mfma16_bf16(qa[ks], b, qk);
+                const bf16x8 b = load16(k + at + 32 * ks);
+                kk = mfma16_bf16(rows.k[ks], b, kk);
+                qk = mfma16_bf16(rows.q[ks], b, qk);
             }
-        }
-        const int j = 16 * jt + col;
+            const float lj = t.L[16 * jt + col], ljr = t.Lrest[16 * jt + col];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * wave + 4 * g + r;
-            float av = 0.f, pv = 0.f;
-            if (j <= i && i < n && ((t.mask[i] >> j) & 1ull)) {
-                const float d = __builtin_amdgcn_exp2f((float)(t.L[i] - t.L[j]));
-                pv = d * qk[r];
-                if (j < i) av = t.beta[i] * d * kk[r];
+            for (int r = 0; r < 4; ++r) {
+                float d = __builtin_amdgcn_exp2f((li[r] - lj) + (lr[r] - ljr));
+                bool on = jt < wave || col <= 4 * g + r;
+                if (TREE) on = (mask[r][jt >> 1] >> (16 * (jt & 1) + col)) & 1u;
+                d = on ? d : 0.f;
+                qk[r] *= d;
+                kk[r] *= bi[r] * d;  // the diagonal is not read
             }
-            t.A[square_at(i, j)] = av;
-            t.P[square_at(i, j)] = pv;
+            put_block(t.P, wave, jt, qk);
+            put_block(t.A, wave, jt, kk);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if ((wave & 1) == 0) {  // the part of the 32 x 32 diagonal blocks that is right of the tiles
+            put_block(t.P, wave, wave + 1, zero);
+            put_block(t.X, wave, wave + 1, zero);
+        }
     }
-    // ---- X: diagonal block `wave`, column `col` (every lane group computes the same), from
-    // what this wavefront itself wrote
-    {
-        const int base = 16 * wave;
+    lds_barrier();
+    // ---- X: the diagonal blocks, block g and column `col` of it a lane of one wavefront
+    if (wave == 0) {
+        const int base = 16 * g;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -136,42 +189,35 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const __bf16 *__res
 #pragma unroll
             for (int c = 0; c < (i + 3) / 4; ++c)
                 row[c] = *reinterpret_cast<const f32x4 *>(&t.A[square_at(base + i, base + 4 * c)]);
-            float acc[2] = {i == col ? 1.f : 0.f, 0.f};
+            float acc[4] = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < i; ++j) acc[j & 1] = fmaf(-row[j >> 2][j & 3], x[j], acc[j & 1]);
-            x[i] = acc[0] + acc[1];
-            if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few rows of A in registers
+            for (int j = 0; j < i; ++j) acc[j & 3] = fmaf(-row[j >> 2][j & 3], x[j], acc[j & 3]);
+            x[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            t.X[square_at(base + i, base + col)] = x[i];
         }
-        // lane group g writes rows 4 g ..; the blocks right of the diagonal are zero
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if ((i >> 2) == g) t.X[square_at(base + i, base + col)] = x[i];
-        for (int jt = wave + 1; jt < 4; ++jt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) t.X[square_at(base + 4 * g + r, 16 * jt + col)] = 0.f;
     }
     lds_barrier();
-    // ---- column `wave` of the blocks below the diagonal, downwards: each needs the diagonal
-    // blocks (above) and the blocks over it, which this wavefront wrote
-    const int j = wave;
-    for (int i = j + 1; i < 4; ++i) {
-        f32x4 y = (f32x4)0.f;
-        if (16 * i < n) {
-            f32x4 s = (f32x4)0.f;
-            for (int b = j; b < i; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    s = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                        t.A[square_at(16 * i + col, 16 * b + 4 * r + g)],
-                        t.X[square_at(16 * b + 4 * r + g, 16 * j + col)], s, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)  // k index 4 g + r on both sides
-                y = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                    t.X[square_at(16 * i + col, 16 * i + 4 * g + r)], -s[r], y, 0, 0, 0);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) t.X[square_at(16 * i + 4 * g + r, 16 * j + col)] = y[r];
+    // ---- within the 32 x 32 blocks
+    if (wave < 2) {
+        const int i = 2 * wave + 1, j = 2 * wave;
+        f32x4 y = zero;
+        if (16 * i < n) y = block_product_reg(t.X, i, i, block_product(t.A, i, j, t.X, j, j, zero), zero);
+        put_block(t.X, i, j, y);
     }
+    lds_barrier();
+    // ---- between them: T = A X of the first 32 tokens (left in X's unused upper right), then
+    // -X T of the last
+    const int i = 2 + (wave >> 1), j = wave & 1;
+    f32x4 y = zero;
+    if (n > 32) {
+        f32x4 s = block_product(t.A, i, 1, t.X, 1, j, zero);
+        if (j == 0) s = block_product(t.A, i, 0, t.X, 0, 0, s);
+        if (i == 2) put_block(t.X, j, 2, s);
+        lds_barrier();
+        y = block_product_reg(t.X, i, i, s, zero);
+        if (i == 3) y = y - block_product(t.X, 3, 2, t.X, j, 2, zero);
+    }
+    put_block(t.X, i, j, y);
     lds_barrier();
 }
 

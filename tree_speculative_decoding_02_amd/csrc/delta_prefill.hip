@@ -52,20 +52,23 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
     const int lo = a.offsets[b] + (slot - slot0) * kChunk, n = min(kChunk, a.offsets[b + 1] - lo);
     if (n <= 0) return;
     ChunkSystem &w = a.ws[(size_t)slot * s.H + h];
+    const size_t sk = (size_t)s.HK * DK, row0 = (size_t)lo * sk + (size_t)hk * DK;
+    SystemRows<DK> rows;
+    rows.load(a.k + row0, a.q + row0, sk, n);
     if (tid < 64) {
+        // tokens past the last do not decay and have no strength
         const bool in = tid < n;
-        const size_t at = (size_t)(lo + tid) * s.H + h;
-        const WaveTopoD c = wave_topology_cumlog_f64(tid - 1, in ? log2_decay(a.gate[at]) : 0.f, n);
-        t.mask[tid] = c.mask;
-        t.L[tid] = c.L;
+        const size_t at = (size_t)(lo + min(tid, n - 1)) * s.H + h;
+        const double L = wave_sum_up_f64(in ? (double)log2_decay(a.gate[at]) : 0.0);
+        t.L[tid] = (float)L;
+        t.Lrest[tid] = (float)(L - (double)(float)L);
         t.beta[tid] = in ? a.beta[at] : 0.f;
-        const double all = shfl_f64(c.L, n - 1);
-        w.start[tid] = in ? __builtin_amdgcn_exp2f((float)c.L) : 0.f;
-        w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - c.L)) : 0.f;
+        const double all = shfl_f64(L, 63);
+        w.start[tid] = in ? __builtin_amdgcn_exp2f((float)L) : 0.f;
+        w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - L)) : 0.f;
     }
     lds_barrier();
-    const size_t sk = (size_t)s.HK * DK, at = (size_t)lo * sk + (size_t)hk * DK;
-    delta_system<DK>(t, a.k + at, a.q + at, sk, n);
+    delta_system<DK, false>(t, rows, a.k + row0, sk, n);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
         if (sb > (wave >> 1)) continue;
@@ -102,6 +105,8 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     __shared__ __align__(16) __bf16 s_r[3][2][64][8];    // R
     __shared__ __align__(16) __bf16 s_e[3][2][64][8];    // end U, for the state
     __shared__ __align__(16) __bf16 s_u[2][2][64][8];    // U, for the output
+    __shared__ __align__(16) __bf16 s_v[2][kChunk * 16]; // V, the workgroup's columns
+    __shared__ __align__(16) float s_w[2][2 * kChunk];   // start, end
     const DeltaShape &s = a.s;
     // the column groups of a unit go to one XCD (workgroups are dealt to the eight in turn):
     // they read the same rows and systems, and fill each other's output lines
@@ -142,7 +147,6 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     };
 
     if (chain) {
-        const char *vb = reinterpret_cast<const char *>(a.v) + (size_t)lo * svb + c0;
         // register e of state row tile j: row tile_token(m0 + j, 4 g + e), as tokens are laid out
         const int m0 = wave * TILES;
         char *Hu = reinterpret_cast<char *>(a.H0 + (size_t)unit * DK * s.DV + 16 * cg);
@@ -155,61 +159,41 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
         for (int j = 0; j < TILES; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) st[j][e] = state_at(j, e);
-        const uint32_t voff = my_token * svb + 2 * col;
         bf16x8 x[2][3];
-        __bf16 v[4];
-        f32x4 start, end;
-        float decay;
-        auto fetch_v = [&](int t0, int last, const ChunkSystem &w) {
-            const char *v0 = vb + (size_t)t0 * svb;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t vo = voff + e * svb;
-                if (last < kChunk - 1) vo = min(my_token + e, last) * svb + 2 * col;
-                v[e] = *reinterpret_cast<const __bf16 *>(v0 + vo);
-            }
-            start = *reinterpret_cast<const f32x4 *>(&w.start[my_token]);
-        };
         // right of the diagonal X is zero: the first two wavefronts' second piece
 #pragma unroll
         for (int i = 0; i < 3; ++i) x[1][i] = (bf16x8)(__bf16)0.f;
-        auto fetch_x = [&](int last, const ChunkSystem &w) {
+        auto fetch_x = [&](int chunk) {
+            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws + min(chunk, chunks - 1) * ws_step);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 x[0][i] = load16(&w.x[i][piece_of(wave, 0)][lane][0]);
                 if (wave >= 2) x[1][i] = load16(&w.x[i][piece_of(wave, 1)][lane][0]);
             }
-            end = *reinterpret_cast<const f32x4 *>(&w.end[my_token]);
-            decay = w.start[last];
         };
-        {
-            const int last = min(kChunk, n) - 1;
-            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws);
-            fetch_v(0, last, w);
-            fetch_x(last, w);
-        }
+        fetch_x(0);
 #pragma unroll
         for (int j = 0; j < TILES; ++j) put(st[j], m0 + j, s_s);
         lds_barrier();
         for (int chunk = 0; chunk < chunks; ++chunk) {
-            const int next = min(chunk + 1, chunks - 1), t1 = next * kChunk, last = min(kChunk, n - t1) - 1;
-            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws + next * ws_step);
+            const int buf = chunk & 1;
             // ---- R = V - diag(start) K S for the wavefront's tokens, a sum for each term of S
             f32x4 r[3];
 #pragma unroll
             for (int i = 0; i < 3; ++i) r[i] = (f32x4)0.f;
-            const __bf16 *krow = &s_k[chunk & 1][my_row * KP + 8 * g];
+            const __bf16 *krow = &s_k[buf][my_row * KP + 8 * g];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const bf16x8 ka = load16(krow + 32 * ks);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) r[i] = mfma16_bf16(ka, load16(&s_s[i][ks][lane][0]), r[i]);
             }
+            const f32x4 start = *reinterpret_cast<const f32x4 *>(&s_w[buf][my_token]);
+            const bf16x4 v = read_transposed(&s_v[buf][(my_token + (col >> 2)) * 16 + 4 * (col & 3)]);
             r[0] += r[2] + r[1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[0][e] = fmaf(-start[e], r[0][e], (float)v[e]);
             put(r[0], wave, s_r);
-            fetch_v(t1, last, w);
             lds_barrier();
             // ---- U = X diag(b) R, a sum for each size of product and half
             f32x4 u[2][3];
@@ -226,13 +210,14 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
                     for (int k = 0; k <= i; ++k) u[sb][i] = mfma16_bf16(x[sb][k], rb[i - k], u[sb][i]);
             }
+            const f32x4 end = *reinterpret_cast<const f32x4 *>(&s_w[buf][kChunk + my_token]);
             u[0][0] += u[1][0] + ((u[0][2] + u[1][2]) + (u[0][1] + u[1][1]));
             put(end * u[0][0], wave, s_e);
             put(u[0][0], wave, s_u);
-            const float d = decay;
-            fetch_x(last, w);
+            fetch_x(chunk + 1);
             lds_barrier();
             // ---- S <- decay S + K^T (end U): K^T through the transposing read
+            const float d = s_w[buf][min(n - chunk * kChunk, kChunk) - 1];
             bf16x8 eb[2][3];
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb)
@@ -247,8 +232,8 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
                 for (int sb = 0; sb < 2; ++sb) {
                     // state rows of lanes 4c .. 4c + 3: 32 (m / 2) + 8 c + 4 (m % 2) ..
-                    const __bf16 *kt = &s_k[chunk & 1][(32 * sb + 8 * g + (col >> 2)) * KP + 32 * (m >> 1) +
-                                                       8 * (col & 3) + 4 * (m & 1)];
+                    const __bf16 *kt = &s_k[buf][(32 * sb + 8 * g + (col >> 2)) * KP + 32 * (m >> 1) +
+                                                 8 * (col & 3) + 4 * (m & 1)];
                     const bf16x8 ka = join(read_transposed(kt), read_transposed(kt + 4 * KP));
 #pragma unroll
                     for (int i = 2; i >= 0; --i) y[sb] = mfma16_bf16(ka, eb[sb][i], y[sb]);
@@ -265,12 +250,13 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     } else {
         const char *kb = reinterpret_cast<const char *>(a.k) + (size_t)lo * skb + (size_t)hk * DK * 2;
         const char *qb = reinterpret_cast<const char *>(a.q) + (size_t)lo * skb + (size_t)hk * DK * 2;
+        const char *vb = reinterpret_cast<const char *>(a.v) + (size_t)lo * svb + c0;
         char *ob = reinterpret_cast<char *>(a.out) + (size_t)lo * svb + c0;
         const uint32_t koff = (uint32_t)(tid / CH) * skb + 16 * (tid % CH), qoff = my_row * skb + 16 * g,
-                       ooff = my_token * svb + 2 * col;
-        bf16x8 kr[PER], q[KS], p[2];
-        f32x4 start;
-        auto fetch_k = [&](int t0, int last) {
+                       ooff = my_row * svb + 8 * g;
+        bf16x8 kr[PER], q[KS], p[2], vr;
+        // with K: V's 64 x 32 bytes by the first two wavefronts, start and end by half the third
+        auto fetch_k = [&](int t0, int last, const ChunkSystem &w) {
             const char *k0 = kb + (size_t)t0 * skb;
             constexpr int ROWS = 256 / CH;
 #pragma unroll
@@ -279,14 +265,17 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
                 if (last < kChunk - 1) off = min(tid / CH + ROWS * j, last) * skb + 16 * (tid % CH);
                 kr[j] = load16(reinterpret_cast<const __bf16 *>(k0 + off));
             }
+            if (tid < 128)
+                vr = load16(reinterpret_cast<const __bf16 *>(vb + (size_t)t0 * svb + (uint32_t)min(tid >> 1, last) * svb + 16 * (tid & 1)));
+            else if (tid < 160)
+                vr = load16(reinterpret_cast<const __bf16 *>(&w.start[0]) + 8 * (tid - 128));
         };
-        auto fetch_q = [&](int t0, int last, const ChunkSystem &w) {
+        auto fetch_q = [&](int t0, int last) {
             const char *q0 = qb + (size_t)t0 * skb;
             uint32_t off = qoff;
             if (last < kChunk - 1) off = min(my_row, last) * skb + 16 * g;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) q[ks] = load16(reinterpret_cast<const __bf16 *>(q0 + off + 64 * ks));
-            start = *reinterpret_cast<const f32x4 *>(&w.start[my_token]);
         };
         p[1] = (bf16x8)(__bf16)0.f;
         auto fetch_p = [&](const ChunkSystem &w) {
@@ -297,49 +286,56 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 *reinterpret_cast<bf16x8 *>(&s_k[buf][(tid / CH + 256 / CH * j) * KP + 8 * (tid % CH)]) = kr[j];
+            if (tid < 128) *reinterpret_cast<bf16x8 *>(&s_v[buf][8 * tid]) = vr;
+            else if (tid < 160) *reinterpret_cast<bf16x8 *>(&s_w[buf][4 * (tid - 128)]) = vr;
         };
         {
             const int last = min(kChunk, n) - 1;
             const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws);
-            fetch_k(0, last);
-            fetch_q(0, last, w);
+            fetch_k(0, last, w);
+            fetch_q(0, last);
             fetch_p(w);
         }
         stage(0);
+        auto chunk_at = [&](int chunk, int &t0, int &last) -> const ChunkSystem & {
+            const int c = min(chunk, chunks - 1);
+            t0 = c * kChunk;
+            last = min(kChunk, n - t0) - 1;
+            return *reinterpret_cast<const ChunkSystem *>(ws + c * ws_step);
+        };
+        int t1, last;
+        {
+            const ChunkSystem &w = chunk_at(1, t1, last);
+            fetch_k(t1, last, w);
+        }
         lds_barrier();
         for (int chunk = 0; chunk < chunks; ++chunk) {
-            const int next = min(chunk + 1, chunks - 1), t1 = next * kChunk, last = min(kChunk, n - t1) - 1;
-            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws + next * ws_step);
-            fetch_k(t1, last);
-            // ---- O = diag(start) Q S
+            const ChunkSystem &w = chunk_at(chunk + 1, t1, last);
+            // ---- O^T = S^T Q^T diag(start): a lane has four columns of one token's row (the
+            // state's pieces serve as left operands just as they do as right ones)
             f32x4 o = (f32x4)0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                o = mfma16_bf16(q[ks], load16(&s_s[1][ks][lane][0]), o);
-                o = mfma16_bf16(q[ks], load16(&s_s[0][ks][lane][0]), o);
+                o = mfma16_bf16(load16(&s_s[1][ks][lane][0]), q[ks], o);
+                o = mfma16_bf16(load16(&s_s[0][ks][lane][0]), q[ks], o);
             }
-            o *= start;
-            fetch_q(t1, last, w);
+            o *= s_w[chunk & 1][my_row];
+            fetch_q(t1, last);
             lds_barrier();
             lds_barrier();
-            // ---- O += P U
+            // ---- O^T += U^T P^T
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb) {
-                o = mfma16_bf16(p[sb], load16(&s_u[1][sb][lane][0]), o);
-                o = mfma16_bf16(p[sb], load16(&s_u[0][sb][lane][0]), o);
+                o = mfma16_bf16(load16(&s_u[1][sb][lane][0]), p[sb], o);
+                o = mfma16_bf16(load16(&s_u[0][sb][lane][0]), p[sb], o);
             }
-            stage((chunk + 1) & 1);
             fetch_p(w);
-            char *o0 = ob + (size_t)(chunk * kChunk) * svb;
-            if (chunk * kChunk + kChunk <= n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) *reinterpret_cast<__bf16 *>(o0 + ooff + e * svb) = (__bf16)o[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (chunk * kChunk + my_token + e < n)
-                        *reinterpret_cast<__bf16 *>(o0 + ooff + e * svb) = (__bf16)o[e];
-            }
+            stage((chunk + 1) & 1);
+            const ChunkSystem &w2 = chunk_at(chunk + 2, t1, last);
+            fetch_k(t1, last, w2);
+            if (chunk * kChunk + my_row < n)
+                *reinterpret_cast<bf16x4 *>(ob + (size_t)(chunk * kChunk) * svb + ooff) =
+                    __builtin_convertvector(o, bf16x4);
             lds_barrier();
         }
     }
@@ -382,7 +378,9 @@ hipError_t launch_delta_prefill(float *H0, const void *q, const void *k, const v
                                 const float *gate, const float *beta, const int32_t *seq_offsets,
                                 void *out, void *workspace, const bole_delta_dims_t &d,
                                 int32_t *seq_status, hipStream_t stream) {
-    const bool aligned = (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) % 16 == 0;
+    const bool aligned = (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+                          reinterpret_cast<uintptr_t>(v)) % 16 == 0 &&
+                         reinterpret_cast<uintptr_t>(out) % 8 == 0;
     if (!chunked(d) || !aligned)
         return launch_delta_prefill_walk(H0, q, k, v, gate, beta, seq_offsets, out, d, seq_status,
                                          stream);

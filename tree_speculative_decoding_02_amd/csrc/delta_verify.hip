@@ -144,12 +144,15 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
                 hr[ks][e] = __builtin_nontemporal_load(
                     reinterpret_cast<const hvec *>(Hu + (size_t)(32 * ks + 8 * g + e) * s.DV));
     }
+    SystemRows<DK> rows;
+    if (n > 0) rows.load(kb, qb, sk, n);
     if (tid < 64) {
         const bool in = tid < n;
         const float lg = in ? log2_decay(gate[(size_t)(lo + tid) * s.H + h]) : 0.f;
         const WaveTopoD w = wave_topology_cumlog_f64(in ? parent[lo + tid] : -1, lg, n);
         t.mask[tid] = w.mask;
-        t.L[tid] = w.L;
+        t.L[tid] = (float)w.L;
+        t.Lrest[tid] = (float)(w.L - (double)(float)w.L);
         t.start[tid] = __builtin_amdgcn_exp2f((float)w.L);
         t.beta[tid] = in ? beta[(size_t)(lo + tid) * s.H + h] : 0.f;
         if (tid == 0) t.bad = w.bad;
@@ -163,7 +166,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         return;
     }
     if (n == 0) return;
-    delta_system<DK>(t, kb, qb, sk, n);
+    delta_system<DK, true>(t, rows, kb, sk, n);
     // row tile m has tokens of the tree
     auto used = [&](int m) { return tile_token(m, 0) < n; };
     if (!live) return;
