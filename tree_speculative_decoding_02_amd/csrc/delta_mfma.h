@@ -36,6 +36,17 @@ __device__ __forceinline__ int square_at(int i, int j) {
     return i * kChunk + ((((j >> 2) ^ i) & 15) << 2 | (j & 3));
 }
 
+// The same for row 16 ai + 4 x + r, column 16 aj + c, spelt out so that what depends on the lane
+// is worked out once: x and c from the lane, ai, aj and r not.
+__device__ __forceinline__ int block_at(int ai, int aj, int x, int r, int c) {
+    return 1024 * ai + 64 * r + (256 * x + ((aj ^ x) << 4)) + ((((c >> 2) ^ r) << 2) | (c & 3));
+}
+
+// Row 16 ai + c, columns 16 aj + 4 x .. + 3.
+__device__ __forceinline__ int block_row_at(int ai, int aj, int x, int c) {
+    return 1024 * ai + 64 * c + ((aj ^ (c >> 2)) << 4) + ((x ^ (c & 3)) << 2);
+}
+
 // Token that lane index r (0..15) of row tile m stands for. Tiles 2s and 2s + 1 cover tokens
 // 32 s .. 32 s + 31 so that a product's results in registers (rows 4g .. 4g + 3 of lane group
 // g, both tiles) are tokens 32 s + 8 g .. + 7: the B operand of the next product.
@@ -101,18 +112,17 @@ struct SystemRows {
 __device__ __forceinline__ f32x4 block_product(const float *a, int ai, int aj, const float *b, int bi,
                                                int bj, f32x4 c) {
     const int col = lane_id() & 15, g = lane_id() >> 4;
-    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[square_at(16 * ai + col, 16 * aj + 4 * g)]);
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[block_row_at(ai, aj, g, col)]);
 #pragma unroll
     for (int r = 0; r < 4; ++r)  // k index 4 g + r on both sides
-        c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], b[square_at(16 * bi + 4 * g + r, 16 * bj + col)], c, 0,
-                                                 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], b[block_at(bi, bj, g, r, col)], c, 0, 0, 0);
     return c;
 }
 
 // c - A B with B in registers as products leave it (row 4 g + r, column col).
 __device__ __forceinline__ f32x4 block_product_reg(const float *a, int ai, int aj, const f32x4 &b, f32x4 c) {
     const int col = lane_id() & 15, g = lane_id() >> 4;
-    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[square_at(16 * ai + col, 16 * aj + 4 * g)]);
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(&a[block_row_at(ai, aj, g, col)]);
 #pragma unroll
     for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], -b[r], c, 0, 0, 0);
     return c;
@@ -121,7 +131,7 @@ __device__ __forceinline__ f32x4 block_product_reg(const float *a, int ai, int a
 __device__ __forceinline__ void put_block(float *a, int ai, int aj, const f32x4 &v) {
     const int col = lane_id() & 15, g = lane_id() >> 4;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) a[square_at(16 * ai + 4 * g + r, 16 * aj + col)] = v[r];
+    for (int r = 0; r < 4; ++r) a[block_at(ai, aj, g, r, col)] = v[r];
 }
 
 // Fills t (X, P) for the n tokens at rows 0 .. n - 1 of k; t.L, t.beta and (TREE) t.mask are set
@@ -132,7 +142,8 @@ __device__ __forceinline__ void put_block(float *a, int ai, int aj, const f32x4 
 template <int DK, bool TREE>
 __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<DK> &rows,
                                              const __bf16 *__restrict__ k, size_t stride, int n) {
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+    const int lane = lane_id(), col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     constexpr int KS = DK / 32;
     const f32x4 zero = (f32x4)0.f;
     // ---- pair products: row tile `wave`, column tiles up to it
@@ -181,19 +192,19 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<DK
     lds_barrier();
     // ---- X: the diagonal blocks, block g and column `col` of it a lane of one wavefront
     if (wave == 0) {
-        const int base = 16 * g;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             f32x4 row[4];
 #pragma unroll
             for (int c = 0; c < (i + 3) / 4; ++c)
-                row[c] = *reinterpret_cast<const f32x4 *>(&t.A[square_at(base + i, base + 4 * c)]);
+                row[c] = *reinterpret_cast<const f32x4 *>(
+                    &t.A[1024 * g + 64 * i + ((g ^ (i >> 2)) << 4) + ((c ^ (i & 3)) << 2)]);
             float acc[4] = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < i; ++j) acc[j & 3] = fmaf(-row[j >> 2][j & 3], x[j], acc[j & 3]);
             x[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            t.X[square_at(base + i, base + col)] = x[i];
+            t.X[1024 * g + 64 * i + ((g ^ (i >> 2)) << 4) + ((((col >> 2) ^ (i & 3)) << 2) | (col & 3))] = x[i];
         }
     }
     lds_barrier();

@@ -86,6 +86,15 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
     }
 }
 
+// K in LDS: element (row, 8 c + x) of part c. A row's 16-byte parts are permuted by its number, so
+// that an operand's rows (tile_token's order) and the four rows of a transposing read lie in
+// distinct banks.
+template <int DK>
+__device__ __forceinline__ int k_at(int row, int c) {
+    return row * DK + 8 * (c ^ (DK == 128 ? ((row & 3) << 2 | ((row >> 2) & 3))
+                                          : (((row >> 1) & 1) << 2 | ((row >> 3) & 3))));
+}
+
 // One workgroup: eight wavefronts, 16 state columns. What bounds it is the chain of a chunk's
 // steps (K S, then U, then the state), so four wavefronts do only these: wavefront w has the
 // tokens of row tile w and the state rows of d_k / 64 row tiles, and what it computes becomes
@@ -99,8 +108,8 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
 // columns of their own and exchange nothing.
 template <int DK>
 __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a, int units, int groups) {
-    constexpr int KS = DK / 32, TILES = DK / 64, CH = DK / 8, PER = kChunk * CH / 256, KP = DK + 8;
-    __shared__ __align__(16) __bf16 s_k[2][kChunk * KP];
+    constexpr int KS = DK / 32, TILES = DK / 64, CH = DK / 8, PER = kChunk * CH / 256;
+    __shared__ __align__(16) __bf16 s_k[2][kChunk * DK];
     __shared__ __align__(16) __bf16 s_s[3][KS][64][8];   // state, three terms
     __shared__ __align__(16) __bf16 s_r[3][2][64][8];    // R
     __shared__ __align__(16) __bf16 s_e[3][2][64][8];    // end U, for the state
@@ -181,10 +190,9 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             f32x4 r[3];
 #pragma unroll
             for (int i = 0; i < 3; ++i) r[i] = (f32x4)0.f;
-            const __bf16 *krow = &s_k[buf][my_row * KP + 8 * g];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const bf16x8 ka = load16(krow + 32 * ks);
+                const bf16x8 ka = load16(&s_k[buf][k_at<DK>(my_row, 4 * ks + g)]);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) r[i] = mfma16_bf16(ka, load16(&s_s[i][ks][lane][0]), r[i]);
             }
@@ -232,9 +240,9 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
                 for (int sb = 0; sb < 2; ++sb) {
                     // state rows of lanes 4c .. 4c + 3: 32 (m / 2) + 8 c + 4 (m % 2) ..
-                    const __bf16 *kt = &s_k[buf][(32 * sb + 8 * g + (col >> 2)) * KP + 32 * (m >> 1) +
-                                                 8 * (col & 3) + 4 * (m & 1)];
-                    const bf16x8 ka = join(read_transposed(kt), read_transposed(kt + 4 * KP));
+                    const int row = 32 * sb + 8 * g + (col >> 2), c = 4 * (m >> 1) + (col & 3);
+                    const bf16x8 ka = join(read_transposed(&s_k[buf][k_at<DK>(row, c) + 4 * (m & 1)]),
+                                           read_transposed(&s_k[buf][k_at<DK>(row + 4, c) + 4 * (m & 1)]));
 #pragma unroll
                     for (int i = 2; i >= 0; --i) y[sb] = mfma16_bf16(ka, eb[sb][i], y[sb]);
                 }
@@ -285,7 +293,7 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
         auto stage = [&](int buf) {
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                *reinterpret_cast<bf16x8 *>(&s_k[buf][(tid / CH + 256 / CH * j) * KP + 8 * (tid % CH)]) = kr[j];
+                *reinterpret_cast<bf16x8 *>(&s_k[buf][k_at<DK>(tid / CH + 256 / CH * j, tid % CH)]) = kr[j];
             if (tid < 128) *reinterpret_cast<bf16x8 *>(&s_v[buf][8 * tid]) = vr;
             else if (tid < 160) *reinterpret_cast<bf16x8 *>(&s_w[buf][4 * (tid - 128)]) = vr;
         };
