@@ -246,20 +246,24 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     for (int dt = 0; dt < D / 32; ++dt) acc[dt] = (f32x16)0.f;
     float m = -INFINITY, l = 0.f;
     const float c2 = s.scale * kLog2e;
+    const bool busy = t.tile * kRowTile + wave * 32 < t.n * G;  // else it only stages
     if (first < last) {
         page = key_page(s, table, t, first * kKeys + lane);
         fetch(first);
         page = key_page(s, table, t, (first + 1) * kKeys + lane);
         stage(0);
         lds_barrier();
-    }
-    for (int tile = first; tile < last; ++tile) {
+    // (a do loop, entered only from here: a loop that could also be reached around these loads
+    // would have to wait for every load in flight in each of its turns)
+    int tile = first;
+    do {
         const int buf = (tile - first) & 1;
         if (tile + 1 < last) {
             fetch(tile + 1);
             page = key_page(s, table, t, (tile + 2) * kKeys + lane);
         }
         const int x0 = tile * kKeys;
+        if (busy) {
         f32x16 z[2];
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
@@ -318,8 +322,10 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                     acc[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, acc[dt], 0, 0, 0);
                 }
             }
+        }
         if (tile + 1 < last) stage(buf ^ 1);
         lds_barrier();
+    } while (++tile < last);
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
@@ -433,8 +439,8 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
         page = key_page(s, table, t, first * kKeys + lane);
         fetch(first);
         page = key_page(s, table, t, (first + 4) * kKeys + lane);
-    }
-    for (int tile = first; tile < last; tile += 4) {
+    int tile = first;
+    do {
         const int x0 = tile * kKeys;
         f32x4 z[4];
 #pragma unroll
@@ -496,6 +502,7 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
                                       p, acc[dt]);
         }
         asm volatile("" ::: "memory");
+    } while ((tile += 4) < last);
     }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
