@@ -151,16 +151,25 @@ __device__ __forceinline__ bool tile_open(const RowTile &t, bool tree, int x0) {
     return false;
 }
 
-// Whether the query (row i of its sequence, window from qe, own nodes qmask for trees) sees
-// key x.
-__device__ __forceinline__ bool sees(const WindowShape &s, const RowTile &t, bool tree, int i, int qe,
-                                     uint64_t qmask, int x) {
-    if (x >= t.total) return false;
-    if (x < t.n1) return true;
-    if (x < t.n1 + t.n2) return t.w0 + (x - t.n1) >= qe;
-    const int j = own_row(t, x);
-    if (tree) return (qmask >> j) & 1ull;
-    return j <= i && (t.len + j >= qe || t.len + j < s.sinks);
+__device__ __forceinline__ uint64_t bits_below(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// The keys x0 .. x0 + 63 that a query sees, as bits: row i of its sequence, window from position
+// qe on, own nodes qmask for trees. Each part of the list shows it an interval (or the path).
+__device__ __forceinline__ uint64_t seen_keys(const RowTile &t, bool tree, int i, int qe, uint64_t qmask,
+                                              int x0) {
+    const int c = t.n1 + t.n2 - x0, from = max(qe, 0);
+    uint64_t m = bits_below(c) & ~bits_below(t.n1 - x0 + max(0, from - t.w0));
+    m |= bits_below(t.n1 - x0);
+    if (tree) {
+        if (c > -64 && c < 64) m |= (c >= 0 ? qmask << c : qmask >> -c) & bits_below(c + t.n4);
+    } else {
+        const int own = c + t.n3;
+        m |= bits_below(c + min(t.n3, i + 1)) & ~bits_below(c);
+        m |= bits_below(own + min(t.n4, i + 1 - t.o2)) & ~bits_below(own + max(0, from - t.len - t.o2));
+    }
+    return m;
 }
 
 // LDS row strides in elements: K rows 16 bytes past a multiple of 256 apart or an odd number
@@ -274,20 +283,22 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                 z[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load16(kp + 16 * ks), qf[ks], z[sub],
                                                                  0, 0, 0);
         }
-        const bool open = tile_open(t, tree, x0);
         float top = -INFINITY;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) z[sub] *= c2;
+        if (!tile_open(t, tree, x0)) {
+            const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * hh);
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    z[sub][r] = ((uint32_t)(seen >> (32 * sub)) >> (8 * (r >> 2) + (r & 3))) & 1u
+                                    ? z[sub][r] : -INFINITY;
+        }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float y = z[sub][r] * c2;
-                if (!open) {
-                    const int x = x0 + sub * 32 + 8 * (r >> 2) + 4 * hh + (r & 3);
-                    y = sees(s, t, tree, i, qe, qmask, x) ? y : -INFINITY;
-                }
-                z[sub][r] = y;
-                top = fmaxf(top, y);
-            }
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, z[sub][r]);
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m, top);
         // nothing seen so far: keep every exponential at 0
@@ -458,18 +469,22 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
             fetch(tile + 4);
             page = key_page(s, table, t, (tile + 8) * kKeys + lane);
         }
-        const bool open = tile_open(t, tree, x0);
         float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[r] *= c2;
+        if (!tile_open(t, tree, x0)) {
+            const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[r][e] = ((uint32_t)(seen >> (32 * (r >> 1))) >> (16 * (r & 1) + e)) & 1u ? z[r][e]
+                                                                                            : -INFINITY;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float y = z[r][e] * c2;
-                if (!open)
-                    y = sees(s, t, tree, i, qe, qmask, x0 + 16 * r + 4 * g + e) ? y : -INFINITY;
-                z[r][e] = y;
-                top = fmaxf(top, y);
-            }
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, z[r][e]);
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
