@@ -105,28 +105,36 @@ __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off,
     return !__any(bad);
 }
 
-// Tile `slot` of the packed rows (MT packed rows a tile): sequence b owns slots from
-// floor(off[b] G / MT) + b, at least one each (slots before the first sequence's are nobody's).
-// `ordered`: whether the offsets are.
-__device__ __forceinline__ bool locate(const int32_t *__restrict__ off, int B, int T, int G, int MT,
-                                       int slot, int &b, int &slot0, bool &ordered) {
+// Tile `slot` of the packed rows (MT packed rows a tile, G packed rows a row): sequence b owns
+// slots from floor(off[b] G / MT) + b, at least one each (slots before the first sequence's are
+// nobody's). `per` (may be NULL): a value of each sequence, loaded along with the offsets.
+struct Located {
+    bool found, ordered;       // found: b owns the slot; ordered: the offsets are
+    int b, lo, n, slot0, per;  // sequence, its rows, its first slot, its value
+};
+
+__device__ __forceinline__ Located locate(const int32_t *__restrict__ off, const int32_t *__restrict__ per,
+                                          int B, int T, int G, int MT, int slot) {
     bool bad = false;
-    int before = 0;
+    Located l = {false, true, -1, 0, 0, 0, 0};
     for (int c = 0; c < B; c += 64) {
-        const int x = c + lane_id();
-        bool at = false;
-        if (x < B) {
-            const int lo = off[x], hi = off[x + 1];
-            bad |= lo < 0 || hi < lo || hi > T;
-            at = (int64_t)lo * G / MT + x <= slot;
+        const int x = min(c + lane_id(), B - 1);
+        const int lo = off[x], hi = off[x + 1], v = per ? per[x] : 0;
+        bad |= lo < 0 || hi < lo || hi > T;
+        // the sequences that start at or before the slot are the first ones
+        const int many = (int)__popcll(__ballot(c + lane_id() < B && (int64_t)lo * G / MT + x <= slot));
+        if (many > 0) {
+            const int at = __builtin_amdgcn_readfirstlane(many - 1);
+            l.b = c + at;
+            l.lo = __builtin_amdgcn_readlane(lo, at);
+            l.n = __builtin_amdgcn_readlane(hi, at) - l.lo;
+            l.per = __builtin_amdgcn_readlane(v, at);
         }
-        before += (int)__popcll(__ballot(at));
     }
-    b = __builtin_amdgcn_readfirstlane(before - 1);
-    ordered = !__any(bad);
-    if (!ordered || b < 0) return false;
-    slot0 = __builtin_amdgcn_readfirstlane((int)((int64_t)off[b] * G / MT) + b);
-    return true;
+    l.ordered = !__any(bad);
+    l.found = l.ordered && l.b >= 0;
+    l.slot0 = (int)((int64_t)l.lo * G / MT) + l.b;
+    return l;
 }
 
 // The accepted path of tree b, validated by one wavefront with the rules of commit_kernel:

@@ -46,10 +46,9 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
     const DeltaShape &s = a.s;
     const int h = blockIdx.x % s.H, slot = blockIdx.x / s.H, hk = h / (s.H / s.HK);
     const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    int b, slot0;
-    bool ordered;
-    if (!locate(a.offsets, s.B, s.T, 1, kChunk, slot, b, slot0, ordered)) return;
-    const int lo = a.offsets[b] + (slot - slot0) * kChunk, n = min(kChunk, a.offsets[b + 1] - lo);
+    const Located l = locate(a.offsets, nullptr, s.B, s.T, 1, kChunk, slot);
+    if (!l.found) return;
+    const int done = (slot - l.slot0) * kChunk, lo = l.lo + done, n = min(kChunk, l.n - done);
     if (n <= 0) return;
     ChunkSystem &w = a.ws[(size_t)slot * s.H + h];
     const size_t sk = (size_t)s.HK * DK, row0 = (size_t)lo * sk + (size_t)hk * DK;

@@ -32,7 +32,8 @@ __global__ __launch_bounds__(64) void window_generic_kernel(const WindowArgs a) 
         mask = shfl_u64(t.mask, i);
         depth = t.depth;
     }
-    if (st == BOLE_TREE_OK) st = cache_status(a, b, len);
+    if (st == BOLE_TREE_OK) st = length_status(s, len);
+    if (st == BOLE_TREE_OK) st = pages_status(a, b, len);
     if (i == 0 && h == 0 && lane == 0 && a.status) a.status[b] = st;
     T *o = static_cast<T *>(a.out) + ((size_t)row * s.H + h) * s.D;
     if (st != BOLE_TREE_OK) {

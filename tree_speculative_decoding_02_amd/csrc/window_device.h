@@ -37,17 +37,20 @@ __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int 
     return lo;
 }
 
-// Whether the sequence's cache holds what its rows see: its length, and the pages of the
-// first min(sinks, len) positions and of those behind the first row's window. One wavefront.
-__device__ __forceinline__ int cache_status(const WindowArgs &a, int b, int len) {
+// Whether the sequence's cache can hold len tokens.
+__device__ __forceinline__ int length_status(const WindowShape &s, int len) {
+    return len < 0 || len > ((int64_t)s.max_pages << s.page_shift) ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
+}
+
+// Whether the pages that the sequence's rows see exist: those of the first min(sinks, len)
+// positions and of the ones behind the first row's window. One wavefront; a valid length.
+__device__ __forceinline__ int pages_status(const WindowArgs &a, int b, int len) {
     const WindowShape &s = a.s;
-    if (len < 0 || len > ((int64_t)s.max_pages << s.page_shift)) return BOLE_TREE_BAD_CACHE;
     const int32_t *table = a.page_table + (size_t)b * s.max_pages;
-    const int sink_end = (min(s.sinks, len) + (1 << s.page_shift) - 1) >> s.page_shift;
-    const int first = max(0, len - s.window + 1) >> s.page_shift;
-    const int end = len == max(0, len - s.window + 1)
-                        ? first
-                        : (int)(((int64_t)len + (1 << s.page_shift) - 1) >> s.page_shift);
+    const int from = max(0, len - s.window + 1), round = (1 << s.page_shift) - 1;
+    const int sink_end = (int)(((int64_t)min(s.sinks, len) + round) >> s.page_shift);
+    const int first = from >> s.page_shift;
+    const int end = len == from ? first : (int)(((int64_t)len + round) >> s.page_shift);
     bool bad = false;
     for (int i = lane_id(); i < sink_end; i += 64) bad |= (unsigned)table[i] >= (unsigned)s.pages;
     for (int i = first + lane_id(); i < end; i += 64) bad |= (unsigned)table[i] >= (unsigned)s.pages;

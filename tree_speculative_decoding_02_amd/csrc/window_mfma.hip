@@ -64,28 +64,25 @@ __device__ __forceinline__ void key_list(const WindowShape &s, bool tree, RowTil
     t.total = t.n1 + t.n2 + t.n3 + t.n4;
 }
 
-// Finds and validates the workgroup's tile; writes the sequence's status. Every wavefront
-// computes the same. mask: of a tree, lane i's node's visible own nodes (its path, cut to the
-// window); depth: its depth. False: nothing to do (st says why).
+// Finds the workgroup's tile and all that is wrong with its sequence but its pages. Every
+// wavefront computes the same. mask: of a tree, lane i's node's visible own nodes (its path, cut
+// to the window); depth: its depth. False: no rows here.
 template <int MT>
 __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, bool report,
                                           RowTile &t, uint64_t &mask, int &depth) {
     const WindowShape &s = a.s;
     const int lane = lane_id();
     t.status = BOLE_TREE_OK;
-    bool ordered;
-    if (!locate(a.offsets, s.B, s.T, G, MT, slot, t.b, t.slot0, ordered)) {
-        if (!ordered && report && slot == 0 && a.status)
+    const Located l = locate(a.offsets, a.cache_len, s.B, s.T, G, MT, slot);
+    if (!l.found) {
+        if (!l.ordered && report && slot == 0 && a.status)
             for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
         return false;
     }
-    t.lo = a.offsets[t.b];
-    t.n = a.offsets[t.b + 1] - t.lo;
+    t.b = l.b, t.lo = l.lo, t.n = l.n, t.slot0 = l.slot0, t.len = l.per;
     t.tile = slot - t.slot0;
-    const int rows = t.n * G;
     if (t.n == 0 && t.tile == 0 && report && lane == 0 && a.status) a.status[t.b] = BOLE_TREE_OK;
-    if (t.tile * MT >= rows) return false;
-    t.len = a.cache_len[t.b];
+    if (t.tile * MT >= t.n * G) return false;
     t.i0 = t.tile * MT / G;
     t.i1 = min(t.n, (t.tile * MT + MT + G - 1) / G);
     if (a.parent) {
@@ -98,8 +95,7 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
             depth = w.depth;
         }
     }
-    if (t.status == BOLE_TREE_OK) t.status = cache_status(a, t.b, t.len);
-    if (report && t.tile == 0 && lane == 0 && a.status) a.status[t.b] = t.status;
+    if (t.status == BOLE_TREE_OK) t.status = length_status(s, t.len);
     if (t.status != BOLE_TREE_OK) return true;
     if (a.parent && s.window < kMaxTree) {
         // path nodes that the window has left behind, unless they are first tokens
@@ -109,6 +105,7 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
         }
     }
     key_list(s, a.parent != nullptr, t);
+    if (t.n1 + t.n2 > 0 && s.pages == 0) t.status = BOLE_TREE_BAD_CACHE;
     return true;
 }
 
@@ -121,20 +118,22 @@ __device__ __forceinline__ int own_row(const RowTile &t, int x) {
     return j < t.n3 ? j : t.o2 + (j - t.n3);
 }
 
-// Page of key x, -1 for the call's own rows and past the end.
+// Page of key x as the table has it; 0 for the call's own rows.
 __device__ __forceinline__ int key_page(const WindowShape &s, const int32_t *__restrict__ table,
                                         const RowTile &t, int x) {
     x = min(x, t.total - 1);
-    return x < t.n1 + t.n2 ? table[cached_position(t, x) >> s.page_shift] : -1;
+    return x < t.n1 + t.n2 ? table[cached_position(t, x) >> s.page_shift] : 0;
 }
 
+// A page that is not in the cache stands for its last one: the first loads go out before the
+// sequence's pages are known to be valid, and are dropped if they are not.
 // Row (of D elements) of key x: in the cache's [page][head][slot] order, or in the call's k and
 // v. At 128 bytes a row and more, 32 bits number more rows than memory holds.
 __device__ __forceinline__ uint32_t key_row(const WindowShape &s, const RowTile &t, int hk, int x,
                                             int page) {
     if (x < t.n1 + t.n2) {
         const uint32_t slot = cached_position(t, x) & ((1 << s.page_shift) - 1);
-        return (((uint32_t)page * s.HK + hk) << s.page_shift) + slot;
+        return ((min((uint32_t)page, (uint32_t)s.pages - 1) * s.HK + hk) << s.page_shift) + slot;
     }
     return (uint32_t)(t.lo + own_row(t, x)) * s.HK + hk;
 }
@@ -205,13 +204,18 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     const size_t row_off = ((size_t)(t.lo + i) * s.H + hk * G + gq) * D;
     __bf16 *out = static_cast<__bf16 *>(a.out) + row_off;
     const size_t part_row = ((size_t)part * slots * s.HK + blockIdx.x) * kRowTile + wave * 32 + col;
-    if (t.status != BOLE_TREE_OK) {
+    auto give_up = [&]() {
         const bool fill = t.status != BOLE_TREE_BAD_SIZE;
         if (parts.n > 1) {
             if (live && hh == 0) parts.ml[part_row * 2] = fill ? __builtin_nanf("") : INFINITY;
         } else if (live && fill) {
             for (int e = hh; e < D; e += 2) out[e] = (__bf16)__builtin_nanf("");
         }
+    };
+    const bool report = hk == 0 && part == 0 && t.tile == 0 && tid == 0 && a.status;
+    if (t.status != BOLE_TREE_OK) {
+        if (report) a.status[t.b] = t.status;
+        give_up();
         return;
     }
     const uint64_t qmask = tree ? shfl_u64(node_mask, i) : 0;
@@ -260,6 +264,14 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         page = key_page(s, table, t, first * kKeys + lane);
         fetch(first);
         page = key_page(s, table, t, (first + 1) * kKeys + lane);
+    }
+    t.status = pages_status(a, t.b, t.len);
+    if (report) a.status[t.b] = t.status;
+    if (t.status != BOLE_TREE_OK) {
+        give_up();
+        return;
+    }
+    if (first < last) {
         stage(0);
         lds_barrier();
     // (a do loop, entered only from here: a loop that could also be reached around these loads
@@ -367,7 +379,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
 }
 
 template <int D>
-__global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs a, const WindowParts parts,
+__global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs a, const WindowParts parts,
                                                                int slots) {
     constexpr int CH = D / 8, VP = Pad<D>::V, VPER = kKeys * CH / 64;
     constexpr int JOIN = 4 * 16 * (D + 4) * 4;  // the last merge: sums, then (m, l), over the values
@@ -393,7 +405,7 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
     const bool live = R < rows;
     const int i = live ? R / G : 0;
     const size_t part_tile = ((size_t)part * slots * s.HK + blockIdx.x) * kTokenTile;
-    if (t.status != BOLE_TREE_OK) {
+    auto give_up = [&]() {
         const bool fill = t.status != BOLE_TREE_BAD_SIZE;
         if (parts.n > 1) {
             if (live && g == 0 && wave == 0)
@@ -402,6 +414,11 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
             __bf16 *o = static_cast<__bf16 *>(a.out) + row_offset(R);
             for (int e = wave * 4 + g; e < D; e += 16) o[e] = (__bf16)__builtin_nanf("");
         }
+    };
+    const bool report = hk == 0 && part == 0 && t.tile == 0 && tid == 0 && a.status;
+    if (t.status != BOLE_TREE_OK) {
+        if (report) a.status[t.b] = t.status;
+        give_up();
         return;
     }
     const uint64_t qmask = tree ? shfl_u64(node_mask, i) : 0;
@@ -450,6 +467,14 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
         page = key_page(s, table, t, first * kKeys + lane);
         fetch(first);
         page = key_page(s, table, t, (first + 4) * kKeys + lane);
+    }
+    t.status = pages_status(a, t.b, t.len);
+    if (report) a.status[t.b] = t.status;
+    if (t.status != BOLE_TREE_OK) {
+        give_up();
+        return;
+    }
+    if (first < last) {
     int tile = first;
     do {
         const int x0 = tile * kKeys;
@@ -564,43 +589,53 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
     for (int e = 0; e < D / 16; ++e) dst[e] = (__bf16)(o[e] * inv);
 }
 
-// Joins the parts of a split call: a workgroup a row tile, sums in the parts' order.
+// Joins the parts of a split call (at most 64): a workgroup a row, wavefront w takes parts w,
+// w + 4, .., a lane two or fewer dimensions; sums in a fixed order.
 template <int D, int MT>
 __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, const WindowParts parts,
                                                           int slots) {
+    __shared__ float s_o[4][D];
     const WindowShape &s = a.s;
-    const int G = s.H / s.HK, hk = blockIdx.x % s.HK, slot = blockIdx.x / s.HK;
-    int b, slot0;
-    bool ordered;
-    if (!locate(a.offsets, s.B, s.T, G, MT, slot, b, slot0, ordered)) return;
-    const int lo = a.offsets[b], rows = (a.offsets[b + 1] - lo) * G, r0 = (slot - slot0) * MT;
-    const size_t stride = (size_t)slots * s.HK * MT, at = (size_t)blockIdx.x * MT;
-    constexpr int Q = D / 4;  // threads a row
-    for (int e = threadIdx.x; e < MT * Q; e += 256) {
-        const int r = e / Q, d = (e - r * Q) * 4, R = r0 + r;
-        if (R >= rows) break;
-        float m = -INFINITY;
-        for (int p = 0; p < parts.n; ++p) {
-            const float mp = parts.ml[(p * stride + at + r) * 2];
-            m = mp != mp ? mp : fmaxf(m, mp);  // every part of a bad sequence says the same
-        }
-        if (m == INFINITY) continue;           // a tree of bad size: not touched
-        f32x4 o = (f32x4)0.f;
-        float l = 0.f;
-        if (m == m) {
-            for (int p = 0; p < parts.n; ++p) {
-                const size_t row = p * stride + at + r;
-                const float f = __builtin_amdgcn_exp2f(parts.ml[row * 2] - m);
-                l += f * parts.ml[row * 2 + 1];
-                o += f * *reinterpret_cast<const f32x4 *>(parts.o + row * D + d);
-            }
-        }
-        const int i = R / G;
-        bf16x4 y;
-        for (int j = 0; j < 4; ++j) y[j] = (__bf16)(m == m ? o[j] / l : m);
-        *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) +
-                                    ((size_t)(lo + i) * s.H + hk * G + (R - i * G)) * D + d) = y;
+    const int G = s.H / s.HK, hk = blockIdx.x % s.HK, slot = blockIdx.x / s.HK, r = blockIdx.y;
+    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    const size_t stride = (size_t)slots * s.HK * MT, at = (size_t)blockIdx.x * MT + r;
+    // every part's maximum and sum, a part a lane (the rows of unused tiles are never read)
+    const Located t = locate(a.offsets, nullptr, s.B, s.T, G, MT, slot);
+    const int R = (slot - t.slot0) * MT + r;
+    if (!t.found || R >= t.n * G) return;
+    float m = -INFINITY, l = 0.f;
+    if (lane < parts.n) {
+        m = parts.ml[(lane * stride + at) * 2];
+        l = parts.ml[(lane * stride + at) * 2 + 1];
     }
+    // all parts of a bad sequence say the same: NaN rows, or (+inf) untouched ones
+    const float m0 = readlane_f(m, 0);
+    if (m0 == INFINITY) return;
+    float top = m;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const float f = __builtin_amdgcn_exp2f(m - top);  // top is finite: some part sees the row itself
+    float sum = f * l;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    constexpr int E = (D + 63) / 64;
+    float o[E] = {};
+#pragma unroll 4
+    for (int p = wave; p < parts.n; p += 4) {
+        const float fp = __shfl(f, p, 64);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (lane + 64 * e < D) o[e] += fp * parts.o[(p * stride + at) * D + lane + 64 * e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (lane + 64 * e < D) s_o[wave][lane + 64 * e] = o[e];
+    __syncthreads();
+    const int d = threadIdx.x, i = R / G;
+    if (d >= D) return;
+    const float y = ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / sum;
+    static_cast<__bf16 *>(a.out)[((size_t)(t.lo + i) * s.H + hk * G + (R - i * G)) * D + d] =
+        (__bf16)(m0 == m0 ? y : m0);
 }
 
 // ---- host
@@ -657,9 +692,9 @@ static hipError_t launch_width(const WindowArgs &a, const bole_window_dims_t &d,
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.parts > 1) {
         if (p.tokens)
-            window_join_kernel<D, kTokenTile><<<dim3(grid.x), block, 0, stream>>>(a, parts, p.slots);
+            window_join_kernel<D, kTokenTile><<<dim3(grid.x, kTokenTile), block, 0, stream>>>(a, parts, p.slots);
         else
-            window_join_kernel<D, kRowTile><<<dim3(grid.x), block, 0, stream>>>(a, parts, p.slots);
+            window_join_kernel<D, kRowTile><<<dim3(grid.x, kRowTile), block, 0, stream>>>(a, parts, p.slots);
         e = hipGetLastError();
     }
     return e;
