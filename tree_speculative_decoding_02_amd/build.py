@@ -18,7 +18,7 @@ SOURCES = ["bole_api.hip", "topology.hip", "validate.hip", "verify_generic.hip",
            "verify_naive.hip", "commit.hip", "tree_build.hip",
            "tree_accept.hip", "delta_api.hip", "delta_walk.hip", "delta_verify.hip",
            "delta_prefill.hip", "window_api.hip", "window_attention.hip",
-           "window_mfma.hip"]
+           "window_mfma.hip", "window_mfma_f32.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 instructions stay off: the compiler would otherwise form them from
