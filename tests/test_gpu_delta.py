@@ -85,7 +85,8 @@ def column_norms(w):
 SHAPES = [  # heads, key heads, d_k, d_v, factors
     (4, 2, 128, 128, BF16), (3, 3, 64, 64, BF16), (6, 2, 128, 96, BF16), (2, 1, 128, 64, F32),
     (2, 2, 72, 40, BF16), (3, 1, 17, 5, F32), (2, 1, 256, 256, BF16), (1, 1, 1, 1, F32),
-    (2, 1, 64, 16, BF16),
+    (2, 1, 64, 16, BF16), (2, 1, 40, 24, F32), (3, 1, 8, 8, BF16), (2, 2, 120, 200, BF16),
+    (2, 1, 128, 128, F32), (2, 2, 64, 130, F32),
 ]
 IDS = ["-".join(map(str, s[:4])) + ("-bf16" if s[4] == BF16 else "-f32") for s in SHAPES]
 

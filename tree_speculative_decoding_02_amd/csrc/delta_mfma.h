@@ -10,8 +10,11 @@
 // X is formed once and serves every state column: the four 16 x 16 diagonal blocks by forward
 // substitution, what lies below them by fp32 matrix products, first within the two 32 x 32
 // diagonal blocks, then between them:   X_ij = -X_ii A_ij X_jj   (blocks of either size).
-// Products of k and q are bf16 products with fp32 sums, exact but for those sums; decays and
-// everything after them are fp32.
+// Products of bf16 k and q are exact but for their fp32 sums; fp32 ones are taken as three bf16
+// terms each. Decays and everything after them are fp32.
+//
+// Kernels are built for d_k = 64 and 128; WHOLE says that the call's d_k is that. Otherwise it is
+// smaller, a multiple of 8, and the 8-element parts of a row from d_k on count as zero.
 #pragma once
 
 #include "delta_device.h"
@@ -82,28 +85,65 @@ __device__ __forceinline__ void split_terms8(const f32x4 &a, const f32x4 &b, bf1
                                        3, 4, 5, 6, 7);
 }
 
-// c += a b with a and b in N terms each, leaving out the products below the last term.
-template <int N>
-__device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[N], const bf16x8 (&b)[N], f32x4 c) {
+// c += a b with a in NA and b in NB >= NA terms, leaving out the products below b's last term.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
 #pragma unroll
-    for (int o = N - 1; o >= 0; --o)  // smallest products first
+    for (int o = NB - 1; o >= 0; --o)  // smallest products first
 #pragma unroll
-        for (int i = 0; i <= o; ++i) c = mfma16_bf16(a[i], b[o - i], c);
+        for (int i = 0; i <= (o < NA ? o : NA - 1); ++i) c = mfma16_bf16(a[i], b[o - i], c);
     return c;
+}
+
+// Terms of a factor (K) and of an fp32 quantity beside it (S) that leave the result's rounding,
+// to the factors' type, the one that counts.
+template <typename TF> struct Terms;
+template <> struct Terms<__bf16> { static constexpr int K = 1, S = 2; };
+template <> struct Terms<float> { static constexpr int K = 3, S = 3; };
+
+// Eight consecutive elements of a factor's row, as loaded and as terms.
+template <typename TF> struct RowPart;
+template <> struct RowPart<__bf16> {
+    bf16x8 x;
+    __device__ __forceinline__ void load(const __bf16 *p) { x = load16(p); }
+    __device__ __forceinline__ void clear() { x = (bf16x8)(__bf16)0.f; }
+    __device__ __forceinline__ void terms(bf16x8 (&y)[1]) const { y[0] = x; }
+};
+template <> struct RowPart<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const f32x4 *>(p);
+        b = *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    __device__ __forceinline__ void clear() { a = b = (f32x4)0.f; }
+    __device__ __forceinline__ void terms(bf16x8 (&y)[3]) const { split_terms8<3>(a, b, y); }
+};
+
+// Part c (of 8 elements) of the row at p; zero from d_k on.
+template <bool WHOLE, typename TF>
+__device__ __forceinline__ RowPart<TF> row_part(const TF *p, int c, int dk) {
+    RowPart<TF> x;
+    if (WHOLE) {
+        x.load(p + 8 * c);
+    } else {
+        x.load(p + (8 * c < dk ? 8 * c : 0));
+        if (8 * c >= dk) x.clear();
+    }
+    return x;
 }
 
 // A wavefront's own rows of k and q (row tile `wave`, tokens 16 wave ..) as operands; rows past
 // the last repeat it. Loaded early, they are in flight while the decays are summed up.
-template <int DK>
+template <typename TF, int DK, bool WHOLE>
 struct SystemRows {
-    bf16x8 k[DK / 32], q[DK / 32];
-    __device__ __forceinline__ void load(const __bf16 *kp, const __bf16 *qp, size_t stride, int n) {
-        const int row = 16 * (threadIdx.x >> 6) + (lane_id() & 15);
-        const size_t at = (size_t)min(row, n - 1) * stride + 8 * (lane_id() >> 4);
+    RowPart<TF> k[DK / 32], q[DK / 32];
+    __device__ __forceinline__ void load(const TF *kp, const TF *qp, size_t stride, int dk, int n) {
+        const int row = 16 * (threadIdx.x >> 6) + (lane_id() & 15), g = lane_id() >> 4;
+        const size_t at = (size_t)min(row, n - 1) * stride;
 #pragma unroll
         for (int ks = 0; ks < DK / 32; ++ks) {
-            k[ks] = load16(kp + at + 32 * ks);
-            q[ks] = load16(qp + at + 32 * ks);
+            k[ks] = row_part<WHOLE>(kp + at, 4 * ks + g, dk);
+            q[ks] = row_part<WHOLE>(qp + at, 4 * ks + g, dk);
         }
     }
 };
@@ -139,12 +179,12 @@ __device__ __forceinline__ void put_block(float *a, int ai, int aj, const f32x4 
 // barrier passed; n >= 1. Four wavefronts; ends with a barrier. What the pieces below read is
 // defined: X's columns from n on are those of the identity (times no strength), P's rows from n
 // on belong to no token. Every other element right of the 32 x 32 diagonal blocks is not.
-template <int DK, bool TREE>
-__device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<DK> &rows,
-                                             const __bf16 *__restrict__ k, size_t stride, int n) {
+template <typename TF, int DK, bool WHOLE, bool TREE>
+__device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<TF, DK, WHOLE> &rows,
+                                             const TF *__restrict__ k, size_t stride, int dk, int n) {
     const int lane = lane_id(), col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    constexpr int KS = DK / 32;
+    constexpr int KS = DK / 32, NK = Terms<TF>::K;
     const f32x4 zero = (f32x4)0.f;
     // ---- pair products: row tile `wave`, column tiles up to it
     {
@@ -164,12 +204,15 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<DK
         for (int jt = 0; jt < 4; ++jt) {
             if (jt > wave) break;
             f32x4 kk = zero, qk = zero;
-            const size_t at = (size_t)min(16 * jt + col, n - 1) * stride + 8 * g;
+            const TF *kj = k + (size_t)min(16 * jt + col, n - 1) * stride;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const bf16x8 b = load16(k + at + 32 * ks);
-                kk = mfma16_bf16(rows.k[ks], b, kk);
-                qk = mfma16_bf16(rows.q[ks], b, qk);
+                bf16x8 x[NK], b[NK];
+                row_part<WHOLE>(kj, 4 * ks + g, dk).terms(b);
+                rows.k[ks].terms(x);
+                kk = mfma_terms(x, b, kk);
+                rows.q[ks].terms(x);
+                qk = mfma_terms(x, b, qk);
             }
             const float lj = t.L[16 * jt + col], ljr = t.Lrest[16 * jt + col];
 #pragma unroll

@@ -40,7 +40,7 @@ struct PrefillArgs {
     DeltaShape s;
 };
 
-template <int DK>
+template <int DK, bool WHOLE>
 __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a) {
     __shared__ DeltaTokens t;
     const DeltaShape &s = a.s;
@@ -51,9 +51,10 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
     const int done = (slot - l.slot0) * kChunk, lo = l.lo + done, n = min(kChunk, l.n - done);
     if (n <= 0) return;
     ChunkSystem &w = a.ws[(size_t)slot * s.H + h];
-    const size_t sk = (size_t)s.HK * DK, row0 = (size_t)lo * sk + (size_t)hk * DK;
-    SystemRows<DK> rows;
-    rows.load(a.k + row0, a.q + row0, sk, n);
+    const int dk = WHOLE ? DK : s.DK;
+    const size_t sk = (size_t)s.HK * dk, row0 = (size_t)lo * sk + (size_t)hk * dk;
+    SystemRows<__bf16, DK, WHOLE> rows;
+    rows.load(a.k + row0, a.q + row0, sk, dk, n);
     if (tid < 64) {
         // tokens past the last do not decay and have no strength
         const bool in = tid < n;
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
         w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - L)) : 0.f;
     }
     lds_barrier();
-    delta_system<DK, false>(t, rows, a.k + row0, sk, n);
+    delta_system<__bf16, DK, WHOLE, false>(t, rows, a.k + row0, sk, dk, n);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
         if (sb > (wave >> 1)) continue;
@@ -105,7 +106,10 @@ __device__ __forceinline__ int k_at(int row, int c) {
 // Measured, one 32768-token prompt of 32 heads (256 workgroups of 512 chunks): 2.1 us a chunk
 // with the four wavefronts doing everything, 4.6 us with wavefronts that do all 64 tokens of 16
 // columns of their own and exchange nothing.
-template <int DK>
+//
+// WHOLE: d_k = DK and d_v is a multiple of 16. Otherwise both are multiples of 8; parts of rows
+// from d_k on count as zero, lanes past the last column load what they do not store.
+template <int DK, bool WHOLE>
 __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a, int units, int groups) {
     constexpr int KS = DK / 32, TILES = DK / 64, CH = DK / 8, PER = kChunk * CH / 256;
     __shared__ __align__(16) __bf16 s_k[2][kChunk * DK];
@@ -134,7 +138,8 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     if (n == 0) return;
     const int chunks = (n + kChunk - 1) / kChunk;
     // addresses are a chunk's (scalar) plus a lane's 32-bit offset in bytes
-    const uint32_t skb = (uint32_t)s.HK * DK * 2, svb = (uint32_t)s.H * s.DV * 2;
+    const int dk = WHOLE ? DK : s.DK;
+    const uint32_t skb = (uint32_t)s.HK * dk * 2, svb = (uint32_t)s.H * s.DV * 2;
     const size_t c0 = ((size_t)h * s.DV + 16 * cg) * 2;
     const char *ws = reinterpret_cast<const char *>(a.ws + ((size_t)(lo / kChunk + b)) * s.H + h);
     const size_t ws_step = (size_t)s.H * sizeof(ChunkSystem);
@@ -157,16 +162,19 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     if (chain) {
         // register e of state row tile j: row tile_token(m0 + j, 4 g + e), as tokens are laid out
         const int m0 = wave * TILES;
-        char *Hu = reinterpret_cast<char *>(a.H0 + (size_t)unit * DK * s.DV + 16 * cg);
+        char *Hu = reinterpret_cast<char *>(a.H0 + (size_t)unit * dk * s.DV + 16 * cg);
         const uint32_t hrow = (uint32_t)s.DV * 4;
         auto state_at = [&](int j, int e) -> float & {
             return *reinterpret_cast<float *>(Hu + (uint32_t)tile_token(m0 + j, 4 * g + e) * hrow + 4 * col);
+        };
+        auto state_has = [&](int j, int e) {
+            return WHOLE || (tile_token(m0 + j, 4 * g + e) < dk && 16 * cg + col < s.DV);
         };
         f32x4 st[TILES];
 #pragma unroll
         for (int j = 0; j < TILES; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st[j][e] = state_at(j, e);
+            for (int e = 0; e < 4; ++e) st[j][e] = state_has(j, e) ? state_at(j, e) : 0.f;
         bf16x8 x[2][3];
         // right of the diagonal X is zero: the first two wavefronts' second piece
 #pragma unroll
@@ -253,15 +261,20 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
         for (int j = 0; j < TILES; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) state_at(j, e) = st[j][e];
+            for (int e = 0; e < 4; ++e)
+                if (state_has(j, e)) state_at(j, e) = st[j][e];
     } else {
-        const char *kb = reinterpret_cast<const char *>(a.k) + (size_t)lo * skb + (size_t)hk * DK * 2;
-        const char *qb = reinterpret_cast<const char *>(a.q) + (size_t)lo * skb + (size_t)hk * DK * 2;
+        const char *kb = reinterpret_cast<const char *>(a.k) + (size_t)lo * skb + (size_t)hk * dk * 2;
+        const char *qb = reinterpret_cast<const char *>(a.q) + (size_t)lo * skb + (size_t)hk * dk * 2;
+        const bool has_part = WHOLE || 8 * (tid % CH) < dk;          // of K
+        const bool has_v = WHOLE || 16 * cg + 8 * (tid & 1) < s.DV;
         const char *vb = reinterpret_cast<const char *>(a.v) + (size_t)lo * svb + c0;
         char *ob = reinterpret_cast<char *>(a.out) + (size_t)lo * svb + c0;
         const uint32_t koff = (uint32_t)(tid / CH) * skb + 16 * (tid % CH), qoff = my_row * skb + 16 * g,
                        ooff = my_row * svb + 8 * g;
-        bf16x8 kr[PER], q[KS], p[2], vr;
+        bf16x8 kr[PER], q[KS], p[2], vr = (bf16x8)(__bf16)0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) kr[j] = (bf16x8)(__bf16)0.f;
         // with K: V's 64 x 32 bytes by the first two wavefronts, start and end by half the third
         auto fetch_k = [&](int t0, int last, const ChunkSystem &w) {
             const char *k0 = kb + (size_t)t0 * skb;
@@ -270,11 +283,11 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             for (int j = 0; j < PER; ++j) {
                 uint32_t off = koff + ROWS * j * skb;
                 if (last < kChunk - 1) off = min(tid / CH + ROWS * j, last) * skb + 16 * (tid % CH);
-                kr[j] = load16(reinterpret_cast<const __bf16 *>(k0 + off));
+                if (has_part) kr[j] = load16(reinterpret_cast<const __bf16 *>(k0 + off));
             }
-            if (tid < 128)
+            if (tid < 128 && has_v)
                 vr = load16(reinterpret_cast<const __bf16 *>(vb + (size_t)t0 * svb + (uint32_t)min(tid >> 1, last) * svb + 16 * (tid & 1)));
-            else if (tid < 160)
+            else if (tid >= 128 && tid < 160)
                 vr = load16(reinterpret_cast<const __bf16 *>(&w.start[0]) + 8 * (tid - 128));
         };
         auto fetch_q = [&](int t0, int last) {
@@ -282,7 +295,10 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             uint32_t off = qoff;
             if (last < kChunk - 1) off = min(my_row, last) * skb + 16 * g;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) q[ks] = load16(reinterpret_cast<const __bf16 *>(q0 + off + 64 * ks));
+            for (int ks = 0; ks < KS; ++ks) {
+                q[ks] = (bf16x8)(__bf16)0.f;
+                if (WHOLE || 32 * ks + 8 * g < dk) q[ks] = load16(reinterpret_cast<const __bf16 *>(q0 + off + 64 * ks));
+            }
         };
         p[1] = (bf16x8)(__bf16)0.f;
         auto fetch_p = [&](const ChunkSystem &w) {
@@ -340,7 +356,7 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             stage((chunk + 1) & 1);
             const ChunkSystem &w2 = chunk_at(chunk + 2, t1, last);
             fetch_k(t1, last, w2);
-            if (chunk * kChunk + my_row < n)
+            if (chunk * kChunk + my_row < n && (WHOLE || 16 * cg + 4 * g < s.DV))
                 *reinterpret_cast<bf16x4 *>(ob + (size_t)(chunk * kChunk) * svb + ooff) =
                     __builtin_convertvector(o, bf16x4);
             lds_barrier();
@@ -352,7 +368,8 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 
 static bool chunked(const bole_delta_dims_t &d) {
     return d.factor_dtype == BOLE_DTYPE_BF16 && !(d.flags & BOLE_FLAG_FORCE_GENERIC) &&
-           (d.d_k == 64 || d.d_k == 128) && d.d_v % 16 == 0;
+           d.d_k <= 128 && d.d_k % 8 == 0 && d.d_v % 8 == 0 &&
+           (int64_t)d.heads * (d.d_v > d.d_k ? d.d_v : d.d_k) * 2 * kChunk <= 0x7fffffffLL;  // 32-bit offsets
 }
 
 static size_t slots_of(const bole_delta_dims_t &d) {
@@ -363,21 +380,16 @@ size_t delta_prefill_workspace(const bole_delta_dims_t &d) {
     return chunked(d) ? slots_of(d) * (size_t)d.heads * sizeof(ChunkSystem) : 0;
 }
 
-template <int DK>
-static void launch_scan(const PrefillArgs &a, hipStream_t stream) {
-    const int units = a.s.B * a.s.H, groups = a.s.DV / 16;
-    const unsigned grid = (unsigned)((units + 7) / 8) * 8u * (unsigned)groups;
-    delta_scan_kernel<DK><<<dim3(grid), dim3(512), 0, stream>>>(a, units, groups);
-}
-
-template <int DK>
+template <int DK, bool WHOLE>
 static hipError_t launch_chunked(const PrefillArgs &a, size_t slots, hipStream_t stream) {
     if (a.s.T > 0) {
-        delta_chunk_kernel<DK><<<dim3((unsigned)(slots * a.s.H)), dim3(256), 0, stream>>>(a);
+        delta_chunk_kernel<DK, WHOLE><<<dim3((unsigned)(slots * a.s.H)), dim3(256), 0, stream>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    launch_scan<DK>(a, stream);
+    const int units = a.s.B * a.s.H, groups = (a.s.DV + 15) / 16;
+    const unsigned grid = (unsigned)((units + 7) / 8) * 8u * (unsigned)groups;
+    delta_scan_kernel<DK, WHOLE><<<dim3(grid), dim3(512), 0, stream>>>(a, units, groups);
     return hipGetLastError();
 }
 
@@ -396,8 +408,11 @@ hipError_t launch_delta_prefill(float *H0, const void *q, const void *k, const v
                            static_cast<__bf16 *>(out), seq_status,
                            static_cast<ChunkSystem *>(workspace),
                            {d.batch, d.heads, d.key_heads, d.d_k, d.d_v, d.total_tokens}};
-    return d.d_k == 64 ? launch_chunked<64>(a, slots_of(d), stream)
-                       : launch_chunked<128>(a, slots_of(d), stream);
+    const size_t slots = slots_of(d);
+    if (d.d_v % 16 == 0 && d.d_k == 64) return launch_chunked<64, true>(a, slots, stream);
+    if (d.d_v % 16 == 0 && d.d_k == 128) return launch_chunked<128, true>(a, slots, stream);
+    return d.d_k <= 64 ? launch_chunked<64, false>(a, slots, stream)
+                       : launch_chunked<128, false>(a, slots, stream);
 }
 
 }  // namespace bole

@@ -100,28 +100,29 @@ __global__ __launch_bounds__(256) void delta_verify_generic_kernel(
     }
 }
 
-// bf16, d_k 64 or 128, d_v a multiple of 16: one workgroup of four wavefronts per (sequence,
-// value head, 64 NT columns). The loads of its state columns are in flight while it forms the
-// tree's system (delta_mfma.h); then every wavefront carries its 16 NT columns through
+// d_k up to 128 (a multiple of 8), any d_v: one workgroup of four wavefronts per (sequence, value
+// head, 64 NT columns). The loads of its state columns are in flight while it forms the tree's
+// system (delta_mfma.h); then every wavefront carries its 16 NT columns through
 //     R = V - diag(2^L) K H0,   U = X diag(b) R,   O = diag(2^L) Q H0 + P U
 // in registers, each product's results being the next one's operand. H0, X, R, P and U are
-// taken as two bf16 terms (2^-17 left), so that the output's own rounding is the one that
-// counts. Row slots past the last node repeat it: their columns of X diag(b) are zero.
+// taken as two bf16 terms (2^-17 left) for bf16 factors, as three for fp32 ones, so that the
+// output's own rounding is the one that counts. Row slots past the last node repeat it: their
+// columns of X diag(b) are zero.
 //
-// NT = 2: lane c of 16 holds columns 2c and 2c + 1, and a state row's 32 columns are one
-// 128-byte read.
-template <int DK, int NT>
+// NT = 2 (d_v a multiple of 32): lane c of 16 holds columns 2c and 2c + 1, and a state row's 32
+// columns are one 128-byte read.
+template <typename TF, int DK, int NT, bool WHOLE>
 __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
-    const float *__restrict__ H0, const __bf16 *__restrict__ q, const __bf16 *__restrict__ k,
-    const __bf16 *__restrict__ v, const float *__restrict__ gate, const float *__restrict__ beta,
+    const float *__restrict__ H0, const TF *__restrict__ q, const TF *__restrict__ k,
+    const TF *__restrict__ v, const float *__restrict__ gate, const float *__restrict__ beta,
     const int32_t *__restrict__ parent, const int32_t *__restrict__ node_offsets,
-    __bf16 *__restrict__ out, int32_t *__restrict__ tree_status, const DeltaShape s) {
+    TF *__restrict__ out, int32_t *__restrict__ tree_status, const DeltaShape s) {
     typedef float hvec __attribute__((ext_vector_type(NT)));
-    typedef __bf16 vvec __attribute__((ext_vector_type(NT)));
-    constexpr int KS = DK / 32;
+    typedef TF vvec __attribute__((ext_vector_type(NT)));
+    constexpr int KS = DK / 32, NK = Terms<TF>::K, NS = Terms<TF>::S;
     __shared__ DeltaTokens t;
     const int unit = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
-    const int col = lane & 15, g = lane >> 4;
+    const int col = lane & 15, g = lane >> 4, dk = WHOLE ? DK : s.DK;
     const int b = unit / s.H, h = unit - b * s.H, hk = h / (s.H / s.HK);
     const bool first = h == 0 && blockIdx.y == 0 && tid == 0 && tree_status;
     const TreeRange tr = tree_range(node_offsets, b, s.T);
@@ -130,22 +131,26 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         return;
     }
     const int lo = tr.lo, n = tr.n;
-    const size_t sk = (size_t)s.HK * DK, sv = (size_t)s.H * s.DV;
-    const __bf16 *kb = k + (size_t)lo * sk + (size_t)hk * DK, *qb = q + (size_t)lo * sk + (size_t)hk * DK;
-    const int c0 = (blockIdx.y * 4 + wave) * 16 * NT + NT * col;  // the lane's columns
-    const bool live = c0 < s.DV && n > 0;                         // wave-uniform: 16 NT divides d_v
-    const float *Hu = H0 + (size_t)unit * DK * s.DV + c0;
+    const size_t sk = (size_t)s.HK * dk, sv = (size_t)s.H * s.DV;
+    const TF *kb = k + (size_t)lo * sk + (size_t)hk * dk, *qb = q + (size_t)lo * sk + (size_t)hk * dk;
+    const int c0 = (blockIdx.y * 4 + wave) * 16 * NT;     // the wavefront's columns, then the lane's
+    const bool live = c0 < s.DV && n > 0;
+    const bool mine = NT == 2 || c0 + col < s.DV;         // lanes past the last column repeat it
+    const int c1 = NT == 2 ? c0 + 2 * col : min(c0 + col, s.DV - 1);
+    const float *Hu = H0 + (size_t)unit * dk * s.DV + c1;
     hvec hr[KS][8];
     if (live) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 8; ++e) {
+                const int row = 32 * ks + 8 * g + e;
                 hr[ks][e] = __builtin_nontemporal_load(
-                    reinterpret_cast<const hvec *>(Hu + (size_t)(32 * ks + 8 * g + e) * s.DV));
+                    reinterpret_cast<const hvec *>(Hu + (size_t)(WHOLE || row < dk ? row : 0) * s.DV));
+            }
     }
-    SystemRows<DK> rows;
-    if (n > 0) rows.load(kb, qb, sk, n);
+    SystemRows<TF, DK, WHOLE> rows;
+    if (n > 0) rows.load(kb, qb, sk, dk, n);
     if (tid < 64) {
         const bool in = tid < n;
         const float lg = in ? log2_decay(gate[(size_t)(lo + tid) * s.H + h]) : 0.f;
@@ -162,15 +167,15 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
     const size_t v0 = (size_t)lo * sv + (size_t)h * s.DV;
     if (t.bad) {
         for (int e = tid; e < n * s.DV; e += 256)
-            out[v0 + (size_t)(e / s.DV) * sv + e % s.DV] = (__bf16)__builtin_nanf("");
+            out[v0 + (size_t)(e / s.DV) * sv + e % s.DV] = (TF)__builtin_nanf("");
         return;
     }
     if (n == 0) return;
-    delta_system<DK, true>(t, rows, kb, sk, n);
+    delta_system<TF, DK, WHOLE, true>(t, rows, kb, sk, dk, n);
     // row tile m has tokens of the tree
     auto used = [&](int m) { return tile_token(m, 0) < n; };
     if (!live) return;
-    const size_t vc = v0 + c0;
+    const size_t vc = v0 + c1;
     f32x4 r[4][NT], o[4][NT];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -178,7 +183,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         for (int c = 0; c < NT; ++c) r[m][c] = o[m][c] = (f32x4)0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-        bf16x8 hb[NT][2];
+        bf16x8 hb[NT][NS];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             f32x4 x, y;
@@ -187,20 +192,21 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
                 x[e] = hr[ks][e][c];
                 y[e] = hr[ks][4 + e][c];
             }
-            split_terms8<2>(x, y, hb[c]);
+            if (!WHOLE && 32 * ks + 8 * g >= dk) x = y = (f32x4)0.f;
+            split_terms8<NS>(x, y, hb[c]);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if (!used(m)) continue;
-            const size_t row = (size_t)min(tile_token(m, col), n - 1) * sk + 32 * ks + 8 * g;
-            const bf16x8 ka = load16(kb + row), qa = load16(qb + row);
+            const size_t row = (size_t)min(tile_token(m, col), n - 1) * sk;
+            bf16x8 ka[NK], qa[NK];
+            row_part<WHOLE>(kb + row, 4 * ks + g, dk).terms(ka);
+            row_part<WHOLE>(qb + row, 4 * ks + g, dk).terms(qa);
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int e = 1; e >= 0; --e) {
-                    r[m][c] = mfma16_bf16(ka, hb[c][e], r[m][c]);
-                    o[m][c] = mfma16_bf16(qa, hb[c][e], o[m][c]);
-                }
+            for (int c = 0; c < NT; ++c) {
+                r[m][c] = mfma_terms(ka, hb[c], r[m][c]);
+                o[m][c] = mfma_terms(qa, hb[c], o[m][c]);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);  // rows of one step at a time in registers
     }
@@ -222,11 +228,11 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
     // U from R, then O, 32 tokens (two row tiles) of the right operand at a time
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
-        bf16x8 rb[2][NT][2];
+        bf16x8 rb[2][NT][NS];
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int c = 0; c < NT; ++c) split_terms8<2>(r[2 * sb][c], r[2 * sb + 1][c], rb[sb][c]);
+            for (int c = 0; c < NT; ++c) split_terms8<NS>(r[2 * sb][c], r[2 * sb + 1][c], rb[sb][c]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if (!used(m)) continue;
@@ -236,14 +242,14 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
 #pragma unroll
             for (int sb = 0; sb <= (m >> 1); ++sb) {
                 f32x4 x, y;
-                bf16x8 a[2];
+                bf16x8 a[NS];
                 if (step == 0) x_piece(t, tile_token(m, col), sb, g, x, y);
                 else p_piece(t, tile_token(m, col), sb, g, x, y);
-                split_terms8<2>(x, y, a);
+                split_terms8<NS>(x, y, a);
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
-                    if (step == 0) r[m][c] = mfma_terms<2>(a, rb[sb][c], r[m][c]);
-                    else o[m][c] = mfma_terms<2>(a, rb[sb][c], o[m][c]);
+                    if (step == 0) r[m][c] = mfma_terms(a, rb[sb][c], r[m][c]);
+                    else o[m][c] = mfma_terms(a, rb[sb][c], o[m][c]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -256,21 +262,17 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
             const int i = tile_token(m, 4 * g + e);
             vvec y;
 #pragma unroll
-            for (int c = 0; c < NT; ++c) y[c] = (__bf16)o[m][c][e];
-            if (i < n) *reinterpret_cast<vvec *>(out + vc + (size_t)i * sv) = y;
+            for (int c = 0; c < NT; ++c) y[c] = (TF)o[m][c][e];
+            if (i < n && mine) *reinterpret_cast<vvec *>(out + vc + (size_t)i * sv) = y;
         }
 }
 
-static bool verify_covers(const bole_delta_dims_t &d, const void *H0, const void *q, const void *k,
-                          const void *v, const void *out) {
-    const uintptr_t rows = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k);
-    const uintptr_t wide = reinterpret_cast<uintptr_t>(H0) | 2 * reinterpret_cast<uintptr_t>(v) |
-                           2 * reinterpret_cast<uintptr_t>(out);
-    return d.factor_dtype == BOLE_DTYPE_BF16 && !(d.flags & BOLE_FLAG_FORCE_GENERIC) &&
-           (d.d_k == 64 || d.d_k == 128) && d.d_v % 16 == 0 && rows % 16 == 0 && wide % 8 == 0;
+static bool verify_covers(const bole_delta_dims_t &d, const void *q, const void *k) {
+    return !(d.flags & BOLE_FLAG_FORCE_GENERIC) && d.d_k <= 128 && d.d_k % 8 == 0 &&
+           (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) % 16 == 0;
 }
 
-template <int DK>
+template <typename TF, int DK, bool WHOLE>
 static hipError_t launch_mfma(const float *H0, const void *q, const void *k, const void *v,
                               const float *gate, const float *beta, const int32_t *parent,
                               const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
@@ -278,17 +280,31 @@ static hipError_t launch_mfma(const float *H0, const void *q, const void *k, con
     const DeltaShape s = {d.batch, d.heads, d.key_heads, d.d_k, d.d_v, d.total_tokens};
     const unsigned units = (unsigned)d.batch * (unsigned)d.heads;
     const dim3 block(256);
-    const __bf16 *qb = static_cast<const __bf16 *>(q), *kb = static_cast<const __bf16 *>(k),
-                 *vb = static_cast<const __bf16 *>(v);
-    __bf16 *ob = static_cast<__bf16 *>(out);
-    // 32 columns a wavefront where that still gives each of the four some
-    if (d.d_v % 32 == 0 && d.d_v > 64)
-        delta_verify_kernel<DK, 2><<<dim3(units, (d.d_v + 127) / 128), block, 0, stream>>>(H0, qb, kb, vb, gate, beta, parent,
-                                                               node_offsets, ob, tree_status, s);
+    const TF *qb = static_cast<const TF *>(q), *kb = static_cast<const TF *>(k), *vb = static_cast<const TF *>(v);
+    TF *ob = static_cast<TF *>(out);
+    // 32 columns a wavefront (in pairs, so on even addresses) where that still gives each of the
+    // four some
+    const uintptr_t pairs = reinterpret_cast<uintptr_t>(H0) % 8 |
+                            (reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(out)) % (2 * sizeof(TF));
+    if (d.d_v % 32 == 0 && d.d_v > 64 && pairs == 0)
+        delta_verify_kernel<TF, DK, 2, WHOLE><<<dim3(units, (d.d_v + 127) / 128), block, 0, stream>>>(
+            H0, qb, kb, vb, gate, beta, parent, node_offsets, ob, tree_status, s);
     else
-        delta_verify_kernel<DK, 1><<<dim3(units, (d.d_v + 63) / 64), block, 0, stream>>>(H0, qb, kb, vb, gate, beta, parent,
-                                                               node_offsets, ob, tree_status, s);
+        delta_verify_kernel<TF, DK, 1, WHOLE><<<dim3(units, (d.d_v + 63) / 64), block, 0, stream>>>(
+            H0, qb, kb, vb, gate, beta, parent, node_offsets, ob, tree_status, s);
     return hipGetLastError();
+}
+
+template <typename TF>
+static hipError_t launch_mfma_width(const float *H0, const void *q, const void *k, const void *v,
+                                    const float *gate, const float *beta, const int32_t *parent,
+                                    const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
+                                    int32_t *tree_status, hipStream_t stream) {
+    auto go = [&](auto launch) {
+        return launch(H0, q, k, v, gate, beta, parent, node_offsets, out, d, tree_status, stream);
+    };
+    if (d.d_k <= 64) return d.d_k == 64 ? go(launch_mfma<TF, 64, true>) : go(launch_mfma<TF, 64, false>);
+    return d.d_k == 128 ? go(launch_mfma<TF, 128, true>) : go(launch_mfma<TF, 128, false>);
 }
 
 template <typename TF>
@@ -309,11 +325,12 @@ hipError_t launch_delta_verify(const float *H0, const void *q, const void *k, co
                                const float *gate, const float *beta, const int32_t *parent,
                                const int32_t *node_offsets, void *out, const bole_delta_dims_t &d,
                                int32_t *tree_status, hipStream_t stream) {
-    if (verify_covers(d, H0, q, k, v, out))
-        return d.d_k == 64 ? launch_mfma<64>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
-                                             tree_status, stream)
-                           : launch_mfma<128>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
-                                              tree_status, stream);
+    if (verify_covers(d, q, k))
+        return d.factor_dtype == BOLE_DTYPE_F32
+                   ? launch_mfma_width<float>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
+                                              tree_status, stream)
+                   : launch_mfma_width<__bf16>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
+                                               tree_status, stream);
     return d.factor_dtype == BOLE_DTYPE_F32
                ? launch_generic<float>(H0, q, k, v, gate, beta, parent, node_offsets, out, d,
                                        tree_status, stream)
