@@ -26,6 +26,28 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// x of this lane and of the lane with bit 3, 4 or 5 of its number flipped, added up or the larger
+// one: one or two vector instructions each, where a shuffle takes a round trip through LDS.
+__device__ __forceinline__ float flip8(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, false));
+}
+
+__device__ __forceinline__ float2 pair16(float x) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return {__uint_as_float(p[0]), __uint_as_float(p[1])};
+}
+
+__device__ __forceinline__ float2 pair32(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return {__uint_as_float(p[0]), __uint_as_float(p[1])};
+}
+
+__device__ __forceinline__ float sum8(float x) { return x + flip8(x); }
+__device__ __forceinline__ float sum16(float x) { const float2 p = pair16(x); return p.x + p.y; }
+__device__ __forceinline__ float sum32(float x) { const float2 p = pair32(x); return p.x + p.y; }
+__device__ __forceinline__ float max16(float x) { const float2 p = pair16(x); return fmaxf(p.x, p.y); }
+__device__ __forceinline__ float max32(float x) { const float2 p = pair32(x); return fmaxf(p.x, p.y); }
+
 // Barrier for data in LDS alone. __syncthreads also waits for every global load in flight, and
 // with it a prefetch for the next step would end at the first barrier of this one.
 __device__ __forceinline__ void lds_barrier() {

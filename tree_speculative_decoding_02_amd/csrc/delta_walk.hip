@@ -8,7 +8,7 @@
 // A wavefront owns 8 CPL columns of one state and keeps all of their rows in registers: lane
 // (rg, cg) = (lane / 8, lane % 8) holds rows rg RPL .. rg RPL + RPL - 1 of columns cg CPL ..
 // cg CPL + CPL - 1. w and z are summed over the lane's rows, then over the eight row groups
-// with three cross-lane exchanges. Nothing is shared between wavefronts: no LDS, no barrier.
+// with three cross-lane steps. Nothing is shared between wavefronts: no LDS, no barrier.
 // The state is read once and written once whatever the number of tokens, with non-temporal
 // 16-byte accesses (a row's eight lanes cover 128 contiguous bytes).
 //
@@ -65,9 +65,25 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(const WalkArgs a, int u
     const int H = a.s.H, DK = a.s.DK, DV = a.s.DV;
     const int b = unit / H, h = unit - b * H, hk = h / (H / a.s.HK);
 
+    const int rg = lane >> 3, c0 = (cb * 8 + (lane & 7)) * CPL, r0 = rg * RPL;
+    const bool live = c0 < DV;  // CPL divides d_v: a lane's columns exist or do not together
+    float *Hu = a.H0 + (size_t)unit * DK * DV + c0;
+    hvec hr[RPL];
+    auto load_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) {
+            hr[i] = (hvec)0.f;
+            if (live && (EXACT || r0 + i < DK))
+                hr[i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const hvec *>(Hu + (size_t)(r0 + i) * DV));
+        }
+    };
+
     // the tokens: `row` of lane m is the m-th of a path, lo + m for the other modes
     int lo = b, n = 1, path_row = -1;
     if constexpr (MODE == kWalkCommit) {
+        // the state is on its way while the path is checked (it is read for nothing if that fails)
+        if (a.accepted_len[b] > 0) load_state();
         const WavePath p = wave_path(a.parent, a.offsets, a.accepted_idx, a.accepted_len, b, a.s.T,
                                      a.max_path);
         n = p.len;
@@ -86,19 +102,9 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(const WalkArgs a, int u
     }
     if (n <= 0) return;
 
-    const int rg = lane >> 3, c0 = (cb * 8 + (lane & 7)) * CPL, r0 = rg * RPL;
-    const bool live = c0 < DV;  // CPL divides d_v: a lane's columns exist or do not together
     const TF *q = static_cast<const TF *>(a.q), *k = static_cast<const TF *>(a.k),
              *v = static_cast<const TF *>(a.v);
-    float *Hu = a.H0 + (size_t)unit * DK * DV + c0;
-    hvec hr[RPL];
-#pragma unroll
-    for (int i = 0; i < RPL; ++i) {
-        hr[i] = (hvec)0.f;
-        if (live && (EXACT || r0 + i < DK))
-            hr[i] = __builtin_nontemporal_load(
-                reinterpret_cast<const hvec *>(Hu + (size_t)(r0 + i) * DV));
-    }
+    if constexpr (MODE != kWalkCommit) load_state();
     constexpr bool OUT = MODE != kWalkCommit;
     const size_t sk = (size_t)a.s.HK * DK, sv = (size_t)H * DV;
     RowPiece<TF, RPL, EXACT> kn, qn;
@@ -135,14 +141,11 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(const WalkArgs a, int u
             }
         }
 #pragma unroll
-        for (int d = 8; d < 64; d <<= 1) {
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                w[c] += __shfl_xor(w[c], d, 64);
-                if constexpr (OUT) z[c] += __shfl_xor(z[c], d, 64);
-            }
-            if constexpr (OUT) kq += __shfl_xor(kq, d, 64);
+        for (int c = 0; c < CPL; ++c) {
+            w[c] = sum32(sum16(sum8(w[c])));
+            if constexpr (OUT) z[c] = sum32(sum16(sum8(z[c])));
         }
+        if constexpr (OUT) kq = sum32(sum16(sum8(kq)));
         float u[CPL];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) u[c] = bc * (vc[c] - ac * w[c]);

@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, z[sub][r]);
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        top = max32(top);
         const float next = fmaxf(m, top);
         // nothing seen so far: keep every exponential at 0
         const float base = next == -INFINITY ? 0.f : next;
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         lds_barrier();
     } while (++tile < last);
     }
-    l += __shfl_xor(l, 32, 64);
+    l = sum32(l);
     if (!live) return;
     if (parts.n > 1) {
         if (hh == 0) {
@@ -369,8 +369,8 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, z[r][e]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        top = max16(top);
+        top = max32(top);
         const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
         const float keep = __builtin_amdgcn_exp2f(m - base);
         m = next;
@@ -403,8 +403,8 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
         asm volatile("" ::: "memory");
     } while ((tile += 4) < last);
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+    l = sum16(l);
+    l = sum32(l);
 
     // the four wavefronts' parts: O^T as [wave][row][D + 4]
     lds_barrier();

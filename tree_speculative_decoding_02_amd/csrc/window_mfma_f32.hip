@@ -145,8 +145,8 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
             for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, z[kt][e]);
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            top = max16(top);
+            top = max32(top);
             const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
             const float keep = __builtin_amdgcn_exp2f(m - base);
             m = next;
@@ -171,8 +171,8 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
                 }
         } while (++tile < last);
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+    l = sum16(l);
+    l = sum32(l);
     if (!live) return;
     if (parts.n > 1) {
         if (g == 0) {

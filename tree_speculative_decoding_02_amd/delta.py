@@ -16,21 +16,30 @@ from .bole import (BOLE_DTYPE_BF16, BOLE_DTYPE_F32, BOLE_FLAG_FORCE_GENERIC, BOL
                    _need, _ptr, bole_delta_dims_t, lib)
 
 
-def _run(fn, what, args, device, stream):
-    """The C call `fn(*args, stream)` on `device`."""
+def _handle(what, device, stream):
+    """The stream's handle, checked once; None for the one that is current at each call."""
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        return None
+    if stream.device != device:
+        raise ValueError(f"{what}: the stream belongs to {stream.device}, the tensors to {device}")
+    return stream.cuda_stream
+
+
+def _launch(fn, what, args, index, handle):
+    """The C call `fn(*args, stream)` on GPU `index`. torch's own accessors stand behind
+    torch.cuda.current_device() and current_stream(): those cost a short call as much as its
+    kernel takes."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if handle is None else handle)
     else:
-        if stream.device != device:
-            raise ValueError(f"{what}: the stream belongs to {stream.device}, the tensors to {device}")
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if handle is None else handle)
     if st != BOLE_OK:
         _check(st, what)
+
+
+def _run(fn, what, args, device, stream):
+    _launch(fn, what, args, device.index, _handle(what, device, stream))
 
 
 def _allocating_on(stream):
@@ -43,11 +52,11 @@ class _BoundCall:
     C call again on these buffers, which the object keeps alive."""
 
     def __init__(self, fn, what, args, device, stream, keep):
-        self._a = (fn, what, args, device, stream)
-        self._keep = keep
+        self._a = (fn, what, args, device.index, _handle(what, device, stream))
+        self._keep = keep, stream
 
     def __call__(self):
-        _run(*self._a)
+        _launch(*self._a)
 
 
 def _shaped(t, name, dtype, device, shape):
