@@ -171,20 +171,29 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(const WalkArgs a, int u
 
 static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+template <int MODE, typename TF, int RPL, int CPL>
+static hipError_t launch_columns(const WalkArgs &a, hipStream_t stream) {
+    const int units = a.s.B * a.s.H, cols = 8 * CPL, blocks = (a.s.DV + cols - 1) / cols;
+    const bool exact = a.s.DK == 8 * RPL && aligned16(a.k) && (MODE == kWalkCommit || aligned16(a.q));
+    const dim3 grid((unsigned)(((int64_t)units * blocks + 3) / 4)), block(256);
+    if (exact)
+        delta_walk_kernel<MODE, TF, RPL, CPL, true><<<grid, block, 0, stream>>>(a, units, blocks);
+    else
+        delta_walk_kernel<MODE, TF, RPL, CPL, false><<<grid, block, 0, stream>>>(a, units, blocks);
+    return hipGetLastError();
+}
+
+// Four columns a lane (16-byte accesses), or one and four times the wavefronts where four would
+// leave the chip unfilled: a token's chain is then a quarter as long, the accesses 32 bytes wide.
+// Steps, which move a state for one token's chain, gain below 512 wide wavefronts (128 x 128
+// states of 32 heads, bf16: 3.4 against 4.0 us for one sequence, 5.4 against 5.0 for four), paths
+// and prompts below 2048 (paths of up to 10 nodes, 8 sequences: 10.9 against 13.2 us; 16: equal).
 template <int MODE, typename TF, int RPL>
 static hipError_t launch_rows(const WalkArgs &a, hipStream_t stream) {
-    const int units = a.s.B * a.s.H;
     const bool wide = a.s.DV % 4 == 0 && aligned16(a.H0);
-    const bool exact = a.s.DK == 8 * RPL && aligned16(a.k) && (MODE == kWalkCommit || aligned16(a.q));
-    const int cols = wide ? 32 : 8, blocks = (a.s.DV + cols - 1) / cols;
-    const dim3 grid((unsigned)(((int64_t)units * blocks + 3) / 4)), block(256);
-    if (wide && exact)
-        delta_walk_kernel<MODE, TF, RPL, 4, true><<<grid, block, 0, stream>>>(a, units, blocks);
-    else if (wide)
-        delta_walk_kernel<MODE, TF, RPL, 4, false><<<grid, block, 0, stream>>>(a, units, blocks);
-    else
-        delta_walk_kernel<MODE, TF, RPL, 1, false><<<grid, block, 0, stream>>>(a, units, blocks);
-    return hipGetLastError();
+    if (wide && (int64_t)a.s.B * a.s.H * ((a.s.DV + 31) / 32) >= (MODE == kWalkStep ? 512 : 2048))
+        return launch_columns<MODE, TF, RPL, 4>(a, stream);
+    return launch_columns<MODE, TF, RPL, 1>(a, stream);
 }
 
 template <int MODE, typename TF>
