@@ -21,27 +21,30 @@ namespace bole {
 // load them, 64 lanes times 8 values a piece. Row tiles 0 and 1 have one piece (tokens 0..31),
 // tiles 2 and 3 two; what lies right of the diagonal is zero and not stored.
 constexpr int kPieces = 6;
+template <typename TF>
 struct ChunkSystem {
-    __bf16 x[3][kPieces][64][8]; // X diag(b), three terms
-    __bf16 p[kPieces][64][8];    // P
+    static constexpr int kP = sizeof(TF) == 2 ? 1 : 3;
+    __bf16 x[3][kPieces][64][8];  // X diag(b), three terms
+    __bf16 p[kP][kPieces][64][8]; // P
     float start[kChunk], end[kChunk];
 };
 
 __device__ __forceinline__ int piece_of(int m, int s) { return s == 0 ? m : 2 + m; }
 
+template <typename TF>
 struct PrefillArgs {
     float *H0;
-    const __bf16 *q, *k, *v;
+    const TF *q, *k, *v;
     const float *gate, *beta;
     const int32_t *offsets;
-    __bf16 *out;
+    TF *out;
     int32_t *status;
-    ChunkSystem *ws;
+    ChunkSystem<TF> *ws;
     DeltaShape s;
 };
 
-template <int DK, bool WHOLE>
-__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a) {
+template <typename TF, int DK, bool WHOLE>
+__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs<TF> a) {
     __shared__ DeltaTokens t;
     const DeltaShape &s = a.s;
     const int h = blockIdx.x % s.H, slot = blockIdx.x / s.H, hk = h / (s.H / s.HK);
@@ -50,10 +53,10 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
     if (!l.found) return;
     const int done = (slot - l.slot0) * kChunk, lo = l.lo + done, n = min(kChunk, l.n - done);
     if (n <= 0) return;
-    ChunkSystem &w = a.ws[(size_t)slot * s.H + h];
+    ChunkSystem<TF> &w = a.ws[(size_t)slot * s.H + h];
     const int dk = WHOLE ? DK : s.DK;
     const size_t sk = (size_t)s.HK * dk, row0 = (size_t)lo * sk + (size_t)hk * dk;
-    SystemRows<__bf16, DK, WHOLE> rows;
+    SystemRows<TF, DK, WHOLE> rows;
     rows.load(a.k + row0, a.q + row0, sk, dk, n);
     if (tid < 64) {
         // tokens past the last do not decay and have no strength
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
         w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - L)) : 0.f;
     }
     lds_barrier();
-    delta_system<__bf16, DK, WHOLE, false>(t, rows, a.k + row0, sk, dk, n);
+    delta_system<TF, DK, WHOLE, false>(t, rows, a.k + row0, sk, dk, n);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
         if (sb > (wave >> 1)) continue;
@@ -80,9 +83,11 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs a
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8 *>(&w.x[i][f][lane][0]) = xt[i];
         p_piece(t, tile_token(wave, col), sb, g, x, y);
-        bf16x8 p[1];
-        split_terms8<1>(x, y, p);
-        *reinterpret_cast<bf16x8 *>(&w.p[f][lane][0]) = p[0];
+        constexpr int NP = ChunkSystem<TF>::kP;
+        bf16x8 p[NP];
+        split_terms8<NP>(x, y, p);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8 *>(&w.p[i][f][lane][0]) = p[i];
     }
 }
 
@@ -107,17 +112,24 @@ __device__ __forceinline__ int k_at(int row, int c) {
 // with the four wavefronts doing everything, 4.6 us with wavefronts that do all 64 tokens of 16
 // columns of their own and exchange nothing.
 //
+// fp32 factors: K lies in LDS as three bf16 terms, Q, U and P are taken as three too, and every
+// product as the six of them that reach 2^-24; one workgroup a CU.
+//
 // WHOLE: d_k = DK and d_v is a multiple of 16. Otherwise both are multiples of 8; parts of rows
 // from d_k on count as zero, lanes past the last column load what they do not store.
-template <int DK, bool WHOLE>
-__global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a, int units, int groups) {
+template <typename TF, int DK, bool WHOLE>
+__global__ __launch_bounds__(512, sizeof(TF) == 2 ? 4 : 2) void delta_scan_kernel(
+    const PrefillArgs<TF> a, int units, int groups) {
+    typedef ChunkSystem<TF> System;
+    typedef TF tf4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = Terms<TF>::K, NS = Terms<TF>::S, SZ = sizeof(TF);
     constexpr int KS = DK / 32, TILES = DK / 64, CH = DK / 8, PER = kChunk * CH / 256;
-    __shared__ __align__(16) __bf16 s_k[2][kChunk * DK];
+    __shared__ __align__(16) __bf16 s_k[2][NK][kChunk * DK];
     __shared__ __align__(16) __bf16 s_s[3][KS][64][8];   // state, three terms
     __shared__ __align__(16) __bf16 s_r[3][2][64][8];    // R
     __shared__ __align__(16) __bf16 s_e[3][2][64][8];    // end U, for the state
-    __shared__ __align__(16) __bf16 s_u[2][2][64][8];    // U, for the output
-    __shared__ __align__(16) __bf16 s_v[2][kChunk * 16]; // V, the workgroup's columns
+    __shared__ __align__(16) __bf16 s_u[NS][2][64][8];   // U, for the output
+    __shared__ __align__(16) TF s_v[2][kChunk * 16];     // V, the workgroup's columns
     __shared__ __align__(16) float s_w[2][2 * kChunk];   // start, end
     const DeltaShape &s = a.s;
     // the column groups of a unit go to one XCD (workgroups are dealt to the eight in turn):
@@ -139,10 +151,10 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
     const int chunks = (n + kChunk - 1) / kChunk;
     // addresses are a chunk's (scalar) plus a lane's 32-bit offset in bytes
     const int dk = WHOLE ? DK : s.DK;
-    const uint32_t skb = (uint32_t)s.HK * dk * 2, svb = (uint32_t)s.H * s.DV * 2;
-    const size_t c0 = ((size_t)h * s.DV + 16 * cg) * 2;
+    const uint32_t skb = (uint32_t)s.HK * dk * SZ, svb = (uint32_t)s.H * s.DV * SZ;
+    const size_t c0 = ((size_t)h * s.DV + 16 * cg) * SZ;
     const char *ws = reinterpret_cast<const char *>(a.ws + ((size_t)(lo / kChunk + b)) * s.H + h);
-    const size_t ws_step = (size_t)s.H * sizeof(ChunkSystem);
+    const size_t ws_step = (size_t)s.H * sizeof(System);
     // Rows past the last token repeat it: their columns of X diag(b) and their `end` are zero,
     // and their outputs are not stored. Past the last chunk it is loaded again.
     const int my_row = tile_token(wave, col), my_token = tile_token(wave, 4 * g);
@@ -180,7 +192,7 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 #pragma unroll
         for (int i = 0; i < 3; ++i) x[1][i] = (bf16x8)(__bf16)0.f;
         auto fetch_x = [&](int chunk) {
-            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws + min(chunk, chunks - 1) * ws_step);
+            const System &w = *reinterpret_cast<const System *>(ws + min(chunk, chunks - 1) * ws_step);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 x[0][i] = load16(&w.x[i][piece_of(wave, 0)][lane][0]);
@@ -199,12 +211,24 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             for (int i = 0; i < 3; ++i) r[i] = (f32x4)0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const bf16x8 ka = load16(&s_k[buf][k_at<DK>(my_row, 4 * ks + g)]);
+                bf16x8 ka[NK];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) r[i] = mfma16_bf16(ka, load16(&s_s[i][ks][lane][0]), r[i]);
+                for (int j = 0; j < NK; ++j) ka[j] = load16(&s_k[buf][j][k_at<DK>(my_row, 4 * ks + g)]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const bf16x8 sb = load16(&s_s[i][ks][lane][0]);
+#pragma unroll
+                    for (int j = 0; j < NK && i + j < 3; ++j) r[i + j] = mfma16_bf16(ka[j], sb, r[i + j]);
+                }
             }
             const f32x4 start = *reinterpret_cast<const f32x4 *>(&s_w[buf][my_token]);
-            const bf16x4 v = read_transposed(&s_v[buf][(my_token + (col >> 2)) * 16 + 4 * (col & 3)]);
+            tf4 v;
+            if constexpr (SZ == 2) {
+                v = read_transposed(&s_v[buf][(my_token + (col >> 2)) * 16 + 4 * (col & 3)]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = s_v[buf][(my_token + e) * 16 + col];
+            }
             r[0] += r[2] + r[1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[0][e] = fmaf(-start[e], r[0][e], (float)v[e]);
@@ -248,10 +272,12 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
                 for (int sb = 0; sb < 2; ++sb) {
                     // state rows of lanes 4c .. 4c + 3: 32 (m / 2) + 8 c + 4 (m % 2) ..
                     const int row = 32 * sb + 8 * g + (col >> 2), c = 4 * (m >> 1) + (col & 3);
-                    const bf16x8 ka = join(read_transposed(&s_k[buf][k_at<DK>(row, c) + 4 * (m & 1)]),
-                                           read_transposed(&s_k[buf][k_at<DK>(row + 4, c) + 4 * (m & 1)]));
+                    bf16x8 ka[NK];
 #pragma unroll
-                    for (int i = 2; i >= 0; --i) y[sb] = mfma16_bf16(ka, eb[sb][i], y[sb]);
+                    for (int i = 0; i < NK; ++i)
+                        ka[i] = join(read_transposed(&s_k[buf][i][k_at<DK>(row, c) + 4 * (m & 1)]),
+                                     read_transposed(&s_k[buf][i][k_at<DK>(row + 4, c) + 4 * (m & 1)]));
+                    y[sb] = mfma_terms(ka, eb[sb], y[sb]);
                 }
                 st[j] = y[0] + y[1];
                 put(st[j], m, s_s);
@@ -264,83 +290,96 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             for (int e = 0; e < 4; ++e)
                 if (state_has(j, e)) state_at(j, e) = st[j][e];
     } else {
-        const char *kb = reinterpret_cast<const char *>(a.k) + (size_t)lo * skb + (size_t)hk * dk * 2;
-        const char *qb = reinterpret_cast<const char *>(a.q) + (size_t)lo * skb + (size_t)hk * dk * 2;
-        const bool has_part = WHOLE || 8 * (tid % CH) < dk;          // of K
-        const bool has_v = WHOLE || 16 * cg + 8 * (tid & 1) < s.DV;
+        const char *kb = reinterpret_cast<const char *>(a.k) + (size_t)lo * skb + (size_t)hk * dk * SZ;
+        const char *qb = reinterpret_cast<const char *>(a.q) + (size_t)lo * skb + (size_t)hk * dk * SZ;
         const char *vb = reinterpret_cast<const char *>(a.v) + (size_t)lo * svb + c0;
         char *ob = reinterpret_cast<char *>(a.out) + (size_t)lo * svb + c0;
-        const uint32_t koff = (uint32_t)(tid / CH) * skb + 16 * (tid % CH), qoff = my_row * skb + 16 * g,
-                       ooff = my_row * svb + 8 * g;
-        bf16x8 kr[PER], q[KS], p[2], vr = (bf16x8)(__bf16)0.f;
+        constexpr int VP = 16 * SZ / 16, VT = kChunk * VP;     // 16-byte parts of a V row, of V
+        const bool has_part = WHOLE || 8 * (tid % CH) < dk;    // of K
+        const bool has_v = WHOLE || 16 * cg + 16 / SZ * (tid % VP) < s.DV;
+        const uint32_t koff = (uint32_t)(tid / CH) * skb + 8 * SZ * (tid % CH), qoff = my_row * skb + 8 * SZ * g,
+                       ooff = my_row * svb + 4 * SZ * g;
+        RowPart<TF> kr[PER], q[KS];
+        bf16x8 p[2][System::kP], vr = (bf16x8)(__bf16)0.f, wr;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) kr[j] = (bf16x8)(__bf16)0.f;
-        // with K: V's 64 x 32 bytes by the first two wavefronts, start and end by half the third
-        auto fetch_k = [&](int t0, int last, const ChunkSystem &w) {
+        for (int j = 0; j < PER; ++j) kr[j].clear();
+        // with K: V by the first threads, start and end (512 bytes) by 32 others
+        auto fetch_k = [&](int t0, int last, const System &w) {
             const char *k0 = kb + (size_t)t0 * skb;
             constexpr int ROWS = 256 / CH;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 uint32_t off = koff + ROWS * j * skb;
-                if (last < kChunk - 1) off = min(tid / CH + ROWS * j, last) * skb + 16 * (tid % CH);
-                if (has_part) kr[j] = load16(reinterpret_cast<const __bf16 *>(k0 + off));
+                if (last < kChunk - 1) off = min(tid / CH + ROWS * j, last) * skb + 8 * SZ * (tid % CH);
+                if (has_part) kr[j].load(reinterpret_cast<const TF *>(k0 + off));
             }
-            if (tid < 128 && has_v)
-                vr = load16(reinterpret_cast<const __bf16 *>(vb + (size_t)t0 * svb + (uint32_t)min(tid >> 1, last) * svb + 16 * (tid & 1)));
-            else if (tid >= 128 && tid < 160)
-                vr = load16(reinterpret_cast<const __bf16 *>(&w.start[0]) + 8 * (tid - 128));
+            if (tid < VT && has_v)
+                vr = load16(reinterpret_cast<const __bf16 *>(vb + (size_t)t0 * svb + (uint32_t)min(tid / VP, last) * svb + 16 * (tid % VP)));
+            if (tid >= 224) wr = load16(reinterpret_cast<const __bf16 *>(&w.start[0]) + 8 * (tid - 224));
         };
         auto fetch_q = [&](int t0, int last) {
             const char *q0 = qb + (size_t)t0 * skb;
             uint32_t off = qoff;
-            if (last < kChunk - 1) off = min(my_row, last) * skb + 16 * g;
+            if (last < kChunk - 1) off = min(my_row, last) * skb + 8 * SZ * g;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                q[ks] = (bf16x8)(__bf16)0.f;
-                if (WHOLE || 32 * ks + 8 * g < dk) q[ks] = load16(reinterpret_cast<const __bf16 *>(q0 + off + 64 * ks));
+                if (!WHOLE) q[ks].clear();
+                if (WHOLE || 32 * ks + 8 * g < dk) q[ks].load(reinterpret_cast<const TF *>(q0 + off + 32 * SZ * ks));
             }
         };
-        p[1] = (bf16x8)(__bf16)0.f;
-        auto fetch_p = [&](const ChunkSystem &w) {
-            p[0] = load16(&w.p[piece_of(wave, 0)][lane][0]);
-            if (wave >= 2) p[1] = load16(&w.p[piece_of(wave, 1)][lane][0]);
+        auto fetch_p = [&](const System &w) {
+#pragma unroll
+            for (int i = 0; i < System::kP; ++i) {
+                p[0][i] = load16(&w.p[i][piece_of(wave, 0)][lane][0]);
+                if (wave >= 2) p[1][i] = load16(&w.p[i][piece_of(wave, 1)][lane][0]);
+            }
         };
+#pragma unroll
+        for (int i = 0; i < System::kP; ++i) p[1][i] = (bf16x8)(__bf16)0.f;
         auto stage = [&](int buf) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                *reinterpret_cast<bf16x8 *>(&s_k[buf][k_at<DK>(tid / CH + 256 / CH * j, tid % CH)]) = kr[j];
-            if (tid < 128) *reinterpret_cast<bf16x8 *>(&s_v[buf][8 * tid]) = vr;
-            else if (tid < 160) *reinterpret_cast<bf16x8 *>(&s_w[buf][4 * (tid - 128)]) = vr;
+            for (int j = 0; j < PER; ++j) {
+                bf16x8 y[NK];
+                kr[j].terms(y);
+#pragma unroll
+                for (int i = 0; i < NK; ++i)
+                    *reinterpret_cast<bf16x8 *>(&s_k[buf][i][k_at<DK>(tid / CH + 256 / CH * j, tid % CH)]) = y[i];
+            }
+            if (tid < VT) *reinterpret_cast<bf16x8 *>(reinterpret_cast<char *>(&s_v[buf][0]) + 16 * tid) = vr;
+            if (tid >= 224) *reinterpret_cast<bf16x8 *>(&s_w[buf][4 * (tid - 224)]) = wr;
         };
-        {
-            const int last = min(kChunk, n) - 1;
-            const ChunkSystem &w = *reinterpret_cast<const ChunkSystem *>(ws);
-            fetch_k(0, last, w);
-            fetch_q(0, last);
-            fetch_p(w);
-        }
-        stage(0);
-        auto chunk_at = [&](int chunk, int &t0, int &last) -> const ChunkSystem & {
+        auto chunk_at = [&](int chunk, int &t0, int &last) -> const System & {
             const int c = min(chunk, chunks - 1);
             t0 = c * kChunk;
             last = min(kChunk, n - t0) - 1;
-            return *reinterpret_cast<const ChunkSystem *>(ws + c * ws_step);
+            return *reinterpret_cast<const System *>(ws + c * ws_step);
         };
         int t1, last;
         {
-            const ChunkSystem &w = chunk_at(1, t1, last);
+            const System &w = chunk_at(0, t1, last);
             fetch_k(t1, last, w);
+            fetch_q(t1, last);
+            fetch_p(w);
+            stage(0);
+            const System &w1 = chunk_at(1, t1, last);
+            fetch_k(t1, last, w1);
         }
         lds_barrier();
         for (int chunk = 0; chunk < chunks; ++chunk) {
-            const ChunkSystem &w = chunk_at(chunk + 1, t1, last);
+            const System &w = chunk_at(chunk + 1, t1, last);
             // ---- O^T = S^T Q^T diag(start): a lane has four columns of one token's row (the
             // state's pieces serve as left operands just as they do as right ones)
             f32x4 o = (f32x4)0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                o = mfma16_bf16(load16(&s_s[1][ks][lane][0]), q[ks], o);
-                o = mfma16_bf16(load16(&s_s[0][ks][lane][0]), q[ks], o);
+                bf16x8 sb[NS], qt[NK];
+                q[ks].terms(qt);
+#pragma unroll
+                for (int i = 0; i < NS; ++i) sb[i] = load16(&s_s[i][ks][lane][0]);
+#pragma unroll
+                for (int i = NS - 1; i >= 0; --i)
+#pragma unroll
+                    for (int j = 0; j < NK && i + j < NS; ++j) o = mfma16_bf16(sb[i], qt[j], o);
             }
             o *= s_w[chunk & 1][my_row];
             fetch_q(t1, last);
@@ -349,16 +388,21 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
             // ---- O^T += U^T P^T
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb) {
-                o = mfma16_bf16(load16(&s_u[1][sb][lane][0]), p[sb], o);
-                o = mfma16_bf16(load16(&s_u[0][sb][lane][0]), p[sb], o);
+                bf16x8 ub[NS];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) ub[i] = load16(&s_u[i][sb][lane][0]);
+#pragma unroll
+                for (int i = NS - 1; i >= 0; --i)
+#pragma unroll
+                    for (int j = 0; j < System::kP && i + j < NS; ++j) o = mfma16_bf16(ub[i], p[sb][j], o);
             }
             fetch_p(w);
             stage((chunk + 1) & 1);
-            const ChunkSystem &w2 = chunk_at(chunk + 2, t1, last);
+            const System &w2 = chunk_at(chunk + 2, t1, last);
             fetch_k(t1, last, w2);
             if (chunk * kChunk + my_row < n && (WHOLE || 16 * cg + 4 * g < s.DV))
-                *reinterpret_cast<bf16x4 *>(ob + (size_t)(chunk * kChunk) * svb + ooff) =
-                    __builtin_convertvector(o, bf16x4);
+                *reinterpret_cast<tf4 *>(ob + (size_t)(chunk * kChunk) * svb + ooff) =
+                    __builtin_convertvector(o, tf4);
             lds_barrier();
         }
     }
@@ -367,9 +411,10 @@ __global__ __launch_bounds__(512, 4) void delta_scan_kernel(const PrefillArgs a,
 // ---- host
 
 static bool chunked(const bole_delta_dims_t &d) {
-    return d.factor_dtype == BOLE_DTYPE_BF16 && !(d.flags & BOLE_FLAG_FORCE_GENERIC) &&
-           d.d_k <= 128 && d.d_k % 8 == 0 && d.d_v % 8 == 0 &&
-           (int64_t)d.heads * (d.d_v > d.d_k ? d.d_v : d.d_k) * 2 * kChunk <= 0x7fffffffLL;  // 32-bit offsets
+    // row offsets within a chunk are 32-bit
+    const int64_t row = (int64_t)d.heads * (d.d_v > d.d_k ? d.d_v : d.d_k) * (d.factor_dtype == BOLE_DTYPE_F32 ? 4 : 2);
+    return !(d.flags & BOLE_FLAG_FORCE_GENERIC) && d.d_k <= 128 && d.d_k % 8 == 0 && d.d_v % 8 == 0 &&
+           row * kChunk <= 0x7fffffffLL;
 }
 
 static size_t slots_of(const bole_delta_dims_t &d) {
@@ -377,42 +422,55 @@ static size_t slots_of(const bole_delta_dims_t &d) {
 }
 
 size_t delta_prefill_workspace(const bole_delta_dims_t &d) {
-    return chunked(d) ? slots_of(d) * (size_t)d.heads * sizeof(ChunkSystem) : 0;
+    if (!chunked(d)) return 0;
+    return slots_of(d) * (size_t)d.heads *
+           (d.factor_dtype == BOLE_DTYPE_F32 ? sizeof(ChunkSystem<float>) : sizeof(ChunkSystem<__bf16>));
 }
 
-template <int DK, bool WHOLE>
-static hipError_t launch_chunked(const PrefillArgs &a, size_t slots, hipStream_t stream) {
+template <typename TF, int DK, bool WHOLE>
+static hipError_t launch_chunked(const PrefillArgs<TF> &a, size_t slots, hipStream_t stream) {
     if (a.s.T > 0) {
-        delta_chunk_kernel<DK, WHOLE><<<dim3((unsigned)(slots * a.s.H)), dim3(256), 0, stream>>>(a);
+        delta_chunk_kernel<TF, DK, WHOLE><<<dim3((unsigned)(slots * a.s.H)), dim3(256), 0, stream>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const int units = a.s.B * a.s.H, groups = (a.s.DV + 15) / 16;
     const unsigned grid = (unsigned)((units + 7) / 8) * 8u * (unsigned)groups;
-    delta_scan_kernel<DK, WHOLE><<<dim3(grid), dim3(512), 0, stream>>>(a, units, groups);
+    delta_scan_kernel<TF, DK, WHOLE><<<dim3(grid), dim3(512), 0, stream>>>(a, units, groups);
     return hipGetLastError();
+}
+
+template <typename TF>
+static hipError_t launch_typed(float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, const float *beta, const int32_t *seq_offsets,
+                               void *out, void *workspace, const bole_delta_dims_t &d,
+                               int32_t *seq_status, hipStream_t stream) {
+    const PrefillArgs<TF> a = {H0, static_cast<const TF *>(q), static_cast<const TF *>(k),
+                               static_cast<const TF *>(v), gate, beta, seq_offsets,
+                               static_cast<TF *>(out), seq_status,
+                               static_cast<ChunkSystem<TF> *>(workspace),
+                               {d.batch, d.heads, d.key_heads, d.d_k, d.d_v, d.total_tokens}};
+    const size_t slots = slots_of(d);
+    if (d.d_v % 16 == 0 && d.d_k == 64) return launch_chunked<TF, 64, true>(a, slots, stream);
+    if (d.d_v % 16 == 0 && d.d_k == 128) return launch_chunked<TF, 128, true>(a, slots, stream);
+    return d.d_k <= 64 ? launch_chunked<TF, 64, false>(a, slots, stream)
+                       : launch_chunked<TF, 128, false>(a, slots, stream);
 }
 
 hipError_t launch_delta_prefill(float *H0, const void *q, const void *k, const void *v,
                                 const float *gate, const float *beta, const int32_t *seq_offsets,
                                 void *out, void *workspace, const bole_delta_dims_t &d,
                                 int32_t *seq_status, hipStream_t stream) {
-    const bool aligned = (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
-                          reinterpret_cast<uintptr_t>(v)) % 16 == 0 &&
-                         reinterpret_cast<uintptr_t>(out) % 8 == 0;
-    if (!chunked(d) || !aligned)
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+                           reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(out);
+    if (!chunked(d) || rows % 16 != 0)
         return launch_delta_prefill_walk(H0, q, k, v, gate, beta, seq_offsets, out, d, seq_status,
                                          stream);
-    const PrefillArgs a = {H0, static_cast<const __bf16 *>(q), static_cast<const __bf16 *>(k),
-                           static_cast<const __bf16 *>(v), gate, beta, seq_offsets,
-                           static_cast<__bf16 *>(out), seq_status,
-                           static_cast<ChunkSystem *>(workspace),
-                           {d.batch, d.heads, d.key_heads, d.d_k, d.d_v, d.total_tokens}};
-    const size_t slots = slots_of(d);
-    if (d.d_v % 16 == 0 && d.d_k == 64) return launch_chunked<64, true>(a, slots, stream);
-    if (d.d_v % 16 == 0 && d.d_k == 128) return launch_chunked<128, true>(a, slots, stream);
-    return d.d_k <= 64 ? launch_chunked<64, false>(a, slots, stream)
-                       : launch_chunked<128, false>(a, slots, stream);
+    return d.factor_dtype == BOLE_DTYPE_F32
+               ? launch_typed<float>(H0, q, k, v, gate, beta, seq_offsets, out, workspace, d,
+                                     seq_status, stream)
+               : launch_typed<__bf16>(H0, q, k, v, gate, beta, seq_offsets, out, workspace, d,
+                                      seq_status, stream);
 }
 
 }  // namespace bole
