@@ -275,21 +275,19 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<TF
     lds_barrier();
 }
 
-// Row `token`, columns 32 s + 8 g .. + 7 of X diag(b).
-__device__ __forceinline__ void x_piece(const DeltaTokens &t, int token, int s, int g, f32x4 &a,
+// Row `token` of X diag(b) and of P, columns c .. c + 3 and d .. d + 3.
+__device__ __forceinline__ void x_piece(const DeltaTokens &t, int token, int c, int d, f32x4 &a,
                                         f32x4 &b) {
-    const int c0 = 32 * s + 8 * g;
-    a = *reinterpret_cast<const f32x4 *>(&t.X[square_at(token, c0)]) *
-        *reinterpret_cast<const f32x4 *>(&t.beta[c0]);
-    b = *reinterpret_cast<const f32x4 *>(&t.X[square_at(token, c0 + 4)]) *
-        *reinterpret_cast<const f32x4 *>(&t.beta[c0 + 4]);
+    a = *reinterpret_cast<const f32x4 *>(&t.X[square_at(token, c)]) *
+        *reinterpret_cast<const f32x4 *>(&t.beta[c]);
+    b = *reinterpret_cast<const f32x4 *>(&t.X[square_at(token, d)]) *
+        *reinterpret_cast<const f32x4 *>(&t.beta[d]);
 }
 
-__device__ __forceinline__ void p_piece(const DeltaTokens &t, int token, int s, int g, f32x4 &a,
+__device__ __forceinline__ void p_piece(const DeltaTokens &t, int token, int c, int d, f32x4 &a,
                                         f32x4 &b) {
-    const int c0 = 32 * s + 8 * g;
-    a = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, c0)]);
-    b = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, c0 + 4)]);
+    a = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, c)]);
+    b = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, d)]);
 }
 
 }  // namespace bole

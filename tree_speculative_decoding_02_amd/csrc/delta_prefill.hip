@@ -77,12 +77,12 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs<T
         if (sb > (wave >> 1)) continue;
         const int f = piece_of(wave, sb);
         f32x4 x, y;
-        x_piece(t, tile_token(wave, col), sb, g, x, y);
+        x_piece(t, tile_token(wave, col), 32 * sb + 8 * g, 32 * sb + 8 * g + 4, x, y);
         bf16x8 xt[3];
         split_terms8<3>(x, y, xt);
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8 *>(&w.x[i][f][lane][0]) = xt[i];
-        p_piece(t, tile_token(wave, col), sb, g, x, y);
+        p_piece(t, tile_token(wave, col), 32 * sb + 8 * g, 32 * sb + 8 * g + 4, x, y);
         constexpr int NP = ChunkSystem<TF>::kP;
         bf16x8 p[NP];
         split_terms8<NP>(x, y, p);

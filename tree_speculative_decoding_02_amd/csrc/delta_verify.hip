@@ -109,10 +109,17 @@ __global__ __launch_bounds__(256) void delta_verify_generic_kernel(
 // output's own rounding is the one that counts. Row slots past the last node repeat it: their
 // columns of X diag(b) are zero.
 //
+// Row tile m is nodes 16 m .. 16 m + 15; as a right operand, tiles 2s and 2s + 1 hold in lane
+// group g nodes 32 s + 4 g .. + 3 and 32 s + 16 + 4 g .. + 3, and X and P are read to match. The
+// wavefronts' own rows of a bf16 K serve all four through LDS, over A, which the system no longer
+// needs; Q is read again from the caches. (64 trees of 64 nodes, 32 heads, 128 x 128: 90.5 us with
+// both from the caches, 81.2 this way, 80.3 with Q in 16 KB more of LDS; of up to 64 nodes: 58.6,
+// 54.7 and 57.4, as the third form leaves two workgroups a CU instead of three.)
+//
 // NT = 2 (d_v a multiple of 32): lane c of 16 holds columns 2c and 2c + 1, and a state row's 32
 // columns are one 128-byte read.
 template <typename TF, int DK, int NT, bool WHOLE>
-__global__ __launch_bounds__(256, 2) void delta_verify_kernel(
+__global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_kernel(
     const float *__restrict__ H0, const TF *__restrict__ q, const TF *__restrict__ k,
     const TF *__restrict__ v, const float *__restrict__ gate, const float *__restrict__ beta,
     const int32_t *__restrict__ parent, const int32_t *__restrict__ node_offsets,
@@ -121,7 +128,11 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
     typedef TF vvec __attribute__((ext_vector_type(NT)));
     constexpr int KS = DK / 32, NK = Terms<TF>::K, NS = Terms<TF>::S;
     __shared__ DeltaTokens t;
-    const int unit = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    constexpr bool SHARE = sizeof(TF) == 2;
+    __bf16 *const s_k = reinterpret_cast<__bf16 *>(t.A);
+    static_assert(4 * KS * 512 * 2 <= sizeof(t.A), "K over A");
+    const int unit = blockIdx.x, tid = threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, dk = WHOLE ? DK : s.DK;
     const int b = unit / s.H, h = unit - b * s.H, hk = h / (s.H / s.HK);
     const bool first = h == 0 && blockIdx.y == 0 && tid == 0 && tree_status;
@@ -172,8 +183,14 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
     }
     if (n == 0) return;
     delta_system<TF, DK, WHOLE, true>(t, rows, kb, sk, dk, n);
-    // row tile m has tokens of the tree
-    auto used = [&](int m) { return tile_token(m, 0) < n; };
+    if constexpr (SHARE) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            *reinterpret_cast<bf16x8 *>(&s_k[((wave * KS + ks) * 64 + lane) * 8]) = rows.k[ks].x;
+        lds_barrier();
+    }
+    // row tile m has nodes of the tree
+    auto used = [&](int m) { return 16 * m < n; };
     if (!live) return;
     const size_t vc = v0 + c1;
     f32x4 r[4][NT], o[4][NT];
@@ -198,9 +215,13 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if (!used(m)) continue;
-            const size_t row = (size_t)min(tile_token(m, col), n - 1) * sk;
+            const size_t row = (size_t)min(16 * m + col, n - 1) * sk;
             bf16x8 ka[NK], qa[NK];
-            row_part<WHOLE>(kb + row, 4 * ks + g, dk).terms(ka);
+            if constexpr (SHARE) {
+                ka[0] = load16(&s_k[((m * KS + ks) * 64 + lane) * 8]);
+            } else {
+                row_part<WHOLE>(kb + row, 4 * ks + g, dk).terms(ka);
+            }
             row_part<WHOLE>(qb + row, 4 * ks + g, dk).terms(qa);
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
@@ -215,7 +236,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
         if (!used(m)) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = tile_token(m, 4 * g + e);
+            const int i = 16 * m + 4 * g + e;
             const float d = t.start[i];
             const vvec vv = *reinterpret_cast<const vvec *>(v + vc + (size_t)min(i, n - 1) * sv);
 #pragma unroll
@@ -243,8 +264,9 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
             for (int sb = 0; sb <= (m >> 1); ++sb) {
                 f32x4 x, y;
                 bf16x8 a[NS];
-                if (step == 0) x_piece(t, tile_token(m, col), sb, g, x, y);
-                else p_piece(t, tile_token(m, col), sb, g, x, y);
+                const int c = 32 * sb + 4 * g;
+                if (step == 0) x_piece(t, 16 * m + col, c, c + 16, x, y);
+                else p_piece(t, 16 * m + col, c, c + 16, x, y);
                 split_terms8<NS>(x, y, a);
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
@@ -259,7 +281,7 @@ __global__ __launch_bounds__(256, 2) void delta_verify_kernel(
     for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = tile_token(m, 4 * g + e);
+            const int i = 16 * m + 4 * g + e;
             vvec y;
 #pragma unroll
             for (int c = 0; c < NT; ++c) y[c] = (TF)o[m][c][e];
