@@ -583,8 +583,8 @@ BOLE_API bole_status_t bole_delta_commit_path(float *H0, const void *k, const vo
  *              row of the call sees are not used and may hold anything
  *   cache_len  int32 [B]
  * The softmax's statistics and sums are fp32; bf16 weights are rounded to bf16 before
- * their product with v, as v is. A NaN or an infinity in a key or value that a row does not
- * see does not reach that row.
+ * their product with v, as v is. Keys and values that no row of a sequence sees may hold
+ * anything; a NaN or an infinity in a value that some row of it sees may reach its other rows.
  *
  * Offsets have to be ordered and inside [0, T]: if any are not, every sequence is reported
  * BOLE_TREE_BAD_SIZE and nothing is written. A tree of more than 64 nodes is reported

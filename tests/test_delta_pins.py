@@ -110,6 +110,21 @@ def test_check_dims_takes_valid():
     assert L.bole_delta_check_dims(None, 0) == bole.BOLE_ERR_INVALID_VALUE
 
 
+def test_check_dims_keeps_launches_below_2_to_the_32_threads():
+    # 128 columns: 1024 threads a state, 4096 for prompts, and 256 a chunk of a prompt; one
+    # column: 256 a state, 512
+    L = bole.lib
+    L_ok = lambda op, **kw: L.bole_delta_check_dims(ctypes.byref(dims(heads=32, key_heads=32, **kw)), op)
+    for op, d_v, units in ((0, 128, 1 << 20), (1, 128, 1 << 22), (2, 128, 1 << 22), (3, 128, 1 << 22),
+                           (1, 1, 1 << 24), (2, 1, 1 << 24), (0, 1, 1 << 23)):
+        for batch, want in ((units // 32, bole.BOLE_ERR_UNSUPPORTED), (units // 32 - 1, bole.BOLE_OK)):
+            T = batch if op == 1 else 0
+            assert L_ok(op, batch=batch, d_v=d_v, total_tokens=T) == want, (op, d_v, batch)
+    assert L_ok(0, batch=1, total_tokens=(1 << 25) - 64) == bole.BOLE_ERR_UNSUPPORTED
+    assert L_ok(0, batch=1, total_tokens=(1 << 25) - 65) == bole.BOLE_OK
+    assert L_ok(2, batch=0x7fffffff, d_v=256) == bole.BOLE_ERR_UNSUPPORTED
+
+
 def test_null_pointers_refused_before_any_launch():
     L = bole.lib
     d, bad = ctypes.byref(dims()), bole.BOLE_ERR_INVALID_VALUE

@@ -84,6 +84,22 @@ def test_check_dims_refuses(field, value, want):
     assert bole.lib.bole_window_check_dims(ctypes.byref(dims(**{field: value}))) == want
 
 
+def test_check_dims_keeps_positions_and_launches_in_32_bits():
+    # a key list is walked up to eight tiles of 64 keys past its end before the end stops it
+    L = bole.lib
+    check = lambda **kw: L.bole_window_check_dims(ctypes.byref(dims(**kw)))
+    big = dict(total_rows=0, page_size=1024, window=0x7fffffff, sinks=0x7fffffff)
+    assert check(max_pages=(1 << 21) - 1, **big) == bole.BOLE_OK
+    assert check(max_pages=1 << 21, **big) == bole.BOLE_ERR_UNSUPPORTED
+    assert check(max_pages=(1 << 21) - 1, **{**big, "total_rows": 1}) == bole.BOLE_ERR_UNSUPPORTED
+    # 64 threads a row, 256 for each 64 packed rows and for three workgroups a sequence
+    few = dict(max_pages=0, num_pages=0, heads=1, kv_heads=1)
+    assert check(batch=1, total_rows=(1 << 26) - 1, **few) == bole.BOLE_OK
+    assert check(batch=1, total_rows=1 << 26, **few) == bole.BOLE_ERR_UNSUPPORTED
+    assert check(batch=(1 << 24) // 3, total_rows=0, **few) == bole.BOLE_OK
+    assert check(batch=(1 << 24) // 3 + 1, total_rows=0, **few) == bole.BOLE_ERR_UNSUPPORTED
+
+
 def test_check_dims_takes_valid_and_null_pointers_are_refused():
     L, bad, P = bole.lib, bole.BOLE_ERR_INVALID_VALUE, 0x1000
     assert L.bole_window_check_dims(ctypes.byref(dims())) == bole.BOLE_OK

@@ -29,11 +29,12 @@ bole_status_t bole_delta_check_dims(const bole_delta_dims_t *d, int32_t op) {
     if (op == kOpStep && d->total_tokens != d->batch) return BOLE_ERR_INVALID_VALUE;
     if (d->d_k > 256 || d->d_v > 256) return BOLE_ERR_UNSUPPORTED;
     if (op == kOpCommit && d->max_path > bole::kMaxTreeNodesHost) return BOLE_ERR_UNSUPPORTED;
-    // workgroups are numbered in 31 bits: up to 32 a unit (one per 8 columns), or one per
-    // 64 tokens and value head
-    if ((int64_t)d->batch * d->heads > (0x7fffffffLL >> 5) ||
-        ((int64_t)d->total_tokens / 64 + d->batch) * d->heads > 0x7fffffffLL)
-        return BOLE_ERR_UNSUPPORTED;
+    // A launch has fewer than 2^32 threads: of a state, 64 for each 8 of its columns and 256 or
+    // more (prompts: 512 for each 16); of a prompt's 64 tokens and value head, 256.
+    const int64_t units = (int64_t)d->batch * d->heads, most = 1LL << 32;
+    const int64_t chunks = op == kOpPrefill ? ((int64_t)d->total_tokens / 64 + d->batch) * d->heads : 0;
+    const int64_t each = op == kOpPrefill ? (d->d_v + 15) / 16 * 512 : d->d_v <= 32 ? 256 : (d->d_v + 7) / 8 * 64;
+    if (units + 8 > most / each || chunks >= most / 256) return BOLE_ERR_UNSUPPORTED;
     return BOLE_OK;
 }
 

@@ -19,9 +19,13 @@ bole_status_t bole_window_check_dims(const bole_window_dims_t *d) {
     if (d->dtype != BOLE_DTYPE_BF16 && d->dtype != BOLE_DTYPE_F32) return BOLE_ERR_INVALID_VALUE;
     if (d->flags & ~BOLE_FLAG_FORCE_GENERIC) return BOLE_ERR_INVALID_VALUE;
     if (d->head_dim > 256 || d->page_size > 1024 || d->heads > 65535) return BOLE_ERR_UNSUPPORTED;
-    // positions, and (sequences + rows) x heads, fit 31 bits
-    if ((int64_t)d->max_pages * d->page_size + d->total_rows > 0x7fffffffLL ||
-        ((int64_t)d->total_rows + d->batch) * d->heads > 0x7fffffffLL)
+    // Positions, those of the next few key tiles behind the last among them, and (sequences +
+    // rows) x heads fit 31 bits, and a launch has fewer than 2^32 threads: 64 a row, or 256 for
+    // each 64 rows a key head packs and up to three times a sequence (of few rows).
+    const int64_t rows = d->total_rows, batch = d->batch;
+    if ((int64_t)d->max_pages * d->page_size + rows > (1LL << 31) - 1024 ||
+        (rows + batch) * d->heads > 0x7fffffffLL || rows >= 1LL << 26 ||
+        rows * d->heads / 64 + 3 * batch * d->kv_heads >= 1LL << 24)
         return BOLE_ERR_UNSUPPORTED;
     return BOLE_OK;
 }
