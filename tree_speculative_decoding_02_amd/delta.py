@@ -5,7 +5,10 @@ Tensors: H0 float32 [B, H, d_k, d_v] (prefill, step and commit update it in plac
 [T, H_k, d_k], v [T, H, d_v] (bfloat16 or float32; H_k divides H), gate and beta float32
 [T, H], out [T, H, d_v] in the factors' type. All are contiguous and on H0's GPU. With
 stream=None a call goes to the stream that is current on that GPU when it is made; a bound
-call looks it up each time it is called.
+call looks it up each time it is called. A workspace that a bound call made for itself belongs
+to `stream`, or to the one that was current when it was bound: as with any tensor, calls on
+another stream have to be ordered behind that one, and ahead of it before the bound call is
+dropped.
 """
 import contextlib
 import ctypes
@@ -161,8 +164,9 @@ def bole_delta_prefill(H0, q, k, v, gate, beta, seq_offsets, out=None, workspace
 def bind_delta_prefill(H0, q, k, v, gate, beta, seq_offsets, out, workspace=None, seq_status=None,
                        stream=None, force_generic=False):
     """Same checks as bole_delta_prefill, done once; the bound call keeps its workspace."""
-    _, args, keep = _prefill_call(H0, q, k, v, gate, beta, seq_offsets, out, workspace, seq_status,
-                                  force_generic)
+    with _allocating_on(stream):
+        _, args, keep = _prefill_call(H0, q, k, v, gate, beta, seq_offsets, out, workspace,
+                                      seq_status, force_generic)
     return _BoundCall(lib.bole_delta_prefill, "bole_delta_prefill", args, H0.device, stream, keep)
 
 

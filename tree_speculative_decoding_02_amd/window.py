@@ -98,7 +98,9 @@ def bind_window_attention(q, k, v, k_cache, v_cache, page_table, cache_len, node
                           sinks, out, parent=None, scale=None, workspace=None, seq_status=None,
                           stream=None, force_generic=False):
     """Same checks as bole_window_attention, done once; the bound call keeps its workspace."""
-    _, args, keep = _call(q, k, v, k_cache, v_cache, page_table, cache_len, node_offsets, window,
-                          sinks, out, parent, scale, workspace, seq_status, force_generic)
+    with _allocating_on(stream):
+        _, args, keep = _call(q, k, v, k_cache, v_cache, page_table, cache_len, node_offsets,
+                              window, sinks, out, parent, scale, workspace, seq_status,
+                              force_generic)
     return _BoundCall(lib.bole_window_attention, "bole_window_attention", args, q.device, stream,
                       keep)
