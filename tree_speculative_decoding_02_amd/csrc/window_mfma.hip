@@ -133,81 +133,81 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     if (first < last) {
         stage(0);
         lds_barrier();
-    // (a do loop, entered only from here: a loop that could also be reached around these loads
-    // would have to wait for every load in flight in each of its turns)
-    int tile = first;
-    do {
-        const int buf = (tile - first) & 1;
-        if (tile + 1 < last) {
-            fetch(tile + 1);
-            page = key_page(s, table, t, (tile + 2) * kKeys + lane);
-        }
-        const int x0 = tile * kKeys;
-        if (busy) {
-        f32x16 z[2];
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            z[sub] = (f32x16)0.f;
-            const __bf16 *kp = &s_k[buf][(sub * 32 + col) * KP + 8 * hh];
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                z[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load16(kp + 16 * ks), qf[ks], z[sub],
-                                                                 0, 0, 0);
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) z[sub] *= c2;
-        if (!tile_open(t, tree, x0)) {
-            const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * hh);
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    z[sub][r] = ((uint32_t)(seen >> (32 * sub)) >> (8 * (r >> 2) + (r & 3))) & 1u
-                                    ? z[sub][r] : -INFINITY;
-        }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, z[sub][r]);
-        top = max32(top);
-        const float next = fmaxf(m, top);
-        // nothing seen so far: keep every exponential at 0
-        const float base = next == -INFINITY ? 0.f : next;
-        if (__any(next > m)) {
-            const float keep = __builtin_amdgcn_exp2f(m - base);
-            l *= keep;
-#pragma unroll
-            for (int dt = 0; dt < D / 32; ++dt) acc[dt] *= keep;
-            m = next;
-        }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                z[sub][r] = __builtin_amdgcn_exp2f(z[sub][r] - base);
-                l += z[sub][r];
+        // (a do loop, entered only from here: a loop that could also be reached around these loads
+        // would have to wait for every load in flight in each of its turns)
+        int tile = first;
+        do {
+            const int buf = (tile - first) & 1;
+            if (tile + 1 < last) {
+                fetch(tile + 1);
+                page = key_page(s, table, t, (tile + 2) * kKeys + lane);
             }
-        const int sl = lane & 15;
-        const __bf16 *vp = &s_v[buf][(4 * hh + (sl >> 2)) * VP + ((lane >> 4) & 1) * 16 + (sl & 3) * 4];
+            const int x0 = tile * kKeys;
+            if (busy) {
+                f32x16 z[2];
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
+                for (int sub = 0; sub < 2; ++sub) {
+                    z[sub] = (f32x16)0.f;
+                    const __bf16 *kp = &s_k[buf][(sub * 32 + col) * KP + 8 * hh];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 p;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = (__bf16)z[sub][8 * kk + j];
-                const __bf16 *v0 = vp + (sub * 32 + kk * 16) * VP;
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) {
-                    const bf16x8 v = join(read_transposed(v0 + dt * 32), read_transposed(v0 + 8 * VP + dt * 32));
-                    acc[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, acc[dt], 0, 0, 0);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        z[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load16(kp + 16 * ks), qf[ks], z[sub],
+                                                                         0, 0, 0);
                 }
+                float top = -INFINITY;
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) z[sub] *= c2;
+                if (!tile_open(t, tree, x0)) {
+                    const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * hh);
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            z[sub][r] = ((uint32_t)(seen >> (32 * sub)) >> (8 * (r >> 2) + (r & 3))) & 1u
+                                            ? z[sub][r] : -INFINITY;
+                }
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) top = fmaxf(top, z[sub][r]);
+                top = max32(top);
+                const float next = fmaxf(m, top);
+                // nothing seen so far: keep every exponential at 0
+                const float base = next == -INFINITY ? 0.f : next;
+                if (__any(next > m)) {
+                    const float keep = __builtin_amdgcn_exp2f(m - base);
+                    l *= keep;
+#pragma unroll
+                    for (int dt = 0; dt < D / 32; ++dt) acc[dt] *= keep;
+                    m = next;
+                }
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        z[sub][r] = __builtin_amdgcn_exp2f(z[sub][r] - base);
+                        l += z[sub][r];
+                    }
+                const int sl = lane & 15;
+                const __bf16 *vp = &s_v[buf][(4 * hh + (sl >> 2)) * VP + ((lane >> 4) & 1) * 16 + (sl & 3) * 4];
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        bf16x8 p;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) p[j] = (__bf16)z[sub][8 * kk + j];
+                        const __bf16 *v0 = vp + (sub * 32 + kk * 16) * VP;
+#pragma unroll
+                        for (int dt = 0; dt < D / 32; ++dt) {
+                            const bf16x8 v = join(read_transposed(v0 + dt * 32), read_transposed(v0 + 8 * VP + dt * 32));
+                            acc[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, acc[dt], 0, 0, 0);
+                        }
+                    }
             }
-        }
-        if (tile + 1 < last) stage(buf ^ 1);
-        lds_barrier();
-    } while (++tile < last);
+            if (tile + 1 < last) stage(buf ^ 1);
+            lds_barrier();
+        } while (++tile < last);
     }
     l = sum32(l);
     if (!live) return;
@@ -334,74 +334,74 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
         return;
     }
     if (first < last) {
-    int tile = first;
-    do {
-        const int x0 = tile * kKeys;
-        f32x4 z[4];
+        int tile = first;
+        do {
+            const int x0 = tile * kKeys;
+            f32x4 z[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            z[r] = (f32x4)0.f;
+            for (int r = 0; r < 4; ++r) {
+                z[r] = (f32x4)0.f;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) z[r] = mfma16_bf16(kf[r][ks], qf[ks], z[r]);
-        }
+                for (int ks = 0; ks < D / 32; ++ks) z[r] = mfma16_bf16(kf[r][ks], qf[ks], z[r]);
+            }
 #pragma unroll
-        for (int j = 0; j < VPER; ++j) {
-            const int e = lane + 64 * j;
-            *reinterpret_cast<bf16x8 *>(s_v + (e / CH) * VP + 8 * (e % CH)) = vr[j];
-        }
-        if (tile + 4 < last) {
-            fetch(tile + 4);
-            page = key_page(s, table, t, (tile + 8) * kKeys + lane);
-        }
-        float top = -INFINITY;
+            for (int j = 0; j < VPER; ++j) {
+                const int e = lane + 64 * j;
+                *reinterpret_cast<bf16x8 *>(s_v + (e / CH) * VP + 8 * (e % CH)) = vr[j];
+            }
+            if (tile + 4 < last) {
+                fetch(tile + 4);
+                page = key_page(s, table, t, (tile + 8) * kKeys + lane);
+            }
+            float top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z[r] *= c2;
-        if (!tile_open(t, tree, x0)) {
-            const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * g);
+            for (int r = 0; r < 4; ++r) z[r] *= c2;
+            if (!tile_open(t, tree, x0)) {
+                const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[r][e] = ((uint32_t)(seen >> (32 * (r >> 1))) >> (16 * (r & 1) + e)) & 1u ? z[r][e]
+                                                                                                : -INFINITY;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    z[r][e] = ((uint32_t)(seen >> (32 * (r >> 1))) >> (16 * (r & 1) + e)) & 1u ? z[r][e]
-                                                                                            : -INFINITY;
-        }
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, z[r][e]);
+            top = max16(top);
+            top = max32(top);
+            const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
+            const float keep = __builtin_amdgcn_exp2f(m - base);
+            m = next;
+            l *= keep;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int dt = 0; dt < D / 16; ++dt) acc[dt] *= keep;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, z[r][e]);
-        top = max16(top);
-        top = max32(top);
-        const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
-        const float keep = __builtin_amdgcn_exp2f(m - base);
-        m = next;
-        l *= keep;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) acc[dt] *= keep;
+                for (int e = 0; e < 4; ++e) {
+                    z[r][e] = __builtin_amdgcn_exp2f(z[r][e] - base);
+                    l += z[r][e];
+                }
+            asm volatile("" ::: "memory");  // the wavefront's own stores to s_v come first
+            const __bf16 *vp = s_v + (4 * g + (col >> 2)) * VP + (col & 3) * 4;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int half = 0; half < 2; ++half) {
+                bf16x8 p;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z[r][e] = __builtin_amdgcn_exp2f(z[r][e] - base);
-                l += z[r][e];
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = (__bf16)z[2 * half][e];
+                    p[4 + e] = (__bf16)z[2 * half + 1][e];
+                }
+                const __bf16 *v0 = vp + half * 32 * VP;
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt)
+                    acc[dt] = mfma16_bf16(join(read_transposed(v0 + dt * 16), read_transposed(v0 + 16 * VP + dt * 16)),
+                                          p, acc[dt]);
             }
-        asm volatile("" ::: "memory");  // the wavefront's own stores to s_v come first
-        const __bf16 *vp = s_v + (4 * g + (col >> 2)) * VP + (col & 3) * 4;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            bf16x8 p;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[e] = (__bf16)z[2 * half][e];
-                p[4 + e] = (__bf16)z[2 * half + 1][e];
-            }
-            const __bf16 *v0 = vp + half * 32 * VP;
-#pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt)
-                acc[dt] = mfma16_bf16(join(read_transposed(v0 + dt * 16), read_transposed(v0 + 16 * VP + dt * 16)),
-                                      p, acc[dt]);
-        }
-        asm volatile("" ::: "memory");
-    } while ((tile += 4) < last);
+            asm volatile("" ::: "memory");
+        } while ((tile += 4) < last);
     }
     l = sum16(l);
     l = sum32(l);
