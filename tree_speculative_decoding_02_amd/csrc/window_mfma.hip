@@ -8,11 +8,11 @@
 // permutation of the keys within a product, the same for both operands). V^T comes from
 // row-major LDS through the transposing read.
 //
-// The keys a tile of rows can see are one virtual list: the cached first tokens, the cached
-// window behind the tile's first row, the call's own first tokens, the call's own rows. Tiles
-// of 64 keys that every row sees are taken without tests; the others test each key. Slots
-// past the end repeat the last key, so nothing that no row of the sequence sees is read, and
-// no load depends on a branch.
+// The keys a tile of rows can see are one virtual list: the cached first tokens and the cached
+// window behind the tile's first row, then, on a key tile's edge, the call's own first tokens and
+// own rows. Tiles of 64 keys that every row sees are taken without tests; the others test each
+// key. Slots past the end of either part repeat its last key, so nothing that no row of the
+// sequence sees is read, and no load depends on a branch.
 //
 // Two shapes of workgroup:
 //  - rows: 128 rows, 32 a wavefront, keys and values staged in LDS for all four wavefronts
@@ -40,6 +40,30 @@ template <int D> struct Pad {
     static constexpr int V = D == 128 ? 160 : 96;
 };
 
+// The factor of q . k in the exponent, positive, so that the largest product is the largest score:
+// a scale's sign goes to the query (and a scale of 0 makes it 0).
+template <int N>
+__device__ __forceinline__ float query_scale(float scale, bf16x8 (&q)[N]) {
+    if (scale > 0.f) return scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = scale < 0.f ? -q[i] : q[i] * (__bf16)0.f;
+    return scale < 0.f ? -scale * kLog2e : 1.f;
+}
+
+// Exponentials are taken from a reference m, which moves to the row's largest score so far once
+// that is 8 above it: until then they stay below 2^8, which costs neither their bf16 roundings
+// nor the fp32 sums anything, and most tiles do not touch the accumulators.
+template <typename A, int N>
+__device__ __forceinline__ void move_reference(float top, float &m, float &l, A (&acc)[N]) {
+    const float next = fmaxf(m, top);
+    if (!__any(next > m + 8.f)) return;
+    const float keep = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.f : next));
+    l *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] *= keep;
+    m = next;
+}
+
 template <int D>
 __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a, const WindowParts parts,
                                                              int slots) {
@@ -47,8 +71,8 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     __shared__ __align__(16) __bf16 s_k[2][kKeys * KP];
     __shared__ __align__(16) __bf16 s_v[2][kKeys * VP];
     const WindowShape &s = a.s;
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, G = s.H / s.HK;
-    const int hk = blockIdx.x % s.HK, slot = blockIdx.x / s.HK, part = blockIdx.y;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6), G = s.H / s.HK;
+    const int slot = uniform(blockIdx.x / s.HK), hk = blockIdx.x - slot * s.HK, part = blockIdx.y;
     const bool tree = a.parent != nullptr;
     RowTile t;
     uint64_t node_mask = 0;
@@ -88,21 +112,20 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     }
     const int32_t *table = a.page_table + (size_t)t.b * s.max_pages;
     const int tiles = (t.total + kKeys - 1) / kKeys;
-    const int first = (int)((int64_t)tiles * part / parts.n);
-    const int last = (int)((int64_t)tiles * (part + 1) / parts.n);
+    const int first = part_edge(tiles, part, parts.n), last = part_edge(tiles, part + 1, parts.n);
 
     // lane x holds the page (one tile ahead of the loads) and then the row of the tile's key x
     int page = -1;
     bf16x8 kr[PER], vr[PER];
     auto fetch = [&](int tile) {
-        const uint32_t mine = key_row(s, t, hk, min(tile * kKeys + lane, t.total - 1), page);
+        const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
+        const KeySide side = key_side(a, t, tile * kKeys);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = tid + 256 * j, x = min(tile * kKeys + e / CH, t.total - 1), c = e % CH;
-            const size_t off = (size_t)(uint32_t)__shfl((int)mine, e / CH, 64) * D + 8 * c;
-            const bool own = x >= t.n1 + t.n2;
-            kr[j] = load16(static_cast<const __bf16 *>(own ? a.k : a.k_cache) + off);
-            vr[j] = load16(static_cast<const __bf16 *>(own ? a.v : a.v_cache) + off);
+            const int e = tid + 256 * j;
+            const size_t off = (size_t)lane_value(mine, e / CH) * D + 8 * (e % CH);
+            kr[j] = load16(static_cast<const __bf16 *>(side.k) + off);
+            vr[j] = load16(static_cast<const __bf16 *>(side.v) + off);
         }
     };
     auto stage = [&](int buf) {
@@ -116,13 +139,13 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     f32x16 acc[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) acc[dt] = (f32x16)0.f;
-    float m = -INFINITY, l = 0.f;
-    const float c2 = s.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;  // the exponentials' reference, and their sum
+    const float c2 = query_scale(s.scale, qf);
     const bool busy = t.tile * kRowTile + wave * 32 < t.n * G;  // else it only stages
     if (first < last) {
-        page = key_page(s, table, t, first * kKeys + lane);
+        page = key_page(s, table, t, first * kKeys);
         fetch(first);
-        page = key_page(s, table, t, (first + 1) * kKeys + lane);
+        page = key_page(s, table, t, (first + 1) * kKeys);
     }
     t.status = pages_status(a, t.b, t.len);
     if (report) a.status[t.b] = t.status;
@@ -140,7 +163,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
             const int buf = (tile - first) & 1;
             if (tile + 1 < last) {
                 fetch(tile + 1);
-                page = key_page(s, table, t, (tile + 2) * kKeys + lane);
+                page = key_page(s, table, t, (tile + 2) * kKeys);
             }
             const int x0 = tile * kKeys;
             if (busy) {
@@ -155,8 +178,6 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                                                                          0, 0, 0);
                 }
                 float top = -INFINITY;
-#pragma unroll
-                for (int sub = 0; sub < 2; ++sub) z[sub] *= c2;
                 if (!tile_open(t, tree, x0)) {
                     const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * hh);
 #pragma unroll
@@ -171,21 +192,13 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
 #pragma unroll
                     for (int r = 0; r < 16; ++r) top = fmaxf(top, z[sub][r]);
                 top = max32(top);
-                const float next = fmaxf(m, top);
-                // nothing seen so far: keep every exponential at 0
-                const float base = next == -INFINITY ? 0.f : next;
-                if (__any(next > m)) {
-                    const float keep = __builtin_amdgcn_exp2f(m - base);
-                    l *= keep;
-#pragma unroll
-                    for (int dt = 0; dt < D / 32; ++dt) acc[dt] *= keep;
-                    m = next;
-                }
+                move_reference(top * c2, m, l, acc);
+                const float base = m == -INFINITY ? 0.f : m;  // (nothing seen: exponentials of 0)
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        z[sub][r] = __builtin_amdgcn_exp2f(z[sub][r] - base);
+                        z[sub][r] = __builtin_amdgcn_exp2f(fmaf(z[sub][r], c2, -base));
                         l += z[sub][r];
                     }
                 const int sl = lane & 15;
@@ -246,8 +259,8 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
     __shared__ __align__(16) char s_mem[4 * kKeys * VP * 2];
     float(*s_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(s_mem + JOIN);
     const WindowShape &s = a.s;
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, G = s.H / s.HK;
-    const int hk = blockIdx.x % s.HK, slot = blockIdx.x / s.HK, part = blockIdx.y;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6), G = s.H / s.HK;
+    const int slot = uniform(blockIdx.x / s.HK), hk = blockIdx.x - slot * s.HK, part = blockIdx.y;
     const bool tree = a.parent != nullptr;
     RowTile t;
     uint64_t node_mask = 0;
@@ -291,8 +304,7 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
     }
     const int32_t *table = a.page_table + (size_t)t.b * s.max_pages;
     const int tiles = (t.total + kKeys - 1) / kKeys;
-    const int first = (int)((int64_t)tiles * part / parts.n) + wave;
-    const int last = (int)((int64_t)tiles * (part + 1) / parts.n);
+    const int first = part_edge(tiles, part, parts.n) + wave, last = part_edge(tiles, part + 1, parts.n);
     __bf16 *s_v = reinterpret_cast<__bf16 *>(s_mem) + wave * kKeys * VP;
 
     // a lane's keys: for K, key 16 r + col of the tile (r = 0..3), 16-byte pieces 4 ks + g; for
@@ -300,32 +312,31 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
     bf16x8 kf[4][D / 32], vr[VPER];
     int page = -1;
     auto fetch = [&](int tile) {
-        const int x0 = tile * kKeys, cached = t.n1 + t.n2;
-        const uint32_t mine = key_row(s, t, hk, min(x0 + lane, t.total - 1), page);
+        const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
+        const KeySide side = key_side(a, t, tile * kKeys);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int x = min(x0 + 16 * r + col, t.total - 1);
-            const size_t off = (size_t)(uint32_t)__shfl((int)mine, 16 * r + col, 64) * D + 8 * g;
-            const __bf16 *p = static_cast<const __bf16 *>(x >= cached ? a.k : a.k_cache) + off;
+            const __bf16 *p = static_cast<const __bf16 *>(side.k) +
+                              ((size_t)lane_value(mine, 16 * r + col) * D + 8 * g);
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks) kf[r][ks] = load16(p + 32 * ks);
         }
 #pragma unroll
         for (int j = 0; j < VPER; ++j) {
-            const int e = lane + 64 * j, x = min(x0 + e / CH, t.total - 1);
-            const size_t off = (size_t)(uint32_t)__shfl((int)mine, e / CH, 64) * D + 8 * (e % CH);
-            vr[j] = load16(static_cast<const __bf16 *>(x >= cached ? a.v : a.v_cache) + off);
+            const int e = lane + 64 * j;
+            vr[j] = load16(static_cast<const __bf16 *>(side.v) +
+                           ((size_t)lane_value(mine, e / CH) * D + 8 * (e % CH)));
         }
     };
     f32x4 acc[D / 16];
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) acc[dt] = (f32x4)0.f;
-    float m = -INFINITY, l = 0.f;
-    const float c2 = s.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;  // the exponentials' reference, and their sum
+    const float c2 = query_scale(s.scale, qf);
     if (first < last) {
-        page = key_page(s, table, t, first * kKeys + lane);
+        page = key_page(s, table, t, first * kKeys);
         fetch(first);
-        page = key_page(s, table, t, (first + 4) * kKeys + lane);
+        page = key_page(s, table, t, (first + 4) * kKeys);
     }
     t.status = pages_status(a, t.b, t.len);
     if (report) a.status[t.b] = t.status;
@@ -351,11 +362,9 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
             }
             if (tile + 4 < last) {
                 fetch(tile + 4);
-                page = key_page(s, table, t, (tile + 8) * kKeys + lane);
+                page = key_page(s, table, t, (tile + 8) * kKeys);
             }
             float top = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) z[r] *= c2;
             if (!tile_open(t, tree, x0)) {
                 const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * g);
 #pragma unroll
@@ -371,17 +380,13 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, z[r][e]);
             top = max16(top);
             top = max32(top);
-            const float next = fmaxf(m, top), base = next == -INFINITY ? 0.f : next;
-            const float keep = __builtin_amdgcn_exp2f(m - base);
-            m = next;
-            l *= keep;
-#pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) acc[dt] *= keep;
+            move_reference(top * c2, m, l, acc);
+            const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[r][e] = __builtin_amdgcn_exp2f(z[r][e] - base);
+                    z[r][e] = __builtin_amdgcn_exp2f(fmaf(z[r][e], c2, -base));
                     l += z[r][e];
                 }
             asm volatile("" ::: "memory");  // the wavefront's own stores to s_v come first

@@ -24,8 +24,8 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
     __shared__ __align__(16) float s_k[kKeys * ST];
     __shared__ __align__(16) float s_v[kKeys * ST];
     const WindowShape &s = a.s;
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, G = s.H / s.HK;
-    const int hk = blockIdx.x % s.HK, slot = blockIdx.x / s.HK, part = blockIdx.y;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6), G = s.H / s.HK;
+    const int slot = uniform(blockIdx.x / s.HK), hk = blockIdx.x - slot * s.HK, part = blockIdx.y;
     const bool tree = a.parent != nullptr;
     RowTile t;
     uint64_t node_mask = 0;
@@ -64,20 +64,19 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
     }
     const int32_t *table = a.page_table + (size_t)t.b * s.max_pages;
     const int tiles = (t.total + kKeys - 1) / kKeys;
-    const int first = (int)((int64_t)tiles * part / parts.n);
-    const int last = (int)((int64_t)tiles * (part + 1) / parts.n);
+    const int first = part_edge(tiles, part, parts.n), last = part_edge(tiles, part + 1, parts.n);
 
     int page = 0;
     f32x4 kr[PER], vr[PER];
     auto fetch = [&](int tile) {
-        const uint32_t mine = key_row(s, t, hk, min(tile * kKeys + lane, t.total - 1), page);
+        const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
+        const KeySide side = key_side(a, t, tile * kKeys);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = tid + 256 * j, x = min(tile * kKeys + e / CH, t.total - 1), c = e % CH;
-            const size_t off = (size_t)(uint32_t)__shfl((int)mine, e / CH, 64) * D + 4 * c;
-            const bool own = x >= t.n1 + t.n2;
-            kr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(own ? a.k : a.k_cache) + off);
-            vr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(own ? a.v : a.v_cache) + off);
+            const int e = tid + 256 * j;
+            const size_t off = (size_t)lane_value(mine, e / CH) * D + 4 * (e % CH);
+            kr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(side.k) + off);
+            vr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(side.v) + off);
         }
     };
     auto stage = [&]() {
@@ -95,9 +94,9 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
     const float c2 = s.scale * kLog2e;
     const bool busy = t.tile * kF32Tile + wave * 16 < t.n * G;  // else it only stages
     if (first < last) {
-        page = key_page(s, table, t, first * kKeys + lane);
+        page = key_page(s, table, t, first * kKeys);
         fetch(first);
-        page = key_page(s, table, t, (first + 1) * kKeys + lane);
+        page = key_page(s, table, t, (first + 1) * kKeys);
     }
     t.status = pages_status(a, t.b, t.len);
     if (report) a.status[t.b] = t.status;
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
             lds_barrier();
             if (tile + 1 < last) {
                 fetch(tile + 1);
-                page = key_page(s, table, t, (tile + 2) * kKeys + lane);
+                page = key_page(s, table, t, (tile + 2) * kKeys);
             }
             if (!busy) continue;
             const int x0 = tile * kKeys;

@@ -31,8 +31,13 @@ struct RowTile {
     int status, len;
     int i0, i1;                      // rows (before packing) of the tile: [i0, i1)
     int n1, n2, n3, n4, w0, o2;      // key list: sinks, window from w0, own sinks, own rows from o2
-    int total, all_from;             // keys; first position every row's window holds
+    int own0, total, all_from;       // first own key (on a tile's edge), keys; first position every
+                                     // row's window holds
 };
+
+// A value that every lane has, as a scalar: divisions end in vector registers, and all that is
+// worked out from them would.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 __device__ __forceinline__ void key_list(const WindowShape &s, bool tree, RowTile &t) {
     const int p0 = tree ? t.len : t.len + t.i0;                      // first and last position
@@ -45,7 +50,8 @@ __device__ __forceinline__ void key_list(const WindowShape &s, bool tree, RowTil
     t.n3 = tree ? 0 : min(max(0, s.sinks - t.len), t.i1);
     t.o2 = tree ? 0 : max(t.n3, edge - t.len);
     t.n4 = tree ? t.n : max(0, t.i1 - t.o2);
-    t.total = t.n1 + t.n2 + t.n3 + t.n4;
+    t.own0 = (t.n1 + t.n2 + kKeys - 1) & ~(kKeys - 1);
+    t.total = t.own0 + t.n3 + t.n4;
 }
 
 // Finds the workgroup's tile and all that is wrong with its sequence but its pages. Every
@@ -67,8 +73,8 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
     t.tile = slot - t.slot0;
     if (t.n == 0 && t.tile == 0 && report && lane == 0 && a.status) a.status[t.b] = BOLE_TREE_OK;
     if (t.tile * MT >= t.n * G) return false;
-    t.i0 = t.tile * MT / G;
-    t.i1 = min(t.n, (t.tile * MT + MT + G - 1) / G);
+    t.i0 = uniform(t.tile * MT / G);
+    t.i1 = min(t.n, uniform((t.tile * MT + MT + G - 1) / G));
     if (a.parent) {
         if (t.n > kMaxTree) {
             t.status = BOLE_TREE_BAD_SIZE;
@@ -93,45 +99,61 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
     return true;
 }
 
+// Where part `part` of `n` of the tiles begins (n <= 64, and fewer than 2^25 tiles).
+__device__ __forceinline__ int part_edge(int tiles, int part, int n) {
+    return uniform((int)((uint32_t)tiles * (uint32_t)part / (uint32_t)n));
+}
+
 __device__ __forceinline__ int cached_position(const RowTile &t, int x) {
     return x < t.n1 ? x : t.w0 + (x - t.n1);
 }
 
 __device__ __forceinline__ int own_row(const RowTile &t, int x) {
-    const int j = x - t.n1 - t.n2;
+    const int j = x - t.own0;
     return j < t.n3 ? j : t.o2 + (j - t.n3);
 }
 
-// Page of key x as the table has it; 0 for the call's own rows.
+// Page of the lane's key of the tile from x0 on, as the table has it; 0 for the call's own rows.
 __device__ __forceinline__ int key_page(const WindowShape &s, const int32_t *__restrict__ table,
-                                        const RowTile &t, int x) {
-    x = min(x, t.total - 1);
-    return x < t.n1 + t.n2 ? table[cached_position(t, x) >> s.page_shift] : 0;
+                                        const RowTile &t, int x0) {
+    if (x0 >= t.own0) return 0;
+    return table[cached_position(t, min(x0 + lane_id(), t.n1 + t.n2 - 1)) >> s.page_shift];
 }
 
-// A page that is not in the cache stands for its last one: the first loads go out before the
-// sequence's pages are known to be valid, and are dropped if they are not.
-// Row (of D elements) of key x: in the cache's [page][head][slot] order, or in the call's k and
-// v. At 128 bytes a row and more, 32 bits number more rows than memory holds.
-__device__ __forceinline__ uint32_t key_row(const WindowShape &s, const RowTile &t, int hk, int x,
+// Row (of D elements) of the lane's key of the tile from x0 on: in the cache's [page][head][slot]
+// order, or in the call's k and v. Slots past the end of either part repeat its last key. A page
+// that is not in the cache stands for its last one: the first loads go out before the sequence's
+// pages are known to be valid, and are dropped if they are not. At 128 bytes a row and more, 32
+// bits number more rows than memory holds.
+__device__ __forceinline__ uint32_t key_row(const WindowShape &s, const RowTile &t, int hk, int x0,
                                             int page) {
-    if (x < t.n1 + t.n2) {
-        const uint32_t slot = cached_position(t, x) & ((1 << s.page_shift) - 1);
-        return ((min((uint32_t)page, (uint32_t)s.pages - 1) * s.HK + hk) << s.page_shift) + slot;
-    }
-    return (uint32_t)(t.lo + own_row(t, x)) * s.HK + hk;
+    const int x = x0 + lane_id();
+    if (x0 >= t.own0) return (uint32_t)(t.lo + own_row(t, min(x, t.total - 1))) * s.HK + hk;
+    const uint32_t slot = cached_position(t, min(x, t.n1 + t.n2 - 1)) & ((1 << s.page_shift) - 1);
+    return ((min((uint32_t)page, (uint32_t)s.pages - 1) * s.HK + hk) << s.page_shift) + slot;
+}
+
+// Where the tile's keys and values are.
+struct KeySide {
+    const void *k, *v;
+};
+__device__ __forceinline__ KeySide key_side(const WindowArgs &a, const RowTile &t, int x0) {
+    return x0 >= t.own0 ? KeySide{a.k, a.v} : KeySide{a.k_cache, a.v_cache};
+}
+
+// Lane `from`'s value of x.
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int from) {
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * from, (int)x);
 }
 
 // Whether every row of the tile sees all 64 keys from x0 on.
 __device__ __forceinline__ bool tile_open(const RowTile &t, bool tree, int x0) {
-    const int x1 = x0 + kKeys, c = t.n1 + t.n2;
-    if (x1 <= t.n1) return true;
-    if (x0 >= t.n1 && x1 <= c) return t.w0 + (x0 - t.n1) >= t.all_from;
-    if (!tree && x0 >= c + t.n3 && x1 <= t.total) {
-        const int j = own_row(t, x0);
-        return j + kKeys - 1 <= t.i0 && t.len + j >= t.all_from;
-    }
-    return false;
+    const int x1 = x0 + kKeys;
+    if (x0 < t.own0)
+        return x1 <= t.n1 || (x0 >= t.n1 && x1 <= t.n1 + t.n2 && t.w0 + (x0 - t.n1) >= t.all_from);
+    if (tree || x0 < t.own0 + t.n3 || x1 > t.total) return false;
+    const int j = own_row(t, x0);
+    return j + kKeys - 1 <= t.i0 && t.len + j >= t.all_from;
 }
 
 __device__ __forceinline__ uint64_t bits_below(int n) {
@@ -142,17 +164,14 @@ __device__ __forceinline__ uint64_t bits_below(int n) {
 // qe on, own nodes qmask for trees. Each part of the list shows it an interval (or the path).
 __device__ __forceinline__ uint64_t seen_keys(const RowTile &t, bool tree, int i, int qe, uint64_t qmask,
                                               int x0) {
-    const int c = t.n1 + t.n2 - x0, from = max(qe, 0);
-    uint64_t m = bits_below(c) & ~bits_below(t.n1 - x0 + max(0, from - t.w0));
-    m |= bits_below(t.n1 - x0);
-    if (tree) {
-        if (c > -64 && c < 64) m |= (c >= 0 ? qmask << c : qmask >> -c) & bits_below(c + t.n4);
-    } else {
-        const int own = c + t.n3;
-        m |= bits_below(c + min(t.n3, i + 1)) & ~bits_below(c);
-        m |= bits_below(own + min(t.n4, i + 1 - t.o2)) & ~bits_below(own + max(0, from - t.len - t.o2));
-    }
-    return m;
+    const int from = max(qe, 0);
+    if (x0 < t.own0)
+        return bits_below(t.n1 - x0) |
+               (bits_below(t.n1 + t.n2 - x0) & ~bits_below(t.n1 - x0 + max(0, from - t.w0)));
+    if (tree) return qmask;  // at most 64 nodes: one tile
+    const int sink = t.own0 - x0, own = sink + t.n3;
+    return (bits_below(sink + min(t.n3, i + 1)) & ~bits_below(sink)) |
+           (bits_below(own + min(t.n4, i + 1 - t.o2)) & ~bits_below(own + max(0, from - t.len - t.o2)));
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
