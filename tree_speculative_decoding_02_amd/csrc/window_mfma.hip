@@ -114,18 +114,25 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     const int tiles = (t.total + kKeys - 1) / kKeys;
     const int first = part_edge(tiles, part, parts.n), last = part_edge(tiles, part + 1, parts.n);
 
-    // lane x holds the page (one tile ahead of the loads) and then the row of the tile's key x
-    int page = -1;
+    // Lane x holds the page and then the row of the tile's key x, `row` the rows that the thread
+    // brings: pages two tiles ahead of the loads, rows one, as each is a trip through memory or LDS.
+    const KeySides<__bf16> sides(a);
+    int page = 0;
+    uint32_t row[PER];
     bf16x8 kr[PER], vr[PER];
-    auto fetch = [&](int tile) {
+    auto find_rows = [&](int tile) {
         const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
-        const KeySide side = key_side(a, t, tile * kKeys);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) row[j] = lane_value(mine, (tid + 256 * j) / CH);
+        page = key_page(s, table, t, (tile + 1) * kKeys);
+    };
+    auto fetch = [&](int tile) {
+        const bool own = tile * kKeys >= t.own0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = tid + 256 * j;
-            const size_t off = (size_t)lane_value(mine, e / CH) * D + 8 * (e % CH);
-            kr[j] = load16(static_cast<const __bf16 *>(side.k) + off);
-            vr[j] = load16(static_cast<const __bf16 *>(side.v) + off);
+            const size_t off = (size_t)row[j] * D + 8 * (tid % CH);
+            kr[j] = sides.k(own, off);
+            vr[j] = sides.v(own, off);
         }
     };
     auto stage = [&](int buf) {
@@ -144,8 +151,9 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     const bool busy = t.tile * kRowTile + wave * 32 < t.n * G;  // else it only stages
     if (first < last) {
         page = key_page(s, table, t, first * kKeys);
+        find_rows(first);
         fetch(first);
-        page = key_page(s, table, t, (first + 1) * kKeys);
+        find_rows(min(first + 1, last - 1));
     }
     t.status = pages_status(a, t.b, t.len);
     if (report) a.status[t.b] = t.status;
@@ -161,10 +169,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         int tile = first;
         do {
             const int buf = (tile - first) & 1;
-            if (tile + 1 < last) {
-                fetch(tile + 1);
-                page = key_page(s, table, t, (tile + 2) * kKeys);
-            }
+            if (tile + 1 < last) fetch(tile + 1);
             const int x0 = tile * kKeys;
             if (busy) {
                 f32x16 z[2];
@@ -218,7 +223,10 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                         }
                     }
             }
-            if (tile + 1 < last) stage(buf ^ 1);
+            if (tile + 1 < last) {
+                stage(buf ^ 1);
+                find_rows(min(tile + 2, last - 1));
+            }
             lds_barrier();
         } while (++tile < last);
     }
@@ -311,21 +319,20 @@ __global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs 
     // V, piece e = lane + 64 j of the tile's kKeys x CH pieces
     bf16x8 kf[4][D / 32], vr[VPER];
     int page = -1;
+    const KeySides<__bf16> sides(a);
     auto fetch = [&](int tile) {
+        const bool own = tile * kKeys >= t.own0;
         const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
-        const KeySide side = key_side(a, t, tile * kKeys);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const __bf16 *p = static_cast<const __bf16 *>(side.k) +
-                              ((size_t)lane_value(mine, 16 * r + col) * D + 8 * g);
+            const size_t off = (size_t)lane_value(mine, 16 * r + col) * D + 8 * g;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) kf[r][ks] = load16(p + 32 * ks);
+            for (int ks = 0; ks < D / 32; ++ks) kf[r][ks] = sides.k(own, off + 32 * ks);
         }
 #pragma unroll
         for (int j = 0; j < VPER; ++j) {
             const int e = lane + 64 * j;
-            vr[j] = load16(static_cast<const __bf16 *>(side.v) +
-                           ((size_t)lane_value(mine, e / CH) * D + 8 * (e % CH)));
+            vr[j] = sides.v(own, (size_t)lane_value(mine, e / CH) * D + 8 * (e % CH));
         }
     };
     f32x4 acc[D / 16];

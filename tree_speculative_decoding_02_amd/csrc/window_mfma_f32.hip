@@ -68,15 +68,16 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
 
     int page = 0;
     f32x4 kr[PER], vr[PER];
+    const KeySides<float> sides(a);
     auto fetch = [&](int tile) {
+        const bool own = tile * kKeys >= t.own0;
         const uint32_t mine = key_row(s, t, hk, tile * kKeys, page);
-        const KeySide side = key_side(a, t, tile * kKeys);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int e = tid + 256 * j;
             const size_t off = (size_t)lane_value(mine, e / CH) * D + 4 * (e % CH);
-            kr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(side.k) + off);
-            vr[j] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(side.v) + off);
+            kr[j] = sides.k(own, off);
+            vr[j] = sides.v(own, off);
         }
     };
     auto stage = [&]() {

@@ -133,13 +133,23 @@ __device__ __forceinline__ uint32_t key_row(const WindowShape &s, const RowTile 
     return ((min((uint32_t)page, (uint32_t)s.pages - 1) * s.HK + hk) << s.page_shift) + slot;
 }
 
-// Where the tile's keys and values are.
-struct KeySide {
-    const void *k, *v;
+// Where a tile's keys and values are: in the call, or in the cache. (The addresses are pinned to
+// registers: the compiler would choose between their places in memory instead, and load one in
+// every tile.) k, v: sixteen bytes at element `off`.
+template <typename T>
+struct KeySides {
+    typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
+    uint64_t k0, v0, k1, v1;
+    __device__ __forceinline__ explicit KeySides(const WindowArgs &a)
+        : k0((uint64_t)a.k_cache), v0((uint64_t)a.v_cache), k1((uint64_t)a.k), v1((uint64_t)a.v) {
+        asm volatile("" : "+s"(k0), "+s"(v0), "+s"(k1), "+s"(v1));
+    }
+    static __device__ __forceinline__ piece load(uint64_t base, size_t off) {
+        return *(const __attribute__((address_space(1))) piece *)(base + off * sizeof(T));
+    }
+    __device__ __forceinline__ piece k(bool own, size_t off) const { return load(own ? k1 : k0, off); }
+    __device__ __forceinline__ piece v(bool own, size_t off) const { return load(own ? v1 : v0, off); }
 };
-__device__ __forceinline__ KeySide key_side(const WindowArgs &a, const RowTile &t, int x0) {
-    return x0 >= t.own0 ? KeySide{a.k, a.v} : KeySide{a.k_cache, a.v_cache};
-}
 
 // Lane `from`'s value of x.
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int from) {
