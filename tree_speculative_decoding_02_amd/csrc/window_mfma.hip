@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
         const bool own = tile * kKeys >= t.own0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const size_t off = (size_t)row[j] * D + 8 * (tid % CH);
+            const size_t off = (size_t)row[j] * D + 8 * ((tid + 256 * j) % CH);
             kr[j] = sides.k(own, off);
             vr[j] = sides.v(own, off);
         }
@@ -182,6 +182,14 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
                         z[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load16(kp + 16 * ks), qf[ks], z[sub],
                                                                          0, 0, 0);
                 }
+                // K's pieces are read four products ahead
+                __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+                for (int k = 0; k < D / 8 - 4; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
                 float top = -INFINITY;
                 if (!tile_open(t, tree, x0)) {
                     const uint64_t seen = seen_keys(t, tree, i, qe, qmask, x0) >> (4 * hh);
