@@ -23,12 +23,16 @@ namespace bole {
 
 constexpr int kChunk = 64;
 
-struct DeltaTokens {           // LDS of one workgroup, 50 KB
-    float A[kChunk * kChunk];  // A, X, P: element (i, j) at square_at(i, j)
-    float X[kChunk * kChunk];
-    float P[kChunk * kChunk];
+struct DeltaTokens {           // LDS of one workgroup, 33 KB
+    float A[kChunk * kChunk];  // A, X: element (i, j) at square_at(i, j)
+    float X[kChunk * kChunk];  // (before there is an X: bf16 rows of K, share_rows)
     float L[kChunk], Lrest[kChunk];      // cumulative log2-decay (fp64) as two fp32 terms
-    float beta[kChunk], start[kChunk];   // strengths, 2^L
+    float beta[kChunk];                  // strengths
+};
+
+struct DeltaTree : DeltaTokens {         // and of a draft tree, 17 KB more
+    float P[kChunk * kChunk];
+    float start[kChunk];                 // 2^L
     uint64_t mask[kChunk];
     int bad;
 };
@@ -132,19 +136,36 @@ __device__ __forceinline__ RowPart<TF> row_part(const TF *p, int c, int dk) {
     return x;
 }
 
-// A wavefront's own rows of k and q (row tile `wave`, tokens 16 wave ..) as operands; rows past
-// the last repeat it. Loaded early, they are in flight while the decays are summed up.
-template <typename TF, int DK, bool WHOLE>
+// Token of row r of row tile m: in order for trees, whose products all meet in LDS; as operands
+// of the next product for chunks.
+template <bool TREE>
+__device__ __forceinline__ int row_of(int m, int r) { return TREE ? 16 * m + r : tile_token(m, r); }
+
+// A wavefront's own rows of k and q (row tile `wave`) as operands; rows past the last repeat it.
+// Loaded early, they are in flight while the decays are summed up.
+template <typename TF, int DK, bool WHOLE, bool TREE>
 struct SystemRows {
+    static constexpr bool kShared = sizeof(TF) == 2;
     RowPart<TF> k[DK / 32], q[DK / 32];
     __device__ __forceinline__ void load(const TF *kp, const TF *qp, size_t stride, int dk, int n) {
-        const int row = 16 * (threadIdx.x >> 6) + (lane_id() & 15), g = lane_id() >> 4;
+        const int row = row_of<TREE>(threadIdx.x >> 6, lane_id() & 15), g = lane_id() >> 4;
         const size_t at = (size_t)min(row, n - 1) * stride;
 #pragma unroll
         for (int ks = 0; ks < DK / 32; ++ks) {
             k[ks] = row_part<WHOLE>(kp + at, 4 * ks + g, dk);
             q[ks] = row_part<WHOLE>(qp + at, 4 * ks + g, dk);
         }
+    }
+    // bf16 rows of K, as operands, to all four wavefronts by way of `to`
+    __device__ __forceinline__ void share(void *to) const {
+        if constexpr (kShared) {
+            const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+#pragma unroll
+            for (int ks = 0; ks < DK / 32; ++ks) *shared(to, wave, ks) = k[ks].x;
+        }
+    }
+    static __device__ __forceinline__ bf16x8 *shared(void *to, int m, int ks) {
+        return static_cast<bf16x8 *>(to) + (m * (DK / 32) + ks) * 64 + lane_id();
     }
 };
 
@@ -174,65 +195,70 @@ __device__ __forceinline__ void put_block(float *a, int ai, int aj, const f32x4 
     for (int r = 0; r < 4; ++r) a[block_at(ai, aj, g, r, col)] = v[r];
 }
 
-// Fills t (X, P) for the n tokens at rows 0 .. n - 1 of k; t.L, t.beta and (TREE) t.mask are set
-// for all 64 tokens, those from n on with their predecessor's decay and no strength, and a
-// barrier passed; n >= 1. Four wavefronts; ends with a barrier. What the pieces below read is
-// defined: X's columns from n on are those of the identity (times no strength), P's rows from n
-// on belong to no token. Every other element right of the 32 x 32 diagonal blocks is not.
-template <typename TF, int DK, bool WHOLE, bool TREE>
-__device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<TF, DK, WHOLE> &rows,
-                                             const TF *__restrict__ k, size_t stride, int dk, int n) {
+// The pair products of the n tokens at rows 0 .. n - 1 of k: A into t, P into t (TREE) or, as the
+// wavefront's operand pieces, p. t.L, t.beta and (TREE) t.mask are set for all 64 tokens, those
+// from n on with their predecessor's decay and no strength, rows.share(t.X) was called, and a
+// barrier passed; n >= 1. Four wavefronts. Each holds K_j's rows on the left and its own on the
+// right, so that a lane has four neighbours of one row. P's rows from n on belong to no token;
+// what lies right of the 32 x 32 diagonal blocks (TREE: of their tiles) is not written.
+template <typename TF, int DK, bool WHOLE, bool TREE, typename Tokens>
+__device__ __forceinline__ void pair_products(Tokens &t, const SystemRows<TF, DK, WHOLE, TREE> &rows,
+                                              const TF *__restrict__ k, size_t stride, int dk, int n,
+                                              f32x4 (&p)[4]) {
     const int lane = lane_id(), col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     constexpr int KS = DK / 32, NK = Terms<TF>::K;
-    const f32x4 zero = (f32x4)0.f;
-    // ---- pair products: row tile `wave`, column tiles up to it
-    {
-        const int i0 = 16 * wave + 4 * g;
-        const f32x4 li = *reinterpret_cast<const f32x4 *>(&t.L[i0]);
-        const f32x4 lr = *reinterpret_cast<const f32x4 *>(&t.Lrest[i0]);
-        const f32x4 bi = *reinterpret_cast<const f32x4 *>(&t.beta[i0]);
-        uint32_t mask[4][2];
-        if (TREE) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                mask[r][0] = (uint32_t)t.mask[i0 + r];
-                mask[r][1] = (uint32_t)(t.mask[i0 + r] >> 32);
-            }
-        }
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            if (jt > wave) break;
-            f32x4 kk = zero, qk = zero;
-            const TF *kj = k + (size_t)min(16 * jt + col, n - 1) * stride;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                bf16x8 x[NK], b[NK];
-                row_part<WHOLE>(kj, 4 * ks + g, dk).terms(b);
-                rows.k[ks].terms(x);
-                kk = mfma_terms(x, b, kk);
-                rows.q[ks].terms(x);
-                qk = mfma_terms(x, b, qk);
-            }
-            const float lj = t.L[16 * jt + col], ljr = t.Lrest[16 * jt + col];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float d = __builtin_amdgcn_exp2f((li[r] - lj) + (lr[r] - ljr));
-                bool on = jt < wave || col <= 4 * g + r;
-                if (TREE) on = (mask[r][jt >> 1] >> (16 * (jt & 1) + col)) & 1u;
-                d = on ? d : 0.f;
-                qk[r] *= d;
-                kk[r] *= bi[r] * d;  // the diagonal is not read
-            }
-            put_block(t.P, wave, jt, qk);
-            put_block(t.A, wave, jt, kk);
-        }
-        if ((wave & 1) == 0) {  // the part of the 32 x 32 diagonal blocks that is right of the tiles
-            put_block(t.P, wave, wave + 1, zero);
-            put_block(t.X, wave, wave + 1, zero);
-        }
+    const int i = row_of<TREE>(wave, col);
+    const float li = t.L[i], lr = t.Lrest[i], bi = t.beta[i];
+    uint32_t mask[2];
+    if constexpr (TREE) {
+        mask[0] = (uint32_t)t.mask[i];
+        mask[1] = (uint32_t)(t.mask[i] >> 32);
     }
-    lds_barrier();
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+        p[jt] = (f32x4)0.f;
+        if (TREE ? jt > wave : jt >> 1 > wave >> 1) continue;
+        f32x4 kk = (f32x4)0.f, qk = (f32x4)0.f;
+        const TF *kj = k + (size_t)min(row_of<TREE>(jt, col), n - 1) * stride;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            bf16x8 x[NK], b[NK];
+            if constexpr (SystemRows<TF, DK, WHOLE, TREE>::kShared) x[0] = *rows.shared(t.X, jt, ks);
+            else row_part<WHOLE>(kj, 4 * ks + g, dk).terms(x);
+            rows.k[ks].terms(b);
+            kk = mfma_terms(x, b, kk);
+            rows.q[ks].terms(b);
+            qk = mfma_terms(x, b, qk);
+        }
+        const int j0 = row_of<TREE>(jt, 4 * g);
+        const f32x4 lj = *reinterpret_cast<const f32x4 *>(&t.L[j0]);
+        const f32x4 ljr = *reinterpret_cast<const f32x4 *>(&t.Lrest[j0]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float d = __builtin_amdgcn_exp2f((li - lj[r]) + (lr - ljr[r]));
+            bool on = j0 + r <= i;
+            if constexpr (TREE) on = (mask[jt >> 1] >> (16 * (jt & 1) + 4 * g + r)) & 1u;
+            d = on ? d : 0.f;
+            qk[r] *= d;
+            kk[r] *= bi * d;  // the diagonal is not read
+        }
+        p[jt] = qk;
+        *reinterpret_cast<f32x4 *>(&t.A[square_at(i, j0)]) = kk;
+        if constexpr (TREE) *reinterpret_cast<f32x4 *>(&t.P[square_at(i, j0)]) = qk;
+    }
+    if constexpr (TREE) {  // the part of the 32 x 32 diagonal blocks that is right of the tiles
+        if ((wave & 1) == 0) put_block(t.P, wave, wave + 1, (f32x4)0.f);
+    }
+}
+
+// X from A, both in t, whose A was written before a barrier; n as above. Ends with a barrier.
+// X's columns from n on are those of the identity (times no strength); what lies right of the
+// 32 x 32 diagonal blocks is not defined.
+__device__ __forceinline__ void invert_system(DeltaTokens &t, int n) {
+    const int lane = lane_id(), col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const f32x4 zero = (f32x4)0.f;
     // ---- X: the diagonal blocks, block g and column `col` of it a lane of one wavefront
     if (wave == 0) {
         float x[16];
@@ -249,6 +275,8 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<TF
             x[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
             t.X[1024 * g + 64 * i + ((g ^ (i >> 2)) << 4) + ((((col >> 2) ^ (i & 3)) << 2) | (col & 3))] = x[i];
         }
+    } else if (wave & 1) {
+        put_block(t.X, wave - 1, wave, zero);
     }
     lds_barrier();
     // ---- within the 32 x 32 blocks
@@ -275,7 +303,7 @@ __device__ __forceinline__ void delta_system(DeltaTokens &t, const SystemRows<TF
     lds_barrier();
 }
 
-// Row `token` of X diag(b) and of P, columns c .. c + 3 and d .. d + 3.
+// Row `token` of X diag(b) and of a tree's P, columns c .. c + 3 and d .. d + 3.
 __device__ __forceinline__ void x_piece(const DeltaTokens &t, int token, int c, int d, f32x4 &a,
                                         f32x4 &b) {
     a = *reinterpret_cast<const f32x4 *>(&t.X[square_at(token, c)]) *
@@ -284,7 +312,7 @@ __device__ __forceinline__ void x_piece(const DeltaTokens &t, int token, int c, 
         *reinterpret_cast<const f32x4 *>(&t.beta[d]);
 }
 
-__device__ __forceinline__ void p_piece(const DeltaTokens &t, int token, int c, int d, f32x4 &a,
+__device__ __forceinline__ void p_piece(const DeltaTree &t, int token, int c, int d, f32x4 &a,
                                         f32x4 &b) {
     a = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, c)]);
     b = *reinterpret_cast<const f32x4 *>(&t.P[square_at(token, d)]);

@@ -44,7 +44,7 @@ struct PrefillArgs {
 };
 
 template <typename TF, int DK, bool WHOLE>
-__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs<TF> a) {
+__global__ __launch_bounds__(256, sizeof(TF) == 2 ? 4 : 2) void delta_chunk_kernel(const PrefillArgs<TF> a) {
     __shared__ DeltaTokens t;
     const DeltaShape &s = a.s;
     const int h = blockIdx.x % s.H, slot = blockIdx.x / s.H, hk = h / (s.H / s.HK);
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs<T
     ChunkSystem<TF> &w = a.ws[(size_t)slot * s.H + h];
     const int dk = WHOLE ? DK : s.DK;
     const size_t sk = (size_t)s.HK * dk, row0 = (size_t)lo * sk + (size_t)hk * dk;
-    SystemRows<TF, DK, WHOLE> rows;
+    SystemRows<TF, DK, WHOLE, false> rows;
     rows.load(a.k + row0, a.q + row0, sk, dk, n);
     if (tid < 64) {
         // tokens past the last do not decay and have no strength
@@ -70,24 +70,32 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(const PrefillArgs<T
         w.start[tid] = in ? __builtin_amdgcn_exp2f((float)L) : 0.f;
         w.end[tid] = in ? __builtin_amdgcn_exp2f((float)(all - L)) : 0.f;
     }
+    rows.share(t.X);
     lds_barrier();
-    delta_system<TF, DK, WHOLE, false>(t, rows, a.k + row0, sk, dk, n);
+    f32x4 pair[4];
+    pair_products(t, rows, a.k + row0, sk, dk, n, pair);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
         if (sb > (wave >> 1)) continue;
-        const int f = piece_of(wave, sb);
+        constexpr int NP = ChunkSystem<TF>::kP;
+        bf16x8 p[NP];
+        split_terms8<NP>(pair[2 * sb], pair[2 * sb + 1], p);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            *reinterpret_cast<bf16x8 *>(&w.p[i][piece_of(wave, sb)][lane][0]) = p[i];
+    }
+    lds_barrier();
+    invert_system(t, n);
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+        if (sb > (wave >> 1)) continue;
         f32x4 x, y;
         x_piece(t, tile_token(wave, col), 32 * sb + 8 * g, 32 * sb + 8 * g + 4, x, y);
         bf16x8 xt[3];
         split_terms8<3>(x, y, xt);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8 *>(&w.x[i][f][lane][0]) = xt[i];
-        p_piece(t, tile_token(wave, col), 32 * sb + 8 * g, 32 * sb + 8 * g + 4, x, y);
-        constexpr int NP = ChunkSystem<TF>::kP;
-        bf16x8 p[NP];
-        split_terms8<NP>(x, y, p);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8 *>(&w.p[i][f][lane][0]) = p[i];
+        for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<bf16x8 *>(&w.x[i][piece_of(wave, sb)][lane][0]) = xt[i];
     }
 }
 

@@ -127,9 +127,8 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_ker
     typedef float hvec __attribute__((ext_vector_type(NT)));
     typedef TF vvec __attribute__((ext_vector_type(NT)));
     constexpr int KS = DK / 32, NK = Terms<TF>::K, NS = Terms<TF>::S;
-    __shared__ DeltaTokens t;
-    constexpr bool SHARE = sizeof(TF) == 2;
-    __bf16 *const s_k = reinterpret_cast<__bf16 *>(t.A);
+    __shared__ DeltaTree t;
+    constexpr bool SHARE = SystemRows<TF, DK, WHOLE, true>::kShared;
     static_assert(4 * KS * 512 * 2 <= sizeof(t.A), "K over A");
     const int unit = blockIdx.x, tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_ker
                     reinterpret_cast<const hvec *>(Hu + (size_t)(WHOLE || row < dk ? row : 0) * s.DV));
             }
     }
-    SystemRows<TF, DK, WHOLE> rows;
+    SystemRows<TF, DK, WHOLE, true> rows;
     if (n > 0) rows.load(kb, qb, sk, dk, n);
     if (tid < 64) {
         const bool in = tid < n;
@@ -173,6 +172,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_ker
         t.beta[tid] = in ? beta[(size_t)(lo + tid) * s.H + h] : 0.f;
         if (tid == 0) t.bad = w.bad;
     }
+    if (n > 0) rows.share(t.X);
     lds_barrier();
     if (first) tree_status[b] = t.bad;
     const size_t v0 = (size_t)lo * sv + (size_t)h * s.DV;
@@ -182,11 +182,12 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_ker
         return;
     }
     if (n == 0) return;
-    delta_system<TF, DK, WHOLE, true>(t, rows, kb, sk, dk, n);
+    f32x4 pair[4];
+    pair_products(t, rows, kb, sk, dk, n, pair);
+    lds_barrier();
+    invert_system(t, n);
     if constexpr (SHARE) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            *reinterpret_cast<bf16x8 *>(&s_k[((wave * KS + ks) * 64 + lane) * 8]) = rows.k[ks].x;
+        rows.share(t.A);
         lds_barrier();
     }
     // row tile m has nodes of the tree
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 3 : 2) void delta_verify_ker
             const size_t row = (size_t)min(16 * m + col, n - 1) * sk;
             bf16x8 ka[NK], qa[NK];
             if constexpr (SHARE) {
-                ka[0] = load16(&s_k[((m * KS + ks) * 64 + lane) * 8]);
+                ka[0] = *rows.shared(t.A, m, ks);
             } else {
                 row_part<WHOLE>(kb + row, 4 * ks + g, dk).terms(ka);
             }
