@@ -392,6 +392,9 @@ __global__ __launch_bounds__(512, sizeof(TF) == 2 ? 4 : 2) void delta_scan_kerne
             o *= s_w[chunk & 1][my_row];
             fetch_q(t1, last);
             lds_barrier();
+            stage((chunk + 1) & 1);
+            const System &w2 = chunk_at(chunk + 2, t1, last);
+            fetch_k(t1, last, w2);
             lds_barrier();
             // ---- O^T += U^T P^T
 #pragma unroll
@@ -405,9 +408,6 @@ __global__ __launch_bounds__(512, sizeof(TF) == 2 ? 4 : 2) void delta_scan_kerne
                     for (int j = 0; j < System::kP && i + j < NS; ++j) o = mfma16_bf16(ub[i], p[sb][j], o);
             }
             fetch_p(w);
-            stage((chunk + 1) & 1);
-            const System &w2 = chunk_at(chunk + 2, t1, last);
-            fetch_k(t1, last, w2);
             if (chunk * kChunk + my_row < n && (WHOLE || 16 * cg + 4 * g < s.DV))
                 *reinterpret_cast<tf4 *>(ob + (size_t)(chunk * kChunk) * svb + ooff) =
                     __builtin_convertvector(o, tf4);
