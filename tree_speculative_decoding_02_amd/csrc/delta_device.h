@@ -117,6 +117,17 @@ __device__ __forceinline__ double wave_sum_up_f64(double x) {
     return x;
 }
 
+// Inclusive sum over lanes 0 .. lane.
+__device__ __forceinline__ int wave_sum_up(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4 and 8 lanes before,
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);  // within rows of 16
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // a row's last lane to the next row,
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 to the upper half
+    return x;
+}
+
 // Whether all B + 1 offsets are ordered and inside [0, T] (wave-uniform; all lanes active).
 __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off, int B, int T) {
     bool bad = false;
@@ -127,35 +138,32 @@ __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off,
     return !__any(bad);
 }
 
-// Tile `slot` of the packed rows (MT packed rows a tile, G packed rows a row): sequence b owns
-// slots from floor(off[b] G / MT) + b, at least one each (slots before the first sequence's are
-// nobody's). `per` (may be NULL): a value of each sequence, loaded along with the offsets.
+// Tile `slot` of the packed rows, MT rows a tile: sequence b owns slots from floor(off[b] / MT) + b,
+// at least one each (slots before the first sequence's are nobody's).
 struct Located {
     bool found, ordered;       // found: b owns the slot; ordered: the offsets are
-    int b, lo, n, slot0, per;  // sequence, its rows, its first slot, its value
+    int b, lo, n, slot0;       // sequence, its rows, its first slot
 };
 
-__device__ __forceinline__ Located locate(const int32_t *__restrict__ off, const int32_t *__restrict__ per,
-                                          int B, int T, int G, int MT, int slot) {
+__device__ __forceinline__ Located locate(const int32_t *__restrict__ off, int B, int T, int MT, int slot) {
     bool bad = false;
-    Located l = {false, true, -1, 0, 0, 0, 0};
+    Located l = {false, true, -1, 0, 0, 0};
     for (int c = 0; c < B; c += 64) {
         const int x = min(c + lane_id(), B - 1);
-        const int lo = off[x], hi = off[x + 1], v = per ? per[x] : 0;
+        const int lo = off[x], hi = off[x + 1];
         bad |= lo < 0 || hi < lo || hi > T;
         // the sequences that start at or before the slot are the first ones
-        const int many = (int)__popcll(__ballot(c + lane_id() < B && (int64_t)lo * G / MT + x <= slot));
+        const int many = (int)__popcll(__ballot(c + lane_id() < B && lo / MT + x <= slot));
         if (many > 0) {
             const int at = __builtin_amdgcn_readfirstlane(many - 1);
             l.b = c + at;
             l.lo = __builtin_amdgcn_readlane(lo, at);
             l.n = __builtin_amdgcn_readlane(hi, at) - l.lo;
-            l.per = __builtin_amdgcn_readlane(v, at);
         }
     }
     l.ordered = !__any(bad);
     l.found = l.ordered && l.b >= 0;
-    l.slot0 = (int)((int64_t)l.lo * G / MT) + l.b;
+    l.slot0 = l.lo / MT + l.b;
     return l;
 }
 

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 4 : 2) void delta_chunk_kern
     const DeltaShape &s = a.s;
     const int h = blockIdx.x % s.H, slot = blockIdx.x / s.H, hk = h / (s.H / s.HK);
     const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const Located l = locate(a.offsets, nullptr, s.B, s.T, 1, kChunk, slot);
+    const Located l = locate(a.offsets, s.B, s.T, kChunk, slot);
     if (!l.found) return;
     const int done = (slot - l.slot0) * kChunk, lo = l.lo + done, n = min(kChunk, l.n - done);
     if (n <= 0) return;

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
 }
 
 template <int D>
-__global__ __launch_bounds__(256, 1) void window_tokens_kernel(const WindowArgs a, const WindowParts parts,
+__global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs a, const WindowParts parts,
                                                                int slots) {
     constexpr int CH = D / 8, VP = Pad<D>::V, VPER = kKeys * CH / 64;
     constexpr int JOIN = 4 * 16 * (D + 4) * 4;  // the last merge: sums, then (m, l), over the values
@@ -481,7 +481,7 @@ static WindowPlan plan(const bole_window_dims_t &d) {
     WindowPlan p;
     const int64_t G = d.heads / d.kv_heads, rows = d.total_rows * G;
     p.f32 = d.dtype == BOLE_DTYPE_F32;
-    p.tokens = !p.f32 && rows <= 32LL * d.batch;
+    p.tokens = !p.f32 && rows <= 16LL * d.batch;
     p.tile = p.f32 ? 64 : p.tokens ? kTokenTile : kRowTile;
     p.slots = (int)(rows / p.tile + d.batch);
     const int64_t cached = (int64_t)d.max_pages * d.page_size;

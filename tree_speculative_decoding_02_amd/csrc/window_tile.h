@@ -54,6 +54,43 @@ __device__ __forceinline__ void key_list(const WindowShape &s, bool tree, RowTil
     t.total = t.own0 + t.n3 + t.n4;
 }
 
+// Row tile `slot` of a call: sequence b's tiles (MT packed rows, G to a row; at least one) lie
+// behind those of the sequences before it, so the slots that are nobody's are the last ones. (In
+// turn with the others they cost more than their exit: 64 sequences of one whole tile and one spare
+// slot each took 251 us, against 190 of one.) per: the sequence's cached tokens.
+struct Slot {
+    bool found, ordered;            // found: b owns the slot; ordered: the offsets are
+    int b, lo, n, slot0, per;       // sequence, its rows, its first slot
+};
+
+template <int MT>
+__device__ __forceinline__ Slot find_slot(const WindowArgs &a, int G, int slot) {
+    const int B = a.s.B;
+    bool bad = false;
+    Slot l = {false, true, 0, 0, 0, 0, 0};
+    int before = 0;
+    for (int c = 0; c < B; c += 64) {
+        const int x = min(c + lane_id(), B - 1);
+        const int lo = a.offsets[x], hi = a.offsets[x + 1], len = a.cache_len[x];
+        bad |= lo < 0 || hi < lo || hi > a.s.T;
+        const int own = c + lane_id() < B ? max(1, (int)(((uint32_t)(hi - lo) * G + MT - 1) / MT)) : 0;
+        const int end = before + wave_sum_up(own);
+        const int at = uniform((int)__popcll(__ballot(c + lane_id() < B && end <= slot)));
+        if (!l.found && at < min(64, B - c)) {
+            l.found = true;
+            l.b = c + at;
+            l.lo = __builtin_amdgcn_readlane(lo, at);
+            l.n = __builtin_amdgcn_readlane(hi, at) - l.lo;
+            l.slot0 = __builtin_amdgcn_readlane(end - own, at);
+            l.per = __builtin_amdgcn_readlane(len, at);
+        }
+        before = __builtin_amdgcn_readlane(end, 63);
+    }
+    l.ordered = !__any(bad);
+    l.found = l.found && l.ordered;
+    return l;
+}
+
 // Finds the workgroup's tile and all that is wrong with its sequence but its pages. Every
 // wavefront computes the same. mask: of a tree, lane i's node's visible own nodes (its path, cut
 // to the window); depth: its depth. False: no rows here.
@@ -63,7 +100,7 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
     const WindowShape &s = a.s;
     const int lane = lane_id();
     t.status = BOLE_TREE_OK;
-    const Located l = locate(a.offsets, a.cache_len, s.B, s.T, G, MT, slot);
+    const Slot l = find_slot<MT>(a, G, slot);
     if (!l.found) {
         if (!l.ordered && report && slot == 0 && a.status)
             for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
@@ -197,7 +234,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     const size_t stride = (size_t)slots * s.HK * MT, at = (size_t)blockIdx.x * MT + r;
     // every part's maximum and sum, a part a lane (the rows of unused tiles are never read)
-    const Located t = locate(a.offsets, nullptr, s.B, s.T, G, MT, slot);
+    const Slot t = find_slot<MT>(a, G, slot);
     const int R = (slot - t.slot0) * MT + r;
     if (!t.found || R >= t.n * G) return;
     float m = -INFINITY, l = 0.f;
