@@ -112,9 +112,13 @@ __global__ __launch_bounds__(256) void delta_verify_generic_kernel(
 // Row tile m is nodes 16 m .. 16 m + 15; as a right operand, tiles 2s and 2s + 1 hold in lane
 // group g nodes 32 s + 4 g .. + 3 and 32 s + 16 + 4 g .. + 3, and X and P are read to match. The
 // wavefronts' own rows of a bf16 K serve all four through LDS, over A, which the system no longer
-// needs; Q is read again from the caches. (64 trees of 64 nodes, 32 heads, 128 x 128: 90.5 us with
-// both from the caches, 81.2 this way, 80.3 with Q in 16 KB more of LDS; of up to 64 nodes: 58.6,
-// 54.7 and 57.4, as the third form leaves two workgroups a CU instead of three.)
+// needs; Q is read again from the caches. (64 trees of 64 nodes, 32 heads, 128 x 128: 83 us with
+// both from the caches, 74 this way; Q through 16 KB more of LDS leaves two workgroups a CU instead
+// of three and took 57.4 instead of 54.7 us for trees of up to 64 nodes.)
+//
+// Measured: 64 trees of up to 64 nodes 48 us (3.5 TB/s: the states' bytes and about as much time
+// again for the systems, whose steps wait for each other), 8 trees of 32 nodes and 32 x 128 x 64
+// states 10 us (one chain of loads, system and products); fp32, 64 trees of 64 nodes 126 us.
 //
 // NT = 2 (d_v a multiple of 32): lane c of 16 holds columns 2c and 2c + 1, and a state row's 32
 // columns are one 128-byte read.

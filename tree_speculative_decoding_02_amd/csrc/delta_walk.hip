@@ -12,7 +12,9 @@
 // The state is read once and written once whatever the number of tokens, with non-temporal
 // 16-byte accesses (a row's eight lanes cover 128 contiguous bytes).
 //
-// Step and commit are bound by the state's round trip through HBM. Tokens of a sequence
+// Step and commit are bound by the state's round trip through HBM: 128 sequences of 32 heads with
+// 128 x 128 states, one token each, 95 us (5.7 TB/s), 64 accepted paths of trees of up to 64 nodes
+// 42 us (5.2 TB/s); one sequence's step, a chain of loads and sums, 3.4 us in a graph. Tokens of a sequence
 // cannot overlap here, so long prompts are bound by the chain of a token's products and
 // exchanges; the chunked kernels take the shapes where that matters.
 #include "delta_device.h"
