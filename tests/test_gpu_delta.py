@@ -127,6 +127,21 @@ def test_prefill(lib, shape, sizes):
             assert torch.equal(t["H0"][b].cpu(), w.H0[b])
 
 
+@pytest.mark.parametrize("shape", [SHAPES[1], SHAPES[4], SHAPES[9], SHAPES[5]],
+                         ids=[IDS[1], IDS[4], IDS[9], IDS[5]])
+def test_many_sequences(lib, shape):
+    """More sequences than a wavefront has lanes, empty ones among them and at both ends."""
+    sizes = [0] + ([33, 1, 0, 64, 5, 0, 70] * 20)[:138] + [0]
+    w = make(24, sizes, shape, spare_rows=3)
+    t = on_gpu(w)
+    out, status = torch.full_like(t["v"], -7.0), torch.full((140,), -1, dtype=torch.int32, device=dev())
+    lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out, seq_status=status)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(t["H0"], S, w)
+    check_prompt(out, ref, w, column_norms(w))
+    assert (out[-3:] == -7.0).all() and status.tolist() == [0] * 140
+
+
 @pytest.mark.parametrize("shape", SHAPES[:4], ids=IDS[:4])
 @pytest.mark.parametrize("kw", [dict(gate_value=1.0), dict(gate_value=0.0), dict(gate_value=1e-30),
                                 dict(gate_value=1.02), dict(strength=0.0), dict(strength=1.0),

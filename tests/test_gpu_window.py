@@ -152,6 +152,46 @@ def test_large_scores(lib, shape):
         check(out, ref, w, 310)
 
 
+@pytest.mark.parametrize("slope", [0.03, 0.11, -0.11, 1.0])
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[4]], ids=[IDS[0], IDS[2], IDS[4]])
+def test_rising_and_falling_scores(lib, shape, slope):
+    """Scores that climb by a little, by about the step of the exponentials' reference, or by far
+    more from one 64-key tile to the next, and that fall: q is a unit vector, k holds the score."""
+    for sizes, tree in (([1, 1], False), ([40, 7], False), ([40, 7], True)):
+        w = make(45, sizes, [700, 130], shape, 600, 4, poison=False)
+        w.q.zero_()
+        w.q[..., 0] = 1.0
+        ps, place = shape[3], np.arange(800.0)
+        for b, c in enumerate(w.cache_len.tolist()):
+            for s in range(c):
+                w.k_cache[w.page_table[b, s // ps], :, s % ps, 0] = float(slope * place[s])
+            lo, n = int(w.offsets[b]), sizes[b]
+            for i in range(n):
+                w.k[lo + i, :, 0] = float(slope * place[c + i])
+        out = lib.bole_window_attention(**on_gpu(w), window=600, sinks=4, scale=1.0,
+                                        parent=g(w.parent) if tree else None)
+        check(out, oracle_of(w, 600, 4, tree, 1.0), w, 650)
+
+
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[4], SHAPES[3]],
+                         ids=[IDS[0], IDS[2], IDS[4], IDS[3]])
+@pytest.mark.parametrize("cycle", [[1], [0, 1, 2, 0, 3], [33, 1, 0, 64, 5, 0, 17]], ids=str)
+def test_many_sequences(lib, shape, cycle):
+    """More sequences than a wavefront has lanes, empty ones among them and at both ends."""
+    sizes = [0] + (cycle * 150)[:148] + [0]
+    cached = [(37 * b) % 150 for b in range(150)]
+    w = make(46, sizes, cached, shape, 100, 2, spare_rows=2)
+    t = on_gpu(w)
+    T = sum(sizes)
+    rows = set(range(0, T, max(1, T // 97))) | {0, T - 1}
+    for parent in (None, g(w.parent)):
+        out, status = torch.full_like(t["q"], -7.0), torch.full((150,), -1, dtype=torch.int32, device=dev())
+        lib.bole_window_attention(**t, window=100, sinks=2, out=out, parent=parent, seq_status=status)
+        check(out, oracle_of(w, 100, 2, parent is not None, rows=rows), w, 200)
+        assert status.tolist() == [0] * 150 and (out[-2:] == -7.0).all()
+        assert out[:T].isfinite().all() and not (out[:T] == -7.0).all(dim=(1, 2)).any()
+
+
 def test_matches_generic(lib):
     w = make(44, [64, 20, 3], [300, 64, 1000], SHAPES[0], 200, 4)
     t = on_gpu(w)
