@@ -366,6 +366,59 @@ def test_unaligned_and_sliced_buffers(lib):
         check_prompt(out, ref, w, column_norms(w))
 
 
+def test_states_past_32_bit_offsets(lib):
+    """5 GB of states, the last sequences of which have rows: they come out as the oracle's, and
+    the state of every sequence without a token keeps its bits."""
+    H, B = 32, 2400
+    shape = (H, 4, 128, 128, BF16)
+
+    def embed(w):
+        lead = B - len(w.offsets) + 1
+        big = torch.empty(B, H, 128, 128, device=dev()).normal_(generator=torch.Generator(dev()).manual_seed(5))
+        big[lead:] = g(w.H0)
+        return big, g(np.concatenate([np.zeros(lead, np.int32), w.offsets])), lead
+
+    w = make(55, [70, 3], shape)
+    t = on_gpu(w)
+    big, offs, lead = embed(w)
+    before = big[:lead].clone()
+    t["H0"] = big
+    out = lib.bole_delta_prefill(**t, seq_offsets=offs)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(big[lead:], S, w)
+    check_prompt(out, ref, w, column_norms(w))
+    assert torch.equal(big[:lead], before)
+
+    w = make(56, [20, 40], shape)
+    t = on_gpu(w)
+    big[lead:] = g(w.H0)
+    t["H0"] = big
+    a = dict(parent=g(w.parent), node_offsets=offs.clone())
+    a["node_offsets"][lead:] = g(w.offsets)
+    out = lib.bole_delta_tree_verify(**t, **a)
+    check_out(out, O.verify(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.parent, w.offsets), w, column_norms(w))
+    t.pop("q")
+    idx = torch.full((B, w.accepted_idx.shape[1]), -1, dtype=torch.int32, device=dev())
+    many = torch.zeros(B, dtype=torch.int32, device=dev())
+    idx[lead:], many[lead:] = g(w.accepted_idx), g(w.accepted_len)
+    lib.bole_delta_commit_path(**t, **a, accepted_idx=idx, accepted_len=many)
+    check_states(big[lead:], O.commit(w.H0, w.k, w.v, w.gate, w.beta, w.offsets, w.accepted_idx,
+                                      w.accepted_len), w)
+    assert torch.equal(big[:lead], before)
+
+    w = make(57, [1, 1], shape)
+    t = on_gpu(w)
+    big[lead:] = g(w.H0)
+    wide = {n: torch.cat([torch.zeros(lead, *x.shape[1:], dtype=x.dtype, device=dev()), x])
+            for n, x in t.items() if n != "H0"}
+    wide["gate"][:lead] = 1.0            # no strength, no decay: those states stay
+    out = lib.bole_delta_step(big, **wide)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(big[lead:], S, w)
+    check_out(out[lead:], ref, w, column_norms(w))
+    assert torch.equal(big[:lead], before)
+
+
 def test_prefill_then_verify_then_commit(lib):
     """One sequence's life: a prompt, a draft tree verified on its state, the accepted path
     committed, the next tree, and a single token after it."""

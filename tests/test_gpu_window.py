@@ -297,6 +297,36 @@ def test_hidden_values_do_not_matter(lib):
     assert torch.equal(a, lib.bole_window_attention(**u, window=64, sinks=4))
 
 
+@pytest.mark.parametrize("tree", [False, True], ids=["tokens", "trees"])
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[4]], ids=[IDS[0], IDS[4]])
+def test_cache_past_32_bit_offsets(lib, shape, tree):
+    """The same pages at the end of a cache of more than 4 GiB: the same bits."""
+    w = make(56, [64, 9] if tree else [1, 1], [300, 77], shape, 100, 4)
+    t = on_gpu(w)
+    parent = g(w.parent) if tree else None
+    ref = lib.bole_window_attention(**t, window=100, sinks=4, parent=parent)
+    check(ref, oracle_of(w, 100, 4, tree), w, 200)
+    page = t["k_cache"][0].numel() * t["k_cache"].element_size()
+    pages, n = (5 << 30) // page, w.k_cache.shape[0]
+    u = dict(t)
+    for c in ("k_cache", "v_cache"):
+        u[c] = torch.empty(pages, *t[c].shape[1:], dtype=t[c].dtype, device=dev())
+        u[c][-n:] = t[c]
+    u["page_table"] = torch.where((t["page_table"] >= 0) & (t["page_table"] < n),
+                                  t["page_table"] + (pages - n), t["page_table"])
+    u["page_table"][u["page_table"] == n + 12345] = pages
+    assert torch.equal(ref, lib.bole_window_attention(**u, window=100, sinks=4, parent=parent))
+
+
+def test_sequences_that_share_pages(lib):
+    """One prefix's pages in several tables, as forked sequences have them."""
+    w = make(57, [1, 1, 1], [500, 500, 200], SHAPES[0], 2**31 - 1, 0, poison=False)
+    w.page_table[1] = w.page_table[0]
+    w.page_table[2] = w.page_table[0]
+    check(lib.bole_window_attention(**on_gpu(w), window=2**31 - 1, sinks=0),
+          oracle_of(w, 2**31 - 1, 0, False), w, 501)
+
+
 def test_streams_and_graph_replays(lib):
     """Two calls at once on two streams; single tokens, trees and prompts captured together and
     replayed with eager work in between, bit for bit; pages that move between replays."""
