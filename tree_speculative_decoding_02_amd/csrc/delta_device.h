@@ -128,12 +128,23 @@ __device__ __forceinline__ int wave_sum_up(int x) {
     return x;
 }
 
+// Every workgroup looks through all offsets, 64 a load, so many loads at a time: attention of 1024
+// single tokens over 256 cached ones 322 us with one, 306 with two, 293 with four, 289 with eight;
+// of one token 10.9 and, with eight, 11.1.
+constexpr int kAtOnce = 4;
+
 // Whether all B + 1 offsets are ordered and inside [0, T] (wave-uniform; all lanes active).
 __device__ __forceinline__ bool offsets_ordered(const int32_t *__restrict__ off, int B, int T) {
     bool bad = false;
-    for (int b = lane_id(); b < B; b += 64) {
-        const int lo = off[b], hi = off[b + 1];
-        bad |= lo < 0 || hi < lo || hi > T;
+    for (int c = 0; c < B; c += 64 * kAtOnce) {
+        int lo[kAtOnce], hi[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int x = min(c + 64 * j + lane_id(), B - 1);
+            lo[j] = off[x], hi[j] = off[x + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > T;
     }
     return !__any(bad);
 }
@@ -148,17 +159,26 @@ struct Located {
 __device__ __forceinline__ Located locate(const int32_t *__restrict__ off, int B, int T, int MT, int slot) {
     bool bad = false;
     Located l = {false, true, -1, 0, 0, 0};
-    for (int c = 0; c < B; c += 64) {
-        const int x = min(c + lane_id(), B - 1);
-        const int lo = off[x], hi = off[x + 1];
-        bad |= lo < 0 || hi < lo || hi > T;
-        // the sequences that start at or before the slot are the first ones
-        const int many = (int)__popcll(__ballot(c + lane_id() < B && lo / MT + x <= slot));
-        if (many > 0) {
-            const int at = __builtin_amdgcn_readfirstlane(many - 1);
-            l.b = c + at;
-            l.lo = __builtin_amdgcn_readlane(lo, at);
-            l.n = __builtin_amdgcn_readlane(hi, at) - l.lo;
+    for (int c0 = 0; c0 < B; c0 += 64 * kAtOnce) {
+        int lo[kAtOnce], hi[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int x = min(c0 + 64 * j + lane_id(), B - 1);
+            lo[j] = off[x], hi[j] = off[x + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int c = c0 + 64 * j;
+            if (c >= B) break;
+            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > T;
+            // the sequences that start at or before the slot are the first ones
+            const int many = (int)__popcll(__ballot(c + lane_id() < B && lo[j] / MT + c + lane_id() <= slot));
+            if (many > 0) {
+                const int at = __builtin_amdgcn_readfirstlane(many - 1);
+                l.b = c + at;
+                l.lo = __builtin_amdgcn_readlane(lo[j], at);
+                l.n = __builtin_amdgcn_readlane(hi[j], at) - l.lo;
+            }
         }
     }
     l.ordered = !__any(bad);

@@ -69,22 +69,31 @@ __device__ __forceinline__ Slot find_slot(const WindowArgs &a, int G, int slot) 
     bool bad = false;
     Slot l = {false, true, 0, 0, 0, 0, 0};
     int before = 0;
-    for (int c = 0; c < B; c += 64) {
-        const int x = min(c + lane_id(), B - 1);
-        const int lo = a.offsets[x], hi = a.offsets[x + 1], len = a.cache_len[x];
-        bad |= lo < 0 || hi < lo || hi > a.s.T;
-        const int own = c + lane_id() < B ? max(1, (int)(((uint32_t)(hi - lo) * G + MT - 1) / MT)) : 0;
-        const int end = before + wave_sum_up(own);
-        const int at = uniform((int)__popcll(__ballot(c + lane_id() < B && end <= slot)));
-        if (!l.found && at < min(64, B - c)) {
-            l.found = true;
-            l.b = c + at;
-            l.lo = __builtin_amdgcn_readlane(lo, at);
-            l.n = __builtin_amdgcn_readlane(hi, at) - l.lo;
-            l.slot0 = __builtin_amdgcn_readlane(end - own, at);
-            l.per = __builtin_amdgcn_readlane(len, at);
+    for (int c0 = 0; c0 < B; c0 += 64 * kAtOnce) {
+        int lo[kAtOnce], hi[kAtOnce], len[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int x = min(c0 + 64 * j + lane_id(), B - 1);
+            lo[j] = a.offsets[x], hi[j] = a.offsets[x + 1], len[j] = a.cache_len[x];
         }
-        before = __builtin_amdgcn_readlane(end, 63);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int c = c0 + 64 * j;
+            if (c >= B) break;
+            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > a.s.T;
+            const int own = c + lane_id() < B ? max(1, (int)(((uint32_t)(hi[j] - lo[j]) * G + MT - 1) / MT)) : 0;
+            const int end = before + wave_sum_up(own);
+            const int at = uniform((int)__popcll(__ballot(c + lane_id() < B && end <= slot)));
+            if (!l.found && at < min(64, B - c)) {
+                l.found = true;
+                l.b = c + at;
+                l.lo = __builtin_amdgcn_readlane(lo[j], at);
+                l.n = __builtin_amdgcn_readlane(hi[j], at) - l.lo;
+                l.slot0 = __builtin_amdgcn_readlane(end - own, at);
+                l.per = __builtin_amdgcn_readlane(len[j], at);
+            }
+            before = __builtin_amdgcn_readlane(end, 63);
+        }
     }
     l.ordered = !__any(bad);
     l.found = l.found && l.ordered;
