@@ -152,6 +152,25 @@ def test_large_scores(lib, shape):
         check(out, ref, w, 310)
 
 
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[4], SHAPES[6]],
+                         ids=[IDS[0], IDS[2], IDS[4], IDS[6]])
+def test_scores_past_fp32(lib, shape):
+    """A query whose scores leave fp32's range gets NaN, as its softmax has; no other row does."""
+    for sizes, cached, tree in (([1, 1], [4000, 70], False), ([40, 2], [4000, 70], True),
+                                ([40, 2], [100, 70], False)):
+        w = make(47, sizes, cached, shape, 5000, 0)
+        t = on_gpu(w)
+        ref = oracle_of(w, 5000, 0, tree)
+        t["q"][0] = 3e38 * torch.sign(t["k"][0, :1].float()).to(t["q"].dtype)
+        t["k"][0] = t["k"][0].sign() * 3e38
+        out = torch.full_like(t["q"], -7.0)
+        lib.bole_window_attention(**t, window=5000, sinks=0, out=out, parent=g(w.parent) if tree else None)
+        G = shape[0] // shape[1]
+        assert out[0, :G].isnan().all()
+        last = sum(sizes) - 1            # another sequence: untouched by it
+        check(out[last:], tuple(x[last:] for x in ref), w, 4100)
+
+
 @pytest.mark.parametrize("slope", [0.03, 0.11, -0.11, 1.0])
 @pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[2], SHAPES[4]], ids=[IDS[0], IDS[2], IDS[4]])
 def test_rising_and_falling_scores(lib, shape, slope):

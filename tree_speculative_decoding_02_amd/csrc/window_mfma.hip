@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(const WindowArgs a,
     auto give_up = [&]() {
         const bool fill = t.status != BOLE_TREE_BAD_SIZE;
         if (parts.n > 1) {
-            if (live && hh == 0) parts.ml[part_row * 2] = fill ? __builtin_nanf("") : INFINITY;
+            if (live && hh == 0) parts.ml[part_row * 2 + 1] = fill ? kNanRow : kLeftRow;
         } else if (live && fill) {
             for (int e = hh; e < D; e += 2) out[e] = (__bf16)__builtin_nanf("");
         }
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(256, 2) void window_tokens_kernel(const WindowArgs 
         const bool fill = t.status != BOLE_TREE_BAD_SIZE;
         if (parts.n > 1) {
             if (live && g == 0 && wave == 0)
-                parts.ml[(part_tile + col) * 2] = fill ? __builtin_nanf("") : INFINITY;
+                parts.ml[(part_tile + col) * 2 + 1] = fill ? kNanRow : kLeftRow;
         } else if (live && fill) {
             __bf16 *o = static_cast<__bf16 *>(a.out) + row_offset(R);
             for (int e = wave * 4 + g; e < D; e += 16) o[e] = (__bf16)__builtin_nanf("");

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256, 2) void window_f32_kernel(const WindowArgs a, 
     auto give_up = [&]() {
         const bool fill = t.status != BOLE_TREE_BAD_SIZE;
         if (parts.n > 1) {
-            if (live && g == 0) parts.ml[part_row * 2] = fill ? __builtin_nanf("") : INFINITY;
+            if (live && g == 0) parts.ml[part_row * 2 + 1] = fill ? kNanRow : kLeftRow;
         } else if (live && fill) {
             for (int e = g; e < D; e += 4) out[e] = __builtin_nanf("");
         }

@@ -9,8 +9,9 @@ namespace bole {
 constexpr int kKeys = 64;        // keys a tile
 
 // Where the unnormalised parts of a split call go: O [parts][tiles][MT][D], then (m, l)
-// [parts][tiles][MT][2]. A part's m is NaN for a sequence whose rows become NaN and +inf for
-// one that is not touched.
+// [parts][tiles][MT][2]. In place of a sum, which is not negative, stands kNanRow for a sequence
+// whose rows become NaN and kLeftRow for one that is not touched.
+constexpr float kNanRow = -1.f, kLeftRow = -2.f;
 struct WindowParts {
     float *o, *ml;
     int n;         // parts of the key list
@@ -251,13 +252,13 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
         m = parts.ml[(lane * stride + at) * 2];
         l = parts.ml[(lane * stride + at) * 2 + 1];
     }
-    // all parts of a bad sequence say the same: NaN rows, or (+inf) untouched ones
-    const float m0 = readlane_f(m, 0);
-    if (m0 == INFINITY) return;
+    // (all parts of a bad sequence say the same)
+    const float l0 = readlane_f(l, 0);
+    if (l0 == kLeftRow) return;
     float top = m;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    const float f = __builtin_amdgcn_exp2f(m - top);  // top is finite: some part sees the row itself
+    const float f = __builtin_amdgcn_exp2f(m - top);
     float sum = f * l;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
     if (d >= D) return;
     const float y = ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / sum;
     static_cast<T *>(a.out)[((size_t)(t.lo + i) * s.H + hk * G + (R - i * G)) * D + d] =
-        (T)(m0 == m0 ? y : m0);
+        (T)(l0 == kNanRow ? __builtin_nanf("") : y);
 }
 
 }  // namespace bole
