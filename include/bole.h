@@ -612,7 +612,7 @@ typedef struct {
     int32_t sinks;       /* >= 0 */
     int32_t dtype;       /* bole_dtype_t */
     int32_t flags;       /* 0 or BOLE_FLAG_FORCE_GENERIC */
-    float scale;         /* finite */
+    float scale;         /* below 2^127 in size */
 } bole_window_dims_t;
 
 /* Host-only check of the dims, the same check the entry point runs first. */

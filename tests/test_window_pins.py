@@ -78,7 +78,7 @@ def dims(**kw):
     ("head_dim", 257, 2), ("total_rows", -1, 1), ("num_pages", -1, 1), ("page_size", 0, 1),
     ("page_size", 24, 1), ("page_size", 2048, 2), ("max_pages", -1, 1), ("max_pages", 1 << 28, 2),
     ("window", 0, 1), ("sinks", -1, 1), ("dtype", 3, 1), ("flags", 4, 1),
-    ("scale", float("nan"), 1), ("scale", float("inf"), 1), ("total_rows", 1 << 29, 2),
+    ("scale", float("nan"), 1), ("scale", float("inf"), 1), ("scale", 3e38, 1), ("total_rows", 1 << 29, 2),
 ])
 def test_check_dims_refuses(field, value, want):
     assert bole.lib.bole_window_check_dims(ctypes.byref(dims(**{field: value}))) == want

@@ -13,7 +13,7 @@ bole_status_t bole_window_check_dims(const bole_window_dims_t *d) {
     if (d == nullptr) return BOLE_ERR_INVALID_VALUE;
     if (d->batch < 0 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads != 0 ||
         d->head_dim < 1 || d->total_rows < 0 || d->num_pages < 0 || d->max_pages < 0 ||
-        d->window < 1 || d->sinks < 0 || !std::isfinite(d->scale))
+        d->window < 1 || d->sinks < 0 || !std::isfinite(2.f * d->scale))  // (so is its product with log2 e)
         return BOLE_ERR_INVALID_VALUE;
     if (d->page_size < 1 || (d->page_size & (d->page_size - 1)) != 0) return BOLE_ERR_INVALID_VALUE;
     if (d->dtype != BOLE_DTYPE_BF16 && d->dtype != BOLE_DTYPE_F32) return BOLE_ERR_INVALID_VALUE;

@@ -1,7 +1,6 @@
 """Binding of windowed attention over a paged cache (include/bole.h). As in bole.py, only
 arguments are checked and marshalled here; streams are handled as in delta.py."""
 import ctypes
-import math
 
 import torch
 
@@ -34,8 +33,8 @@ def _dims(q, k, v, k_cache, v_cache, page_table, cache_len, window, sinks, scale
     if not (1 <= window <= 0x7fffffff and 0 <= sinks <= 0x7fffffff):
         raise ValueError("window must be at least 1 and sinks at least 0")
     scale = d ** -0.5 if scale is None else float(scale)
-    if not math.isfinite(scale):
-        raise ValueError("scale must be finite")
+    if not abs(scale) < 2.0 ** 127:
+        raise ValueError("scale must be finite, and below 2^127 in size")
     return bole_window_dims_t(page_table.shape[0], H, k.shape[1], d, T, k_cache.shape[0],
                               k_cache.shape[2], page_table.shape[1], window, sinks, dt,
                               BOLE_FLAG_FORCE_GENERIC if force_generic else 0, scale)
