@@ -327,7 +327,8 @@ __global__ __launch_bounds__(512, sizeof(TF) == 2 ? 4 : 2) void delta_scan_kerne
                 if (has_part) kr[j].load(reinterpret_cast<const TF *>(k0 + off));
             }
             if (tid < VT && has_v)
-                vr = load16(reinterpret_cast<const __bf16 *>(vb + (size_t)t0 * svb + (uint32_t)min(tid / VP, last) * svb + 16 * (tid % VP)));
+                vr = load16(reinterpret_cast<const __bf16 *>(
+                    vb + (size_t)t0 * svb + (uint32_t)min(tid / VP, last) * svb + 16 * (tid % VP)));
             if (tid >= 224) wr = load16(reinterpret_cast<const __bf16 *>(&w.start[0]) + 8 * (tid - 224));
         };
         auto fetch_q = [&](int t0, int last) {
