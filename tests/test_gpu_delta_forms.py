@@ -1,0 +1,107 @@
+"""The gated delta rule's launch forms that small calls do not reach, against the fp64 oracle:
+the token walk with four columns a lane (batches that fill the chip).
+
+Every row of a sequence is compared: the oracle has to be finite there. Tolerances:
+  - the walk is fp32 throughout. A token's sums have d_k terms, what earlier tokens left decays:
+    states within 2 (d_k + 64) 2^-24 of the head's largest value, outputs within the same part of
+    |q| |H| and the rounding to their type, half a step of it.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import delta as O
+from test_gpu_delta import BF16, F32, check_states, column_norms, dev, g, make, on_gpu, state_tol
+from test_gpu_delta import lib  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+H, HK, B = 16, 4, 65
+
+
+def wide_wavefronts(d_v):
+    return B * H * -(-d_v // 32)
+
+
+def check_rows(got, ref, w):
+    """All rows of all sequences, and no others, have a reference and are within the walk's limits."""
+    T = int(w.offsets[-1])
+    assert np.isfinite(ref[:T]).all() and np.isnan(ref[T:]).all()
+    half = 2.0 ** -8 if w.q.dtype == BF16 else 2.0 ** -24
+    qn = np.repeat(np.linalg.norm(w.q.double().numpy(), axis=-1), w.v.shape[1] // w.q.shape[1], axis=1)
+    lim = half * np.abs(ref[:T]) + (state_tol(w) * qn * column_norms(w)[None])[:T, :, None]
+    e = np.abs(got.double().cpu().numpy()[:T] - ref[:T])
+    assert (e <= lim).all(), float((e / lim).max())
+
+
+def off(x):
+    """The same values one element behind a 16-byte boundary."""
+    return torch.zeros(x.numel() + 8, dtype=x.dtype, device=dev())[1:1 + x.numel()].view(x.shape).copy_(x)
+
+
+# key rows in whole 16-byte parts or not, of 8, 16 and 32 rows a lane, filled or not; a last block
+# of columns that is partly used (40) or whole
+WIDTHS = [(64, 40), (40, 64), (17, 128), (128, 40), (72, 64), (100, 128), (256, 40), (200, 64), (130, 40)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", WIDTHS, ids=str)
+def test_wide_walk(lib, dk, dv, dt):
+    assert wide_wavefronts(dv) >= 2048
+    shape = (H, HK, dk, dv, dt)
+    w = make(201, [1] * B, shape)
+    t = on_gpu(w)
+    out = lib.bole_delta_step(**t)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(t["H0"], S, w)
+    check_rows(out, ref, w)
+
+    sizes = ([5, 0, 9, 1, 12] * B)[:B]
+    w = make(202, sizes, shape, kind="deep", spare_rows=2)
+    t = on_gpu(w)
+    t.pop("q")
+    status = torch.full((B,), -1, dtype=torch.int32, device=dev())
+    nodes = torch.full((B, 16), -9, dtype=torch.int32, device=dev())
+    lib.bole_delta_commit_path(**t, parent=g(w.parent), node_offsets=g(w.offsets),
+                               accepted_idx=g(w.accepted_idx), accepted_len=g(w.accepted_len),
+                               path_nodes=nodes, tree_status=status)
+    assert (w.accepted_len > 1).any() and (w.accepted_len == 0).any()
+    check_states(t["H0"], O.commit(w.H0, w.k, w.v, w.gate, w.beta, w.offsets, w.accepted_idx,
+                                   w.accepted_len), w)
+    want = np.where(w.accepted_idx >= 0, w.accepted_idx + w.offsets[:-1, None], -1)
+    assert np.array_equal(nodes.cpu().numpy(), want) and status.tolist() == [0] * B
+    none = g(w.accepted_len == 0)
+    assert torch.equal(t["H0"][none], g(w.H0)[none])
+
+    w = make(203, ([3, 0, 1, 6] * B)[:B], shape, spare_rows=3)
+    t = on_gpu(w)
+    out = torch.full_like(t["v"], -7.0)
+    lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out, seq_status=status, force_generic=True)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(t["H0"], S, w)
+    check_rows(out, ref, w)
+    assert (out[-3:] == -7.0).all() and status.tolist() == [0] * B
+
+
+@pytest.mark.parametrize("which", ["H0", "k", "v", "gate"])
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_wide_walk_off_16_byte_addresses(lib, which, dt):
+    """A state off 16-byte addresses is walked a column a lane, key rows off them by elements."""
+    shape = (H, HK, 128, 64, dt)
+    w = make(204, [1] * B, shape)
+    t = on_gpu(w)
+    t[which] = off(t[which])
+    if which == "k":
+        t["q"] = off(t["q"])
+    out = lib.bole_delta_step(**t)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(t["H0"], S, w)
+    check_rows(out, ref, w)
+    w = make(205, ([7, 1, 12] * B)[:B], shape, kind="deep")
+    t = on_gpu(w)
+    t.pop("q")
+    t[which] = off(t[which])
+    lib.bole_delta_commit_path(**t, parent=g(w.parent), node_offsets=g(w.offsets),
+                               accepted_idx=g(w.accepted_idx), accepted_len=g(w.accepted_len))
+    check_states(t["H0"], O.commit(w.H0, w.k, w.v, w.gate, w.beta, w.offsets, w.accepted_idx,
+                                   w.accepted_len), w)
