@@ -1,10 +1,15 @@
 """The gated delta rule's launch forms that small calls do not reach, against the fp64 oracle:
-the token walk with four columns a lane (batches that fill the chip).
+the token walk with four columns a lane (batches that fill the chip) and prompts of many chunks.
 
 Every row of a sequence is compared: the oracle has to be finite there. Tolerances:
   - the walk is fp32 throughout. A token's sums have d_k terms, what earlier tokens left decays:
     states within 2 (d_k + 64) 2^-24 of the head's largest value, outputs within the same part of
-    |q| |H| and the rounding to their type, half a step of it.
+    |q| |H| and the rounding to their type, half a step of it;
+  - prompts of many chunks: states by their Frobenius norm. d_k + 64 roundings a token, of `many`
+    tokens' worth that the decays keep, add up as independent ones do:
+    2 sqrt((d_k + 64) many) 2^-24. A chunk's decay has an error in common of two units in its last
+    place, 4 x 2^-24, for each 64 of those tokens. A column's share may be four times the mean's;
+    the rest of an output's limit is test_gpu_delta's.
 """
 import numpy as np
 import pytest
@@ -105,3 +110,45 @@ def test_wide_walk_off_16_byte_addresses(lib, which, dt):
                                accepted_idx=g(w.accepted_idx), accepted_len=g(w.accepted_len))
     check_states(t["H0"], O.commit(w.H0, w.k, w.v, w.gate, w.beta, w.offsets, w.accepted_idx,
                                    w.accepted_len), w)
+
+
+# ---- prompts of many chunks
+
+def state_norm_tol(w, many):
+    return (2.0 * ((w.H0.shape[2] + 64) * many) ** 0.5 + 4.0 * many / 64) * 2.0 ** -24
+
+
+def check_long(out, H0, w, many):
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    T, tol = int(w.offsets[-1]), state_norm_tol(w, many)
+    d = np.linalg.norm(H0.double().cpu().numpy() - S, axis=(2, 3)) / np.linalg.norm(S, axis=(2, 3))
+    print(f"states off by {d.max():.2e} of their norm, limit {tol:.2e}", flush=True)
+    assert d.max() <= tol, d.max()
+    assert np.isfinite(ref[:T]).all()
+    bf = w.q.dtype == BF16
+    lim = (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(ref[:T])
+    if bf:
+        lim = lim + 2.0 ** -8 * O.pair_terms(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)[:T]
+    qn = np.repeat(np.linalg.norm(w.q.double().numpy(), axis=-1), w.v.shape[1] // w.q.shape[1], axis=1)
+    lim = lim + ((4 * tol + (4 * 2.0 ** -16 if bf else 0.0)) * qn * column_norms(w)[None])[:T, :, None]
+    e = np.abs(out.double().cpu().numpy()[:T] - ref[:T])
+    assert (e <= lim).all(), float((e / lim).max())
+
+
+LONG = [(2, 1, 128, 128, BF16), (2, 2, 64, 16, BF16), (1, 1, 72, 40, BF16), (2, 1, 128, 64, F32),
+        (1, 1, 40, 24, F32)]
+LONG_IDS = ["-".join(map(str, s[:4])) + ("-bf16" if s[4] == BF16 else "-f32") for s in LONG]
+
+
+@pytest.mark.parametrize("gate", [None, 0.999], ids=["drawn", "slow"])
+@pytest.mark.parametrize("shape", LONG, ids=LONG_IDS)
+def test_prompts_of_many_chunks(lib, shape, gate):
+    """4,000 tokens, ten chunks with and without a token more, seven and a bit: lines are read
+    three chunks early and dropped, buffers alternate, and states carry over all of it. With a
+    decay of 0.999 a thousand tokens' worth stays."""
+    w = make(211, [4000, 641, 1, 640, 0, 450], shape, spare_rows=3, gate_value=gate)
+    t = on_gpu(w)
+    out = torch.full_like(t["v"], -7.0)
+    lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out)
+    check_long(out, t["H0"], w, 1000.0 if gate else 1.0)
+    assert (out[-3:] == -7.0).all() and torch.equal(t["H0"][4].cpu(), w.H0[4])
