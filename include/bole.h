@@ -485,9 +485,13 @@ BOLE_API bole_status_t bole_tree_accept(const float *p_ctx, const float *p_node,
  *   v     [T][H][d_v]              factor_dtype
  *   gate  float [T][H]             the decay a itself: finite and >= 0, typically in (0, 1]
  *   beta  float [T][H]             the strength b
- *   out   [T][H][d_v]              factor_dtype: what the layer's next product reads. Its
- *                                  rounding is the only one to that type on a row's way to
- *                                  H0; states are fp32 throughout
+ *   out   [T][H][d_v]              factor_dtype: what the layer's next product reads
+ * Roundings: states, and all that they are made from, are kept to fp32 (products of bf16 terms
+ * that leave 2^-25). Outputs are rounded to factor_dtype once, at the end. With bf16 factors
+ * what only outputs see is taken in fewer bits before that: by tree verification the state, the
+ * updates and the pair weights D_{j->i} (q_i . k_j) as two bf16 terms (2^-17 left); by prompts
+ * the first two so, and each pair weight, of tokens of the same 64, rounded to bf16 (half a step
+ * of that term of the output's sum). BOLE_FLAG_FORCE_GENERIC walks a prompt's tokens in fp32.
  * Values must be finite: a NaN or an infinity in one token reaches every token of its
  * sequence (its head alone), earlier ones of the same 64 tokens among them. Gates are not
  * checked. Buffers that a call writes must not overlap any other buffer of that call.

@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from oracle import delta as O
-from test_gpu_delta import BF16, F32, check_states, column_norms, dev, g, make, on_gpu, state_tol
+from test_gpu_delta import BF16, F32, check_prompt, check_states, column_norms, dev, g, make, on_gpu, state_tol
 from test_gpu_delta import lib  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -152,3 +152,16 @@ def test_prompts_of_many_chunks(lib, shape, gate):
     lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out)
     check_long(out, t["H0"], w, 1000.0 if gate else 1.0)
     assert (out[-3:] == -7.0).all() and torch.equal(t["H0"][4].cpu(), w.H0[4])
+
+
+def test_walked_prompt_rounds_its_outputs_alone(lib):
+    """The token walk of a prompt has bf16 outputs within their own rounding, where the chunked
+    kernels also round each pair weight."""
+    w = make(212, [200, 65], (4, 2, 128, 128, BF16))
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    t = on_gpu(w)
+    check_rows(lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), force_generic=True), ref, w)
+    check_states(t["H0"], S, w)
+    t = on_gpu(w)
+    check_prompt(lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets)), ref, w, column_norms(w))
+    check_states(t["H0"], S, w)
