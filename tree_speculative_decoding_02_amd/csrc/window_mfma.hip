@@ -488,9 +488,11 @@ static bool covers(const bole_window_dims_t &d) {
 
 // From a call's sizes alone. The tokens form (bf16) for up to one of its tiles a sequence on
 // average: with 8 rows 189 us against 193 in the rows form (64 sequences), 29 against 33 (8); from
-// 20 rows on 238 against 192, 35 against 35. Parts so that 512 workgroups (two a CU) run, each with
-// 256 keys or more: of 8 single tokens 29 us, with 256 or 768 workgroups 35 and 32; one token in
-// parts of 128 or 512 keys 15 and 14 us against 11.
+// 20 rows on 238 against 192, 35 against 35. Parts so that 512 workgroups (two a CU) run, but no more
+// than one for each 256 keys begun (so that each has more than 128): of 8 single tokens 29 us, with
+// 256 or 768 workgroups 35 and 32; one token in parts of 128 or 512 keys 15 and 14 us against 11.
+// The keys are those that the cache can show a row, and the row's own: lengths are not known here,
+// and a prompt's own rows are not counted, so one behind a short cache runs in one part.
 static WindowPlan plan(const bole_window_dims_t &d) {
     WindowPlan p;
     const int64_t G = d.heads / d.kv_heads, rows = d.total_rows * G;
