@@ -118,3 +118,16 @@ def test_seven_hundred_sequences(lib, shape, cycle):
         check_rows(out, ref, w, 70, 2 * (shape[2] + 2) * 2.0 ** -24 * ref[2], rows)
         assert status.tolist() == [0] * 700 and (out[-2:] == -7.0).all()
         assert out[:T].isfinite().all() and not (out[:T] == -7.0).all(dim=(1, 2)).any()
+
+
+def test_refuses_heads_without_width(lib):
+    """A width of 0 is refused as the other shapes are, with or without a scale."""
+    w = make(148, [2, 1], [20, 5], SHAPES[0], 16, 2)
+    t = {n: x[..., :0].contiguous() if n in ("q", "k", "v", "k_cache", "v_cache") else x
+         for n, x in on_gpu(w).items()}
+    for scale in (None, 1.0):
+        with pytest.raises(ValueError, match="d at least 1"):
+            lib.bole_window_attention(**t, window=16, sinks=2, scale=scale)
+    t.pop("node_offsets")
+    with pytest.raises(ValueError, match="d at least 1"):
+        lib.bole_window_workspace_size(**t, window=16, sinks=2)

@@ -15,8 +15,8 @@ def _dims(q, k, v, k_cache, v_cache, page_table, cache_len, window, sinks, scale
     dt = {torch.bfloat16: BOLE_DTYPE_BF16, torch.float32: BOLE_DTYPE_F32}.get(q.dtype)
     if dt is None:
         raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
-    if q.dim() != 3:
-        raise ValueError("q must be [T, H, d]")
+    if q.dim() != 3 or q.shape[2] < 1:
+        raise ValueError("q must be [T, H, d] with d at least 1")
     T, H, d = q.shape
     _need(k, "k", q.dtype, dev)
     if k.dim() != 3 or k.shape[0] != T or k.shape[2] != d or k.shape[1] < 1 or H % k.shape[1] != 0:
