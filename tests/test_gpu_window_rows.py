@@ -1,6 +1,6 @@
 """Windowed attention against the fp64 oracle, every row of every sequence compared: large scores
 within limits that their arithmetic gives, scores past fp32, more sequences than a call's first
-look through its offsets takes.
+look through its offsets takes, widths and head groups beside test_gpu_window's.
 
 Large scores: q and k are whole numbers whose products' sums stay below 2^24, so that q . k is exact
 in fp32 in any order and in both types. What is left of a score's error is relative to it: the
@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from oracle import window as O
-from test_gpu_window import BF16, SHAPES, IDS, dev, g, make, on_gpu, oracle_of
+from test_gpu_window import BF16, F32, SHAPES, IDS, dev, g, make, on_gpu, oracle_of
 from test_gpu_window import lib  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -118,6 +118,29 @@ def test_seven_hundred_sequences(lib, shape, cycle):
         check_rows(out, ref, w, 70, 2 * (shape[2] + 2) * 2.0 ** -24 * ref[2], rows)
         assert status.tolist() == [0] * 700 and (out[-2:] == -7.0).all()
         assert out[:T].isfinite().all() and not (out[:T] == -7.0).all(dim=(1, 2)).any()
+
+
+MORE = [(4, 2, 64, 16, F32), (6, 2, 96, 32, F32), (3, 1, 96, 8, BF16), (64, 1, 64, 16, BF16),
+        (71, 1, 128, 16, BF16), (130, 1, 64, 32, BF16), (130, 2, 96, 16, F32), (200, 1, 128, 8, F32)]
+MORE_IDS = ["-".join(map(str, s[:4])) + ("-bf16" if s[4] == BF16 else "-f32") for s in MORE]
+
+
+@pytest.mark.parametrize("window,sinks", [(40, 3), (2**31 - 1, 0)], ids=str)
+@pytest.mark.parametrize("shape", MORE, ids=MORE_IDS)
+def test_more_widths_and_groups(lib, shape, window, sinks):
+    """fp32 of every width with a matrix-core kernel; groups of more query heads than a tile has
+    rows, whose rows lie in several tiles."""
+    for seed, sizes, cached, tree in ((151, [1, 1, 1], [300, 64, 0], False),
+                                      (152, [9, 0, 3, 33], [70, 10, 0, 129], True),
+                                      (153, [40, 1, 0, 5], [0, 90, 10, 65], False)):
+        w = make(seed, sizes, cached, shape, window, sinks, spare_rows=2)
+        t = on_gpu(w)
+        out, status = torch.full_like(t["q"], -7.0), torch.full((len(sizes),), -1, dtype=torch.int32, device=dev())
+        lib.bole_window_attention(**t, window=window, sinks=sinks, out=out, seq_status=status,
+                                  parent=g(w.parent) if tree else None)
+        ref = oracle_of(w, window, sinks, tree)
+        check_rows(out, ref, w, 310, 2 * (shape[2] + 2) * 2.0 ** -24 * ref[2])
+        assert (out[-2:] == -7.0).all() and status.tolist() == [0] * len(sizes)
 
 
 def test_refuses_heads_without_width(lib):
