@@ -1,5 +1,6 @@
 """The gated delta rule's launch forms that small calls do not reach, against the fp64 oracle:
-the token walk with four columns a lane (batches that fill the chip) and prompts of many chunks.
+the token walk with four columns a lane (batches that fill the chip), widths of the matrix-core
+kernels beside test_gpu_delta's, and prompts of many chunks.
 
 Every row of a sequence is compared: the oracle has to be finite there. Tolerances:
   - the walk is fp32 throughout. A token's sums have d_k terms, what earlier tokens left decays:
@@ -16,7 +17,8 @@ import pytest
 import torch
 
 from oracle import delta as O
-from test_gpu_delta import BF16, F32, check_prompt, check_states, column_norms, dev, g, make, on_gpu, state_tol
+from test_gpu_delta import (BF16, F32, check_out, check_prompt, check_states, column_norms, dev, g, make,
+                            on_gpu, state_tol)
 from test_gpu_delta import lib  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -110,6 +112,49 @@ def test_wide_walk_off_16_byte_addresses(lib, which, dt):
                                accepted_idx=g(w.accepted_idx), accepted_len=g(w.accepted_len))
     check_states(t["H0"], O.commit(w.H0, w.k, w.v, w.gate, w.beta, w.offsets, w.accepted_idx,
                                    w.accepted_len), w)
+
+
+# ---- widths in pairs of columns, and fp32 ones, of the matrix-core kernels
+
+MORE = [(4, 2, 64, 128, BF16), (2, 1, 40, 96, BF16), (2, 2, 72, 160, BF16), (4, 2, 64, 128, F32),
+        (2, 1, 40, 96, F32), (2, 1, 72, 160, F32), (3, 3, 64, 64, F32), (2, 2, 72, 40, F32),
+        (2, 1, 120, 200, F32)]
+MORE_IDS = ["-".join(map(str, s[:4])) + ("-bf16" if s[4] == BF16 else "-f32") for s in MORE]
+
+
+@pytest.mark.parametrize("shape", MORE, ids=MORE_IDS)
+def test_more_widths(lib, shape):
+    """Prompts and trees of widths that test_gpu_delta's shapes leave out."""
+    w = make(221, [65, 0, 1, 63, 130], shape, spare_rows=3)
+    t = on_gpu(w)
+    out = torch.full_like(t["v"], -7.0)
+    lib.bole_delta_prefill(**t, seq_offsets=g(w.offsets), out=out)
+    ref, S = O.prefill(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.offsets)
+    check_states(t["H0"], S, w)
+    assert np.isfinite(ref[:-3]).all()
+    check_prompt(out, ref, w, column_norms(w))
+    assert (out[-3:] == -7.0).all()
+    for kind in ("random", "chain"):
+        w = make(222, [64, 33, 0, 5, 16, 49], shape, kind=kind, spare_rows=2)
+        t = on_gpu(w)
+        out = torch.full_like(t["v"], -7.0)
+        lib.bole_delta_tree_verify(**t, parent=g(w.parent), node_offsets=g(w.offsets), out=out)
+        ref = O.verify(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.parent, w.offsets)
+        assert np.isfinite(ref[:-2]).all()
+        check_out(out, ref, w, column_norms(w))
+        assert (out[-2:] == -7.0).all() and torch.equal(t["H0"].cpu(), w.H0)
+
+
+@pytest.mark.parametrize("shape", [MORE[0], MORE[2], MORE[5]], ids=[MORE_IDS[0], MORE_IDS[2], MORE_IDS[5]])
+def test_tree_verify_off_16_byte_addresses(lib, shape):
+    w = make(223, [64, 20, 7], shape)
+    t = on_gpu(w)
+    a = dict(parent=g(w.parent), node_offsets=g(w.offsets))
+    ref = O.verify(w.H0, w.q, w.k, w.v, w.gate, w.beta, w.parent, w.offsets)
+    for which in ("H0", "q", "k", "v", "gate", "beta", "out"):
+        u = dict(t, out=torch.zeros_like(t["v"]))
+        u[which] = off(u[which])
+        check_out(lib.bole_delta_tree_verify(**u, **a), ref, w, column_norms(w))
 
 
 # ---- prompts of many chunks
