@@ -45,8 +45,8 @@ struct PrefillArgs {
 
 // One workgroup a chunk and value head. Most of its time is waiting, for rows, sums and the inverse's
 // steps, so what counts is how many run: 33 KB of LDS and up to 128 registers are four a CU. (One
-// 32768-token prompt of 32 heads, 16384 systems: 199 us, 0.4 GB written; with P in LDS and K's rows
-// from the caches three a CU and 249 us.)
+// 32768-token prompt of 32 heads, 16384 systems: 199 us, 181 with warm clocks, 0.4 GB written; with P
+// in LDS and K's rows from the caches three a CU and 249 us.)
 template <typename TF, int DK, bool WHOLE>
 __global__ __launch_bounds__(256, sizeof(TF) == 2 ? 4 : 2) void delta_chunk_kernel(const PrefillArgs<TF> a) {
     __shared__ DeltaTokens t;
@@ -112,7 +112,7 @@ __device__ __forceinline__ int k_at(int row, int c) {
                                           : (((row >> 1) & 1) << 2 | ((row >> 3) & 3))));
 }
 
-// One workgroup: eight wavefronts, 16 state columns. What bounds it is the chain of a chunk's
+// One workgroup: eight wavefronts, 16 state columns. What bounds one alone is the chain of a chunk's
 // steps (K S, then U, then the state), so four wavefronts do only these: wavefront w has the
 // tokens of row tile w and the state rows of d_k / 64 row tiles, and what it computes becomes
 // the others' operand through LDS (S, then R, then U; three barriers a chunk). In operand
@@ -124,6 +124,9 @@ __device__ __forceinline__ int k_at(int row, int c) {
 // which LDS is at work for half and the matrix cores for a quarter; 2.1 us with four wavefronts that
 // do everything, 4.6 us with wavefronts that do all 64 tokens of 16 columns of their own and
 // exchange nothing, 1.6 us with K S in parts by state rows (no exchange of S, one of the sums).
+// A second workgroup on the CU hides nothing: of 8192-token prompts one takes 188 us, two (two
+// workgroups a CU) 360, four 706, with the units as busy as before (LDS 49 %, vector ALU 38 %, matrix
+// cores 27 %). There the CU's throughput counts: 2.8 us for a step of both.
 //
 // fp32 factors: K lies in LDS as three bf16 terms, Q, U and P are taken as three too, and every
 // product as the six of them that reach 2^-24; one workgroup a CU.

@@ -24,9 +24,9 @@
 // merges the parts.
 //
 // Measured, 32 query heads over 8 key heads of 128, a window of 4096 (prompts: 1024) and 4 first
-// tokens: 64 single tokens 163 us (5.7 TB/s), 64 draft trees of up to 32 nodes 172 us (5.4 TB/s),
+// tokens: 64 single tokens 162 us (5.7 TB/s), 64 draft trees of up to 32 nodes 171 us (5.4 TB/s),
 // both bound by the cache's bytes; one single token 11 us, its two kernels' chains of loads; two
-// prompts of 8192 tokens 365 us (756 TFLOP/s). Of those the matrix instructions alone take 177,
+// prompts of 8192 tokens 363 us (761 TFLOP/s). Of those the matrix instructions alone take 177,
 // with LDS reads and exponentials 266; the rest is keys on their way through registers to LDS.
 #include "window_tile.h"
 #include "launch.h"

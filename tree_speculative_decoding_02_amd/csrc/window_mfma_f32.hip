@@ -8,7 +8,8 @@
 // One workgroup: 64 rows, 16 a wavefront, keys and values staged in LDS 64 at a time, the next
 // 64 in registers meanwhile. The fp32 matrix rate (a sixteenth of bf16's) bounds prompts and
 // trees, the cache's bytes single tokens: 32 heads over 8 of 128, a window of 4096, 64 single
-// tokens 457 us (4.0 TB/s), 32 trees of up to 32 nodes 484 us (43 TFLOP/s).
+// tokens 442 us (4.2 TB/s), 64 trees of up to 32 nodes 1077 us (45 TFLOP/s, the matrix instructions
+// at work half of the time); two prompts of 2048 tokens, window 1024, 679 us (102 TFLOP/s).
 #include "window_tile.h"
 #include "launch.h"
 
