@@ -630,6 +630,210 @@ BOLE_API bole_status_t bole_window_attention(const void *q, const void *k, const
                                const bole_window_dims_t *dims, int32_t *seq_status,
                                bole_stream_t stream);
 
+/*
+ * Linear attention with a decay: prompts and single tokens of the layers whose draft trees
+ * bole_tree_verify and bole_commit_path take. For one head, state H [d_k][d_v], token with key k,
+ * value v, query q and decay a (a number a head, or one for each key channel, which scales the
+ * state's rows):
+ *     H <- a H + k v^T,   o = H^T q   (taken after the token's own update).
+ * Value head h reads key head h / (heads / key_heads). q is used as given: a scale is the caller's.
+ *
+ * Layouts, row-major and contiguous in device memory:
+ *   H0    float [B][H][d_k][d_v]   state of each sequence and value head
+ *   q, k  [T][H_k][d_k]            factor_dtype (bf16 or fp32)
+ *   v     [T][H][d_v]              factor_dtype
+ *   gate  float [T][H] (BOLE_GATE_SCALAR) or [T][H][d_k] (BOLE_GATE_VECTOR): the decay itself,
+ *         finite and >= 0, typically in (0, 1]
+ *   out   [T][H][d_v]              factor_dtype: what the layer's next product reads
+ * With H_k = H and out in fp32 these are the layouts of bole_dims_t.
+ * Roundings: states, and all that they are made from, are kept to fp32 (products of bf16 terms
+ * that leave 2^-25). Outputs are rounded to factor_dtype once, at the end. With bf16 factors a
+ * prompt's outputs see the state before their 64 tokens as two bf16 terms (2^-17 left), and the
+ * weights D_{j->i} (q_i . k_j) of tokens of the same 64 rounded to bf16 (half a step of that term
+ * of the output's sum). BOLE_FLAG_FORCE_GENERIC walks a prompt's tokens in fp32, as do prompts
+ * with BOLE_GATE_VECTOR.
+ * Values must be finite: a NaN or an infinity in one token may reach every token of its sequence
+ * (its head alone), earlier ones of the same 64 tokens among them. Gates are not checked. Buffers
+ * that a call writes must not overlap any other buffer of that call. Rows that belong to no
+ * sequence are neither read nor written.
+ */
+typedef struct {
+    int32_t batch;        /* B >= 0 sequences */
+    int32_t heads;        /* H >= 1 value heads */
+    int32_t key_heads;    /* H_k >= 1, a divisor of heads */
+    int32_t d_k;          /* key width = state rows, 1..256 */
+    int32_t d_v;          /* value width = state columns, 1..256 */
+    int32_t total_tokens; /* T >= 0, rows of the packed arrays */
+    int32_t factor_dtype; /* bole_dtype_t of q, k, v and out */
+    int32_t gate_kind;    /* bole_gate_kind_t */
+    int32_t flags;        /* 0 or BOLE_FLAG_FORCE_GENERIC */
+} bole_linear_dims_t;
+
+/* Host-only check of the dims, the same check both entry points run first. `op` is 0 for
+ * prefill, 1 for step. */
+BOLE_API bole_status_t bole_linear_check_dims(const bole_linear_dims_t *dims, int32_t op);
+
+/*
+ * Prompts: every token of every sequence, in order, from the state H0 of the sequence, which is
+ * replaced by the state after its last token. seq_offsets, seq_status and workspace follow
+ * bole_delta_prefill (bole_linear_prefill_workspace_size(dims) bytes).
+ */
+BOLE_API size_t bole_linear_prefill_workspace_size(const bole_linear_dims_t *dims);
+BOLE_API bole_status_t bole_linear_prefill(float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, const int32_t *seq_offsets, void *out,
+                               void *workspace, size_t workspace_bytes,
+                               const bole_linear_dims_t *dims, int32_t *seq_status,
+                               bole_stream_t stream);
+
+/* One token a sequence: row b belongs to sequence b (total_tokens has to equal batch). */
+BOLE_API bole_status_t bole_linear_step(float *H0, const void *q, const void *k, const void *v,
+                               const float *gate, void *out, const bole_linear_dims_t *dims,
+                               bole_stream_t stream);
+
+/*
+ * Norm and rotation of queries and keys, one pass: what an attention layer does with them between
+ * its projection and bole_window_attention or bole_prefix_attention. For each row and head x[d]:
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ * (weight NULL: neither the norm nor a weight), then, with position p and the angle
+ * t = p inv_freq[j], pair j of the first rotary_dim dimensions turns by t:
+ *     (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ * where (a, b) = (j, j + rotary_dim / 2), or (2 j, 2 j + 1) under BOLE_FLAG_INTERLEAVED. The other
+ * dimensions are not turned. rotary_dim 0: no rotation.
+ * Row i of sequence b is at position first_position[b] + i, or, with a parent array (draft trees
+ * as bole_tree_verify takes them, of up to 64 nodes), first_position[b] + (nodes on its path) - 1.
+ * Angles are taken in fp64 and reduced to one turn before they are rounded to fp32.
+ *
+ *   q, k          rows q_stride and k_stride elements apart, each [heads][d] and [kv_heads][d]:
+ *                 they may lie side by side, as one projection leaves them
+ *   q_weight, k_weight  [d]            dtype; either may be NULL
+ *   inv_freq      float [rotary_dim / 2]
+ *   first_position int32 [B], >= 0;   node_offsets int32 [B + 1]
+ *   q_out, k_out  [T][heads][d] and [T][kv_heads][d], dtype; may be q and k themselves where
+ *                 those are contiguous, and must not overlap any other buffer of the call
+ * Sums, norms and rotations are fp32; outputs are rounded once. A NaN stays in its own head.
+ * Statuses and errors follow bole_window_attention: BOLE_TREE_BAD_SIZE leaves the rows untouched,
+ * rows of a bad-parent tree, and of a sequence whose first_position is negative or so large that
+ * first_position + rows - 1 passes 2^31 - 1 (BOLE_TREE_BAD_CACHE), become NaN.
+ */
+enum { BOLE_FLAG_INTERLEAVED = 8 };
+
+typedef struct {
+    int32_t batch;       /* B >= 0 sequences */
+    int32_t heads;       /* >= 1 query heads */
+    int32_t kv_heads;    /* >= 1 key heads */
+    int32_t head_dim;    /* d, 1..256 */
+    int32_t rotary_dim;  /* even, 0..d */
+    int32_t total_rows;  /* T >= 0 */
+    int32_t dtype;       /* bole_dtype_t */
+    int32_t flags;       /* BOLE_FLAG_FORCE_GENERIC, BOLE_FLAG_INTERLEAVED */
+    int64_t q_stride;    /* elements from a row of q to the next, >= heads d */
+    int64_t k_stride;    /* of k, >= kv_heads d */
+    float eps;           /* finite, >= 0 */
+} bole_rotary_dims_t;
+
+/* Host-only check of the dims, the same check the entry point runs first. */
+BOLE_API bole_status_t bole_rotary_check_dims(const bole_rotary_dims_t *dims);
+BOLE_API bole_status_t bole_qk_norm_rotary(const void *q, const void *k, const void *q_weight,
+                               const void *k_weight, const float *inv_freq,
+                               const int32_t *first_position, const int32_t *parent,
+                               const int32_t *node_offsets, void *q_out, void *k_out,
+                               const bole_rotary_dims_t *dims, int32_t *seq_status,
+                               bole_stream_t stream);
+
+/*
+ * Attention of sequences that share a long prefix: the prefix's keys and values are read once for
+ * all rows of the sequences that share it, and the softmax is joined with that over each
+ * sequence's own tokens. Every key is seen: there is no window.
+ *
+ * Group g owns sequences group_offsets[g] .. group_offsets[g+1]-1, whose first prefix_len[g] tokens
+ * lie in the pages of prefix_table[g]. Behind them sequence b has cache_len[b] tokens of its own in
+ * the pages of page_table[b] (position s of either is row s % page_size of its page s / page_size),
+ * and rows node_offsets[b] .. node_offsets[b+1]-1 of q, k and v, a draft tree with a parent array
+ * or its next tokens without one, as bole_window_attention takes them. A row sees its group's
+ * prefix, its sequence's cached tokens, itself and the rows on its path before it;
+ *     out = sum_s w_s v_s,   w = softmax over the seen keys of scale (q . k_s).
+ * Sequences before the first group's and behind the last one's have no prefix; groups 0 is a batch
+ * without any.
+ *
+ * Layouts, types, roundings, workspace and errors follow bole_window_attention, with
+ *   prefix_table int32 [groups][max_prefix_pages],  prefix_len int32 [groups],
+ *   group_offsets int32 [groups + 1].
+ * Offsets of either kind have to be ordered and inside [0, T] and [0, B]: if any are not, every
+ * sequence is reported BOLE_TREE_BAD_SIZE and nothing is written. A prefix_len outside
+ * [0, max_prefix_pages page_size], or a page of a prefix that is not in [0, num_pages), makes every
+ * sequence of the group that has rows BOLE_TREE_BAD_CACHE, as its own cache would. A prefix that no
+ * row sees is not checked. A NaN or an infinity in a value of a prefix may reach all rows that see it.
+ */
+typedef struct {
+    int32_t batch;       /* B >= 0 sequences */
+    int32_t heads;       /* H >= 1 query heads */
+    int32_t kv_heads;    /* H_kv >= 1, a divisor of heads */
+    int32_t head_dim;    /* d, 1..256 */
+    int32_t total_rows;  /* T >= 0, rows of the packed arrays */
+    int32_t num_pages;   /* pages of the cache, >= 0 */
+    int32_t page_size;   /* positions a page, a power of two from 1 to 1024 */
+    int32_t max_pages;   /* row stride of page_table, >= 0 */
+    int32_t groups;      /* >= 0 */
+    int32_t max_prefix_pages; /* row stride of prefix_table, >= 0 */
+    int32_t dtype;       /* bole_dtype_t */
+    int32_t flags;       /* 0 or BOLE_FLAG_FORCE_GENERIC */
+    float scale;         /* below 2^127 in size */
+} bole_prefix_dims_t;
+
+/* Host-only check of the dims, the same check the entry point runs first. */
+BOLE_API bole_status_t bole_prefix_check_dims(const bole_prefix_dims_t *dims);
+BOLE_API size_t bole_prefix_workspace_size(const bole_prefix_dims_t *dims);
+BOLE_API bole_status_t bole_prefix_attention(const void *q, const void *k, const void *v,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *prefix_table, const int32_t *prefix_len,
+                               const int32_t *group_offsets, const int32_t *page_table,
+                               const int32_t *cache_len, const int32_t *parent,
+                               const int32_t *node_offsets, void *out, void *workspace,
+                               size_t workspace_bytes, const bole_prefix_dims_t *dims,
+                               int32_t *seq_status, bole_stream_t stream);
+
+/*
+ * New tokens into the paged cache that bole_window_attention and bole_prefix_attention read: of
+ * sequence b, in order,
+ *  - with accepted_idx and accepted_len (as bole_commit_path takes them, with the trees' parent
+ *    array), the rows of the accepted path;
+ *  - without them (and without parent), all its rows node_offsets[b] .. node_offsets[b+1]-1.
+ * The m-th goes to position cache_len[b] + m: row s % page_size of page page_table[b][s / page_size].
+ * new_len int32 [B] (may be NULL) receives cache_len[b] plus the rows added; cache_len is not
+ * written, so that every layer's call reads the same one.
+ *   k, v          rows k_stride and v_stride elements apart, each [kv_heads][d]
+ *   k_cache, v_cache  [num_pages][kv_heads][page_size][d]
+ * seq_status (int32 [B], may be NULL): BOLE_TREE_BAD_SIZE (offsets), BAD_PARENT, BAD_PATH as
+ * bole_commit_path reports them; BOLE_TREE_BAD_CACHE where cache_len is negative, the new tokens
+ * pass max_pages page_size, or a page that one goes to is not in [0, num_pages). A bad sequence
+ * adds nothing (its new_len is its cache_len). Without a path, offsets have to be ordered and inside
+ * [0, T]: if any are not, every sequence is BOLE_TREE_BAD_SIZE. Positions of two sequences in one
+ * row of a page, and buffers that overlap, are not allowed. Values are copied as they are.
+ */
+typedef struct {
+    int32_t batch;       /* B >= 0 sequences */
+    int32_t kv_heads;    /* >= 1 */
+    int32_t head_dim;    /* d, 1..256 */
+    int32_t total_rows;  /* T >= 0 */
+    int32_t num_pages;   /* >= 0 */
+    int32_t page_size;   /* a power of two from 1 to 1024 */
+    int32_t max_pages;   /* row stride of page_table, >= 0 */
+    int32_t max_path;    /* row stride of accepted_idx, 0..64; 0 without paths */
+    int32_t dtype;       /* bole_dtype_t */
+    int32_t flags;       /* 0 */
+    int64_t k_stride;    /* elements from a row of k to the next, >= kv_heads d */
+    int64_t v_stride;    /* of v */
+} bole_append_dims_t;
+
+/* Host-only check of the dims, the same check the entry point runs first. */
+BOLE_API bole_status_t bole_append_check_dims(const bole_append_dims_t *dims);
+BOLE_API bole_status_t bole_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                               const int32_t *page_table, const int32_t *cache_len,
+                               const int32_t *parent, const int32_t *node_offsets,
+                               const int32_t *accepted_idx, const int32_t *accepted_len,
+                               int32_t *new_len, const bole_append_dims_t *dims,
+                               int32_t *seq_status, bole_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

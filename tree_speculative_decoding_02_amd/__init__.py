@@ -12,8 +12,16 @@ from .delta import (bind_delta_commit_path, bind_delta_prefill, bind_delta_step,
                     bole_delta_prefill_workspace_size, bole_delta_step, bole_delta_tree_verify)
 from .window import (bind_window_attention, bole_window_attention,
                      bole_window_workspace_size)
+from .linear import (bind_linear_prefill, bind_linear_step, bole_linear_prefill,
+                     bole_linear_prefill_workspace_size, bole_linear_step)
+from .paged import (bind_cache_append, bind_prefix_attention, bind_qk_norm_rotary, bole_cache_append,
+                    bole_prefix_attention, bole_prefix_workspace_size, bole_qk_norm_rotary)
 
-__all__ = ["bind_window_attention", "bole_window_attention", "bole_window_workspace_size",
+__all__ = ["bind_linear_prefill", "bind_linear_step", "bole_linear_prefill",
+           "bole_linear_prefill_workspace_size", "bole_linear_step",
+           "bind_cache_append", "bind_prefix_attention", "bind_qk_norm_rotary", "bole_cache_append",
+           "bole_prefix_attention", "bole_prefix_workspace_size", "bole_qk_norm_rotary",
+           "bind_window_attention", "bole_window_attention", "bole_window_workspace_size",
            "bind_delta_commit_path", "bind_delta_prefill", "bind_delta_step",
            "bind_delta_tree_verify", "bole_delta_commit_path", "bole_delta_prefill",
            "bole_delta_prefill_workspace_size", "bole_delta_step", "bole_delta_tree_verify",

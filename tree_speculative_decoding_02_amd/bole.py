@@ -21,6 +21,7 @@ BOLE_GATE_SCALAR, BOLE_GATE_VECTOR = 0, 1
 BOLE_FLAG_FORCE_GENERIC = 1
 BOLE_FLAG_TREES_LE_32 = 2
 BOLE_FLAG_VALIDATE_GATES = 4
+BOLE_FLAG_INTERLEAVED = 8
 MAX_TREE_NODES = 64
 
 EXPORTED = ("bole_max_tree_nodes", "bole_status_string", "bole_check_dims",
@@ -32,7 +33,11 @@ EXPORTED = ("bole_max_tree_nodes", "bole_status_string", "bole_check_dims",
             "bole_tree_accept", "bole_delta_check_dims", "bole_delta_prefill_workspace_size",
             "bole_delta_prefill", "bole_delta_step", "bole_delta_tree_verify",
             "bole_delta_commit_path", "bole_window_check_dims", "bole_window_workspace_size",
-            "bole_window_attention")
+            "bole_window_attention",
+            "bole_linear_check_dims", "bole_linear_prefill_workspace_size", "bole_linear_prefill",
+            "bole_linear_step", "bole_rotary_check_dims", "bole_qk_norm_rotary",
+            "bole_prefix_check_dims", "bole_prefix_workspace_size", "bole_prefix_attention",
+            "bole_append_check_dims", "bole_cache_append")
 BOLE_ACCEPT_GREEDY, BOLE_ACCEPT_SAMPLE = 0, 1
 BOLE_BUILD_FIXED_BUDGET = 1
 
@@ -80,6 +85,39 @@ class bole_window_dims_t(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class bole_linear_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("key_heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("factor_dtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class bole_rotary_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("total_rows", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class bole_prefix_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("total_rows", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("max_prefix_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class bole_append_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("total_rows", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_path", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 class BoleError(RuntimeError):
@@ -151,6 +189,32 @@ def _load():
     lib.bole_window_workspace_size.argtypes = [WD]
     lib.bole_window_attention.restype = ctypes.c_int
     lib.bole_window_attention.argtypes = [P] * 11 + [SZ, WD, P, P]
+    LD = ctypes.POINTER(bole_linear_dims_t)
+    lib.bole_linear_check_dims.restype = ctypes.c_int
+    lib.bole_linear_check_dims.argtypes = [LD, I32]
+    lib.bole_linear_prefill_workspace_size.restype = SZ
+    lib.bole_linear_prefill_workspace_size.argtypes = [LD]
+    lib.bole_linear_prefill.restype = ctypes.c_int
+    lib.bole_linear_prefill.argtypes = [P] * 8 + [SZ, LD, P, P]
+    lib.bole_linear_step.restype = ctypes.c_int
+    lib.bole_linear_step.argtypes = [P] * 6 + [LD, P]
+    RD = ctypes.POINTER(bole_rotary_dims_t)
+    lib.bole_rotary_check_dims.restype = ctypes.c_int
+    lib.bole_rotary_check_dims.argtypes = [RD]
+    lib.bole_qk_norm_rotary.restype = ctypes.c_int
+    lib.bole_qk_norm_rotary.argtypes = [P] * 10 + [RD, P, P]
+    XD = ctypes.POINTER(bole_prefix_dims_t)
+    lib.bole_prefix_check_dims.restype = ctypes.c_int
+    lib.bole_prefix_check_dims.argtypes = [XD]
+    lib.bole_prefix_workspace_size.restype = SZ
+    lib.bole_prefix_workspace_size.argtypes = [XD]
+    lib.bole_prefix_attention.restype = ctypes.c_int
+    lib.bole_prefix_attention.argtypes = [P] * 14 + [SZ, XD, P, P]
+    CD = ctypes.POINTER(bole_append_dims_t)
+    lib.bole_append_check_dims.restype = ctypes.c_int
+    lib.bole_append_check_dims.argtypes = [CD]
+    lib.bole_cache_append.restype = ctypes.c_int
+    lib.bole_cache_append.argtypes = [P] * 11 + [CD, P, P]
     return lib
 
 

@@ -35,33 +35,6 @@ struct WalkArgs {
     int max_path;
 };
 
-// How key rows are laid out for loads: of any width and address; in 16-byte parts, on 16-byte
-// addresses; and of d_k = 8 RPL as well. (Parts against single elements, 128 steps of 32 heads:
-// 96 x 96 in bf16 59.8 -> 55.2 us, 72 x 40 29.2 -> 23.1; one step 5.6 -> 3.7 and 6.4 -> 4.5.)
-enum { kAnyRow = 0, kParts = 1, kExact = 2 };
-
-// Lane's RPL key-row values, row rg RPL + i (zero past d_k).
-template <typename TF, int RPL, int ROW>
-struct RowPiece {
-    TF x[RPL];
-    __device__ __forceinline__ void load(const TF *p, int r0, int DK) {
-        if constexpr (ROW != kAnyRow) {
-            constexpr int V = 16 / sizeof(TF);
-            typedef TF vec __attribute__((ext_vector_type(V)));
-#pragma unroll
-            for (int i = 0; i < RPL; i += V) {
-                const bool in = ROW == kExact || r0 + i < DK;
-                const vec t = *reinterpret_cast<const vec *>(p + (in ? r0 + i : 0));
-#pragma unroll
-                for (int j = 0; j < V; ++j) x[i + j] = in ? t[j] : (TF)0.f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < RPL; ++i) x[i] = r0 + i < DK ? p[r0 + i] : (TF)0.f;
-        }
-    }
-};
-
 template <int MODE, typename TF, int RPL, int CPL, int ROW>
 __global__ __launch_bounds__(256) void delta_walk_kernel(const WalkArgs a, int units, int blocks) {
     typedef float hvec __attribute__((ext_vector_type(CPL)));

@@ -144,4 +144,36 @@ hipError_t launch_window(const void *q, const void *k, const void *v, const void
                          void *workspace, const bole_window_dims_t &d, int32_t *seq_status,
                          hipStream_t stream);
 
+// Linear attention with a decay (linear_prefill.hip, linear_walk.hip).
+size_t linear_prefill_workspace(const bole_linear_dims_t &d);
+hipError_t launch_linear_prefill(float *H0, const void *q, const void *k, const void *v,
+                                 const float *gate, const int32_t *seq_offsets, void *out,
+                                 void *workspace, const bole_linear_dims_t &d, int32_t *seq_status,
+                                 hipStream_t stream);
+hipError_t launch_linear_step(float *H0, const void *q, const void *k, const void *v,
+                              const float *gate, void *out, const bole_linear_dims_t &d,
+                              hipStream_t stream);
+
+// Norm and rotation of queries and keys (rotary.hip).
+hipError_t launch_rotary(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                         const float *inv_freq, const int32_t *first_position, const int32_t *parent,
+                         const int32_t *node_offsets, void *q_out, void *k_out,
+                         const bole_rotary_dims_t &d, int32_t *seq_status, hipStream_t stream);
+
+// New tokens into the cache (append.hip).
+hipError_t launch_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                         const int32_t *page_table, const int32_t *cache_len, const int32_t *parent,
+                         const int32_t *node_offsets, const int32_t *accepted_idx,
+                         const int32_t *accepted_len, int32_t *new_len, const bole_append_dims_t &d,
+                         int32_t *seq_status, hipStream_t stream);
+
+// Attention behind shared prefixes (prefix_attention.hip).
+size_t prefix_workspace(const bole_prefix_dims_t &d);
+hipError_t launch_prefix(const void *q, const void *k, const void *v, const void *k_cache,
+                         const void *v_cache, const int32_t *prefix_table, const int32_t *prefix_len,
+                         const int32_t *group_offsets, const int32_t *page_table,
+                         const int32_t *cache_len, const int32_t *parent, const int32_t *node_offsets,
+                         void *out, void *workspace, const bole_prefix_dims_t &d, int32_t *seq_status,
+                         hipStream_t stream);
+
 }  // namespace bole

@@ -1,0 +1,46 @@
+// prefix_device.h - arguments of attention behind shared prefixes.
+#pragma once
+
+#include "window_device.h"
+
+namespace bole {
+
+struct PrefixArgs {
+    WindowArgs w;                    // own tokens: a window of everything, no first tokens
+    const int32_t *prefix_table, *prefix_len, *group_offsets;
+    int groups, max_prefix_pages;
+};
+
+// Sequences [b0, b1) of group g share the prefix of len tokens; found: the sequence has one.
+struct Group {
+    bool found;
+    int g, len;
+};
+
+// The group of sequence b (ordered group offsets).
+__device__ __forceinline__ Group group_of(const PrefixArgs &a, int b) {
+    Group x = {false, 0, 0};
+    if (a.groups == 0) return x;
+    x.g = sequence_of(a.group_offsets, a.groups, b);
+    x.found = a.group_offsets[x.g] <= b && b < a.group_offsets[x.g + 1];
+    if (x.found) x.len = a.prefix_len[x.g];
+    return x;
+}
+
+// Whether prefix g of len tokens lies in pages that exist. One wavefront.
+__device__ __forceinline__ int prefix_status(const PrefixArgs &a, int g, int len) {
+    const int shift = a.w.s.page_shift;
+    if (len < 0 || len > ((int64_t)a.max_prefix_pages << shift)) return BOLE_TREE_BAD_CACHE;
+    const int32_t *table = a.prefix_table + (size_t)g * a.max_prefix_pages;
+    const int pages = (int)(((int64_t)len + (1 << shift) - 1) >> shift);
+    bool bad = false;
+    for (int i = lane_id(); i < pages; i += 64) bad |= (unsigned)table[i] >= (unsigned)a.w.s.pages;
+    return __any(bad) ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
+}
+
+// The matrix-core kernels (prefix_mfma.hip).
+bool prefix_mfma_applies(const bole_prefix_dims_t &d, const PrefixArgs &a);
+hipError_t launch_prefix_mfma(const PrefixArgs &a, const bole_prefix_dims_t &d, void *workspace,
+                              hipStream_t stream);
+
+}  // namespace bole

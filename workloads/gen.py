@@ -452,3 +452,81 @@ def make_window(seed: int, sizes: Sequence[int], cached: Sequence[int], heads: i
     return WindowWorkload(q, k, v, _cast(kc, dtype), _cast(vc, dtype),
                           torch.from_numpy(table.astype(np.int32)),
                           torch.tensor(list(map(int, cached)), dtype=torch.int32), offs, parent)
+
+
+@dataclass
+class LinearWorkload:
+    """Inputs of linear attention with a decay: packed rows of prompts or single tokens."""
+    H0: torch.Tensor           # float32 [B, H, d_k, d_v]
+    q: torch.Tensor            # [T, H_k, d_k], bf16 or fp32
+    k: torch.Tensor            # [T, H_k, d_k]
+    v: torch.Tensor            # [T, H, d_v]
+    gate: torch.Tensor         # float32 [T, H], or [T, H, d_k]
+    offsets: np.ndarray        # int32 [B + 1]
+
+
+def make_linear(seed: int, sizes: Sequence[int], heads: int, key_heads: int, d_k: int, d_v: int,
+                factor_dtype: torch.dtype = torch.bfloat16, channel: bool = False,
+                gate_value: Optional[float] = None, spare_rows: int = 0) -> LinearWorkload:
+    """Seeded inputs for sequences of ``sizes`` tokens: keys of unit length, queries of length
+    d_k^-1/2, decays exp(-softplus(N(0,1))) or ``gate_value``, one a head or (``channel``) one a
+    key channel. ``spare_rows`` rows, all NaN, follow the last sequence."""
+    rng = np.random.default_rng(np.random.SeedSequence([seed, 0x11ea2]))
+    offs = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    n, T = int(offs[-1]), int(offs[-1]) + spare_rows
+    unit = lambda x, s: s * x / np.maximum(np.linalg.norm(x, axis=-1, keepdims=True), 1e-30)
+    q = unit(rng.standard_normal((T, key_heads, d_k)), d_k ** -0.5)
+    k = unit(rng.standard_normal((T, key_heads, d_k)), 1.0)
+    v = rng.standard_normal((T, heads, d_v))
+    gate = np.exp(-softplus(rng.standard_normal((T, heads) + ((d_k,) if channel else ()))))
+    if gate_value is not None:
+        gate = np.full(gate.shape, gate_value)
+    for x in (q, k, v, gate):
+        x[n:] = np.nan
+    H0 = rng.standard_normal((len(sizes), heads, d_k, d_v)) * 0.3
+    return LinearWorkload(_cast(H0, torch.float32), _cast(q, factor_dtype), _cast(k, factor_dtype),
+                          _cast(v, factor_dtype), _cast(gate, torch.float32), offs)
+
+
+@dataclass
+class PrefixWorkload(WindowWorkload):
+    prefix_table: torch.Tensor   # int32 [groups, pages]
+    prefix_len: torch.Tensor     # int32 [groups]
+    group_offsets: torch.Tensor  # int32 [groups + 1]
+
+
+def make_prefix(seed: int, sizes: Sequence[int], cached: Sequence[int], prefixes: Sequence[int],
+                group_offsets: Sequence[int], heads: int, kv_heads: int, d: int, page_size: int,
+                dtype: torch.dtype = torch.bfloat16, kind: str = "random", spread: float = 1.0,
+                spare_rows: int = 0) -> PrefixWorkload:
+    """Seeded inputs of attention behind shared prefixes, as make_window's: pages in random order,
+    everything that no row may read NaN or a page that does not exist."""
+    rng = np.random.default_rng(np.random.SeedSequence([seed, 0x93ef1]))
+    parents = [random_tree(rng, int(n), kind if n <= 64 else "chain") for n in sizes]
+    _, offs = _pack(parents)
+    parent = np.concatenate(parents + [np.full(spare_rows, -1, np.int32)]).astype(np.int32)
+    T = int(offs[-1]) + spare_rows
+    pages = lambda n: -(-int(n) // page_size)
+    lists = [int(c) for c in cached] + [int(p) for p in prefixes]
+    total = sum(map(pages, lists)) + 2
+    order = list(rng.permutation(total))
+    kc = rng.standard_normal((total, kv_heads, page_size, d))
+    vc = rng.standard_normal((total, kv_heads, page_size, d))
+    seen = np.zeros((total, page_size), bool)
+
+    def table(lens, spare):
+        t = np.full((len(lens), max([pages(n) for n in lens] + [0]) + spare), -1, np.int64)
+        t[rng.random(t.shape) < 0.5] = total + 12345
+        for i, n in enumerate(lens):
+            for j in range(pages(n)):
+                t[i, j] = order.pop()
+                seen[t[i, j], :max(0, min(page_size, n - j * page_size))] = True
+        return torch.from_numpy(t.astype(np.int32))
+    own, shared = table(lists[:len(cached)], 1), table(lists[len(cached):], 0)
+    kc[~seen[:, None, :, None] & np.ones(kc.shape, bool)] = np.nan
+    vc[~seen[:, None, :, None] & np.ones(vc.shape, bool)] = np.nan
+    q = _cast(rng.standard_normal((T, heads, d)) * spread, dtype)
+    k, v = (_cast(rng.standard_normal((T, kv_heads, d)), dtype) for _ in range(2))
+    i32 = lambda x: torch.tensor([int(y) for y in x], dtype=torch.int32)
+    return PrefixWorkload(q, k, v, _cast(kc, dtype), _cast(vc, dtype), own, i32(cached), offs, parent,
+                          shared, i32(prefixes), i32(group_offsets))
