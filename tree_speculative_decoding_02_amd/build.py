@@ -19,7 +19,7 @@ SOURCES = ["bole_api.hip", "topology.hip", "validate.hip", "verify_generic.hip",
            "tree_accept.hip", "delta_api.hip", "delta_walk.hip", "delta_verify.hip",
            "delta_prefill.hip", "window_api.hip", "window_attention.hip",
            "window_mfma.hip", "window_mfma_f32.hip", "linear_api.hip", "linear_walk.hip",
-           "linear_prefill.hip", "rotary.hip", "append.hip", "prefix_attention.hip"]
+           "linear_prefill.hip", "rotary.hip", "append.hip", "prefix_attention.hip", "prefix_mfma.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 instructions stay off: the compiler would otherwise form them from

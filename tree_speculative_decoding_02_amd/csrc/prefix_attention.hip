@@ -94,11 +94,6 @@ __global__ __launch_bounds__(64) void prefix_generic_kernel(const PrefixArgs p) 
         if (lane + 64 * j < s.D) o[lane + 64 * j] = (T)(acc[j] / sum);
 }
 
-size_t prefix_workspace(const bole_prefix_dims_t &d) {
-    (void)d;
-    return 0;
-}
-
 hipError_t launch_prefix(const void *q, const void *k, const void *v, const void *k_cache,
                          const void *v_cache, const int32_t *prefix_table, const int32_t *prefix_len,
                          const int32_t *group_offsets, const int32_t *page_table,
@@ -110,7 +105,7 @@ hipError_t launch_prefix(const void *q, const void *k, const void *v, const void
                            {d.batch, d.heads, d.kv_heads, d.head_dim, d.total_rows, d.num_pages,
                             __builtin_ctz((unsigned)d.page_size), d.max_pages, 0x7fffffff, 0, d.scale}},
                           prefix_table, prefix_len, group_offsets, d.groups, d.max_prefix_pages};
-    (void)workspace;
+    if (prefix_mfma_applies(d, a)) return launch_prefix_mfma(a, d, workspace, stream);
     const dim3 grid((unsigned)(d.total_rows > 0 ? d.total_rows : 1), (unsigned)d.heads);
     if (d.dtype == BOLE_DTYPE_F32)
         prefix_generic_kernel<float><<<grid, dim3(64), 0, stream>>>(a);
@@ -134,12 +129,12 @@ bole_status_t bole_prefix_check_dims(const bole_prefix_dims_t *d) {
     if (d->flags & ~BOLE_FLAG_FORCE_GENERIC) return BOLE_ERR_INVALID_VALUE;
     if (d->head_dim > 256 || d->page_size > 1024 || d->heads > 65535) return BOLE_ERR_UNSUPPORTED;
     // Positions, those of the next few key tiles behind the last among them, and (sequences +
-    // groups + rows) x heads fit 31 bits, and a launch has fewer than 2^32 threads: 64 a row and
-    // head, or 256 for each 16 rows a key head packs and each sequence and group, parts and all.
+    // groups) x heads fit 31 bits, and a launch has fewer than 2^32 threads: 64 a row and head, or 256
+    // for each 16 rows a key head packs and up to three times a sequence or group (of few rows).
     const int64_t rows = d->total_rows, lists = (int64_t)d->batch + d->groups;
     if ((int64_t)d->max_pages * d->page_size + rows > (1LL << 31) - 1024 ||
         (int64_t)d->max_prefix_pages * d->page_size > (1LL << 31) - 1024 ||
-        (rows + lists) * d->heads > 0x7fffffffLL || rows >= 1LL << 26 ||
+        lists * d->heads > 0x7fffffffLL || rows * d->heads >= 1LL << 26 ||
         rows * d->heads / 16 + 3 * lists * d->kv_heads >= 1LL << 24)
         return BOLE_ERR_UNSUPPORTED;
     return BOLE_OK;

@@ -1,0 +1,248 @@
+// prefix_mfma.hip - attention behind shared prefixes on the matrix cores, bf16 and fp32, head widths
+// 64, 96 and 128.
+//
+// A group's sequences are neighbours, so their rows are neighbours too: with the G = H / H_kv query
+// heads that share a key head they are one list of rows, all of which see all of the prefix, and the
+// workgroups of windowed attention (window_rows.h, window_rows_f32.h) run over it as over the rows of
+// one sequence without rows of its own keys. Beside them, in the same launch, run the workgroups of
+// each sequence's own tokens. All leave unnormalised parts - sum, largest score, sum of weights - at
+// [part][row][head], and a second kernel joins a row's parts.
+#include "prefix_device.h"
+#include "window_rows.h"
+#include "window_rows_f32.h"
+#include "launch.h"
+
+namespace bole {
+
+// A sequence's own tokens: everything windowed attention shows with a window of everything.
+struct OwnKeys {
+    const PrefixArgs &p;
+    static constexpr bool kOwnRows = true, kSplit = true;
+    __device__ __forceinline__ const WindowArgs &args() const { return p.w; }
+    template <int MT>
+    __device__ __forceinline__ bool find(int G, int slot, bool report, RowTile &t, uint64_t &mask, int &depth) const {
+        return find_tile<MT>(p.w, G, slot, report, t, mask, depth);
+    }
+    __device__ __forceinline__ const int32_t *table(int b) const { return p.w.page_table + (size_t)b * p.w.s.max_pages; }
+    __device__ __forceinline__ int pages_status(int b, int len) const { return bole::pages_status(p.w, b, len); }
+};
+
+struct GroupRanges {
+    const PrefixArgs &p;
+    __device__ __forceinline__ int count() const { return p.groups; }
+    __device__ __forceinline__ void load(int x, int &lo, int &hi, int &len, bool &bad) const {
+        const int b0 = p.group_offsets[x], b1 = p.group_offsets[x + 1], B = p.w.s.B;
+        bad |= b0 < 0 || b1 < b0 || b1 > B;
+        lo = p.w.offsets[min(max(b0, 0), B)], hi = p.w.offsets[min(max(b1, 0), B)], len = p.prefix_len[x];
+    }
+};
+
+// A group's prefix: rows of all its sequences, cached keys alone. `b` of the tile is the group.
+struct SharedKeys {
+    const PrefixArgs &p;
+    static constexpr bool kOwnRows = false, kSplit = true;
+    __device__ __forceinline__ const WindowArgs &args() const { return p.w; }
+    template <int MT>
+    __device__ __forceinline__ bool find(int G, int slot, bool, RowTile &t, uint64_t &, int &) const {
+        const Slot l = find_slot<MT>(GroupRanges{p}, p.w.s.T, G, slot);
+        if (!l.found) return false;
+        t.b = l.b, t.lo = l.lo, t.n = l.n, t.slot0 = l.slot0, t.len = l.per;
+        t.tile = slot - t.slot0;
+        if (t.tile * MT >= t.n * G) return false;
+        t.i0 = uniform(t.tile * MT / G);
+        t.i1 = min(t.n, uniform((t.tile * MT + MT + G - 1) / G));
+        t.status = t.len < 0 || t.len > ((int64_t)p.max_prefix_pages << p.w.s.page_shift) || (t.len > 0 && p.w.s.pages == 0)
+                       ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
+        t.n1 = t.n3 = t.n4 = t.w0 = t.o2 = t.all_from = 0;
+        t.n2 = t.len;
+        t.own0 = t.total = (t.len + kKeys - 1) & ~(kKeys - 1);
+        return true;
+    }
+    __device__ __forceinline__ const int32_t *table(int g) const { return p.prefix_table + (size_t)g * p.max_prefix_pages; }
+    __device__ __forceinline__ int pages_status(int g, int len) const { return prefix_status(p, g, len); }
+};
+
+// How a call runs: form, row tiles (slots) and parts of either kind of key list.
+struct PrefixPlan {
+    bool f32, own_tokens, shared_tokens;
+    int own_slots, own_parts, shared_slots, shared_parts;
+};
+
+struct PrefixParts {
+    WindowParts own, shared;
+    int own_slots, shared_slots, shared_blocks;
+};
+
+// The workgroups of the prefixes come first: theirs is the most work.
+template <int D, bool OWN_TOKENS, bool SHARED_TOKENS>
+__global__ __launch_bounds__(256, 2) void prefix_kernel(const PrefixArgs p, const PrefixParts parts) {
+    constexpr int LDS = (OWN_TOKENS && SHARED_TOKENS) ? kTokensLds<D>
+                                                      : (kRowsLds<D> > kTokensLds<D> ? kRowsLds<D> : kTokensLds<D>);
+    __shared__ __align__(16) char s_mem[LDS];
+    const int HK = p.w.s.HK;
+    if ((int)blockIdx.x < parts.shared_blocks) {
+        const int per = parts.shared_slots * HK, part = uniform(blockIdx.x / per), block = blockIdx.x - part * per;
+        if constexpr (SHARED_TOKENS) tokens_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
+        else rows_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
+    } else {
+        const int x = blockIdx.x - parts.shared_blocks, per = parts.own_slots * HK;
+        const int part = uniform(x / per), block = x - part * per;
+        if constexpr (OWN_TOKENS) tokens_body<D>(OwnKeys{p}, parts.own, parts.own_slots, block, part, s_mem);
+        else rows_body<D>(OwnKeys{p}, parts.own, parts.own_slots, block, part, s_mem);
+    }
+}
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void prefix_f32_kernel(const PrefixArgs p, const PrefixParts parts) {
+    __shared__ __align__(16) char s_mem[kF32Lds<D>];
+    const int HK = p.w.s.HK;
+    if ((int)blockIdx.x < parts.shared_blocks) {
+        const int per = parts.shared_slots * HK, part = uniform(blockIdx.x / per);
+        f32_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, blockIdx.x - part * per, part, s_mem);
+    } else {
+        const int x = blockIdx.x - parts.shared_blocks, per = parts.own_slots * HK, part = uniform(x / per);
+        f32_body<D>(OwnKeys{p}, parts.own, parts.own_slots, x - part * per, part, s_mem);
+    }
+}
+
+// Joins the parts of a row and head (at most 64), a wavefront each, in a fixed order; a lane has
+// D / 64 dimensions (96: two of three lanes' worth).
+template <typename T, int D>
+__global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, const PrefixParts parts) {
+    const WindowArgs &a = p.w;
+    const WindowShape &s = a.s;
+    const int lane = lane_id();
+    const int64_t at = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6), all = (int64_t)s.T * s.H;
+    const bool ordered = offsets_ordered(a.offsets, s.B, s.T) &&
+                         (p.groups == 0 || offsets_ordered(p.group_offsets, p.groups, s.B));
+    if (!ordered) {
+        if (at == 0 && a.status)
+            for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
+        return;
+    }
+    if (at >= all) return;
+    const int row = uniform((int)(at / s.H)), h = (int)(at - (int64_t)row * s.H);
+    if (row < a.offsets[0] || row >= a.offsets[s.B]) return;
+    int n = parts.own.n;
+    if (p.groups > 0 && row >= a.offsets[p.group_offsets[0]] && row < a.offsets[p.group_offsets[p.groups]])
+        n += parts.shared.n;
+    const int64_t stride = all;  // (own parts, then shared ones)
+    float m = -INFINITY, l = 0.f;
+    if (lane < n) {
+        const float2 x = *reinterpret_cast<const float2 *>(parts.own.ml + (lane * stride + at) * 2);
+        m = x.x, l = x.y;
+    }
+    const float own = readlane_f(l, 0), shared = readlane_f(l, n - 1);  // (all parts of a bad list say the same)
+    if (own == kLeftRow) return;
+    T *out = static_cast<T *>(a.out) + at * D;
+    if (own == kNanRow || shared == kNanRow) {
+        if (own != kNanRow && h == 0 && lane == 0 && a.status) a.status[sequence_of(a.offsets, s.B, row)] = BOLE_TREE_BAD_CACHE;
+        for (int e = lane; e < D; e += 64) out[e] = (T)__builtin_nanf("");
+        return;
+    }
+    float top = m;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const float f = __builtin_amdgcn_exp2f(m - top);
+    float sum = f * l;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    constexpr int E = D == 64 ? 1 : 2;
+    const bool has = lane * E < D;
+    const float *src = parts.own.o + at * D + (has ? lane * E : 0);
+    float o[E] = {};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float fi = readlane_f(f, i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(fi, src[i * stride * D + e], o[e]);
+    }
+    if (has) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[lane * E + e] = (T)(o[e] / sum);
+    }
+}
+
+// ---- host
+
+static bool covers(const bole_prefix_dims_t &d) {
+    return !(d.flags & BOLE_FLAG_FORCE_GENERIC) &&
+           (d.head_dim == 64 || d.head_dim == 96 || d.head_dim == 128) && d.batch > 0;
+}
+
+static int parts_for(int64_t workgroups, int64_t keys, int most) {
+    int64_t n = (512 + workgroups - 1) / workgroups;
+    if (n > (keys + 255) / 256) n = (keys + 255) / 256;
+    return (int)(n > most ? most : n < 1 ? 1 : n);
+}
+
+// From a call's sizes alone, by windowed attention's rules (window_mfma.hip): the tokens form for up
+// to one of its tiles a list on average, parts so that 512 workgroups run on either kind of list, but
+// no more than one for each 256 keys begun. Lengths are not known here: the lists' longest count.
+static PrefixPlan plan(const bole_prefix_dims_t &d) {
+    PrefixPlan p;
+    const int64_t G = d.heads / d.kv_heads, rows = d.total_rows * G;
+    p.f32 = d.dtype == BOLE_DTYPE_F32;
+    p.own_tokens = !p.f32 && rows <= (int64_t)kTokenTile * d.batch;
+    p.shared_tokens = p.own_tokens && rows <= (int64_t)kTokenTile * d.groups;
+    const int own = p.f32 ? kF32Tile : p.own_tokens ? kTokenTile : kRowTile;
+    const int shared = p.f32 ? kF32Tile : p.shared_tokens ? kTokenTile : kRowTile;
+    p.own_slots = (int)(rows / own + d.batch);
+    p.own_parts = parts_for((int64_t)p.own_slots * d.kv_heads, (int64_t)d.max_pages * d.page_size + 1, 16);
+    p.shared_slots = (int)(d.groups == 1 ? (rows > 0 ? (rows + shared - 1) / shared : 1) : rows / shared + d.groups);
+    p.shared_parts = 0;
+    if (d.groups > 0)
+        p.shared_parts = parts_for((int64_t)p.shared_slots * d.kv_heads, (int64_t)d.max_prefix_pages * d.page_size, 48);
+    else
+        p.shared_slots = 0;
+    return p;
+}
+
+size_t prefix_workspace(const bole_prefix_dims_t &d) {
+    if (!covers(d)) return 0;
+    const PrefixPlan p = plan(d);
+    return (size_t)(p.own_parts + p.shared_parts) * d.total_rows * d.heads * (d.head_dim + 2) * sizeof(float);
+}
+
+bool prefix_mfma_applies(const bole_prefix_dims_t &d, const PrefixArgs &a) {
+    uintptr_t bits = 0;
+    for (const void *p : {a.w.q, a.w.k, a.w.v, a.w.k_cache, a.w.v_cache, static_cast<const void *>(a.w.out)})
+        bits |= reinterpret_cast<uintptr_t>(p);
+    return covers(d) && bits % 16 == 0;
+}
+
+template <int D>
+static hipError_t launch_width(const PrefixArgs &a, const PrefixPlan &p, const PrefixParts &parts, hipStream_t stream) {
+    const int64_t HK = a.w.s.HK;
+    const dim3 block(256), grid((unsigned)(parts.shared_blocks + p.own_slots * HK * p.own_parts));
+    if (p.f32) prefix_f32_kernel<D><<<grid, block, 0, stream>>>(a, parts);
+    else if (p.own_tokens && p.shared_tokens) prefix_kernel<D, true, true><<<grid, block, 0, stream>>>(a, parts);
+    else if (p.own_tokens) prefix_kernel<D, true, false><<<grid, block, 0, stream>>>(a, parts);
+    else prefix_kernel<D, false, false><<<grid, block, 0, stream>>>(a, parts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t lines = (int64_t)a.w.s.T * a.w.s.H;
+    const dim3 join((unsigned)(lines > 0 ? (lines + 3) / 4 : 1));
+    if (p.f32) prefix_join_kernel<float, D><<<join, block, 0, stream>>>(a, parts);
+    else prefix_join_kernel<__bf16, D><<<join, block, 0, stream>>>(a, parts);
+    return hipGetLastError();
+}
+
+hipError_t launch_prefix_mfma(const PrefixArgs &a, const bole_prefix_dims_t &d, void *workspace, hipStream_t stream) {
+    const PrefixPlan p = plan(d);
+    const size_t lines = (size_t)d.total_rows * d.heads, all = p.own_parts + p.shared_parts;
+    float *o = static_cast<float *>(workspace), *ml = o + all * lines * d.head_dim;
+    PrefixParts parts;
+    parts.own = {o, ml, p.own_parts};
+    parts.shared = {o + p.own_parts * lines * d.head_dim, ml + p.own_parts * lines * 2, p.shared_parts};
+    parts.own_slots = p.own_slots;
+    parts.shared_slots = p.shared_slots;
+    parts.shared_blocks = p.shared_slots * d.kv_heads * p.shared_parts;
+    switch (d.head_dim) {
+        case 64: return launch_width<64>(a, p, parts, stream);
+        case 96: return launch_width<96>(a, p, parts, stream);
+        default: return launch_width<128>(a, p, parts, stream);
+    }
+}
+
+}  // namespace bole

@@ -7,6 +7,9 @@
 namespace bole {
 
 constexpr int kKeys = 64;        // keys a tile
+constexpr int kRowTile = 128;    // rows a workgroup, rows form
+constexpr int kTokenTile = 16;   // rows a workgroup, tokens form
+constexpr int kF32Tile = 64;     // rows a workgroup, fp32
 
 // Where the unnormalised parts of a split call go: O [parts][tiles][MT][D], then (m, l)
 // [parts][tiles][MT][2]. In place of a sum, which is not negative, stands kNanRow for a sequence
@@ -64,9 +67,18 @@ struct Slot {
     int b, lo, n, slot0, per;       // sequence, its rows, its first slot
 };
 
-template <int MT>
-__device__ __forceinline__ Slot find_slot(const WindowArgs &a, int G, int slot) {
-    const int B = a.s.B;
+// Ranges: B of them; load(x, ..) gives the x-th's rows [lo, hi) and tokens, and whether it is bad.
+struct SequenceRanges {
+    const WindowArgs &a;
+    __device__ __forceinline__ int count() const { return a.s.B; }
+    __device__ __forceinline__ void load(int x, int &lo, int &hi, int &len, bool &) const {
+        lo = a.offsets[x], hi = a.offsets[x + 1], len = a.cache_len[x];
+    }
+};
+
+template <int MT, class Ranges>
+__device__ __forceinline__ Slot find_slot(const Ranges &ranges, int T, int G, int slot) {
+    const int B = ranges.count();
     bool bad = false;
     Slot l = {false, true, 0, 0, 0, 0, 0};
     int before = 0;
@@ -75,13 +87,13 @@ __device__ __forceinline__ Slot find_slot(const WindowArgs &a, int G, int slot) 
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int x = min(c0 + 64 * j + lane_id(), B - 1);
-            lo[j] = a.offsets[x], hi[j] = a.offsets[x + 1], len[j] = a.cache_len[x];
+            ranges.load(x, lo[j], hi[j], len[j], bad);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int c = c0 + 64 * j;
             if (c >= B) break;
-            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > a.s.T;
+            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > T;
             const int own = c + lane_id() < B ? max(1, (int)(((uint32_t)(hi[j] - lo[j]) * G + MT - 1) / MT)) : 0;
             const int end = before + wave_sum_up(own);
             const int at = uniform((int)__popcll(__ballot(c + lane_id() < B && end <= slot)));
@@ -110,7 +122,7 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
     const WindowShape &s = a.s;
     const int lane = lane_id();
     t.status = BOLE_TREE_OK;
-    const Slot l = find_slot<MT>(a, G, slot);
+    const Slot l = find_slot<MT>(SequenceRanges{a}, s.T, G, slot);
     if (!l.found) {
         if (!l.ordered && report && slot == 0 && a.status)
             for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
@@ -231,6 +243,19 @@ __device__ __forceinline__ uint64_t seen_keys(const RowTile &t, bool tree, int i
            (bits_below(own + min(t.n4, i + 1 - t.o2)) & ~bits_below(own + max(0, from - t.len - t.o2)));
 }
 
+// The keys of windowed attention, for the workgroups of window_rows.h and window_rows_f32.h.
+struct WindowKeys {
+    const WindowArgs &a;
+    static constexpr bool kOwnRows = true, kSplit = false;
+    __device__ __forceinline__ const WindowArgs &args() const { return a; }
+    template <int MT>
+    __device__ __forceinline__ bool find(int G, int slot, bool report, RowTile &t, uint64_t &mask, int &depth) const {
+        return find_tile<MT>(a, G, slot, report, t, mask, depth);
+    }
+    __device__ __forceinline__ const int32_t *table(int b) const { return a.page_table + (size_t)b * a.s.max_pages; }
+    __device__ __forceinline__ int pages_status(int b, int len) const { return bole::pages_status(a, b, len); }
+};
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Joins the parts of a split call (at most 64): a workgroup a row, wavefront w takes parts w,
@@ -244,7 +269,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     const size_t stride = (size_t)slots * s.HK * MT, at = (size_t)blockIdx.x * MT + r;
     // every part's maximum and sum, a part a lane (the rows of unused tiles are never read)
-    const Slot t = find_slot<MT>(a, G, slot);
+    const Slot t = find_slot<MT>(SequenceRanges{a}, s.T, G, slot);
     const int R = (slot - t.slot0) * MT + r;
     if (!t.found || R >= t.n * G) return;
     float m = -INFINITY, l = 0.f;
