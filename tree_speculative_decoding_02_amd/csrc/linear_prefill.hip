@@ -71,7 +71,7 @@ __device__ __forceinline__ int lower_piece(int m, int s) { return s == 0 ? m : 2
 // WHOLE: d_k = DK and the columns fill the groups. Otherwise d_k and d_v are multiples of 8; parts of
 // rows from d_k on and of columns from d_v on count as zero.
 template <typename TF, int DK, int CT, bool WHOLE, bool LOCAL>
-__global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void linear_chunk_kernel(
+__global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 : 3) void linear_chunk_kernel(
     const LinearArgs a, const LinearPlan p, const LinearSpace w) {
     typedef TF tf4 __attribute__((ext_vector_type(4)));
     constexpr int NK = Terms<TF>::K, NS = Terms<TF>::S;
@@ -123,37 +123,63 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
     const size_t at_ws = space_slot(l.lo, p.seg, slot - l.slot0) * s.H + h;
     f32x4 *sw = w.s + (at_ws * p.groups * 4 * CT + (cg * 4 + wave) * CT) * TILES * 64 + lane;
     f32x4 st[CT][TILES];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-            st[ct][j] = (f32x4)0.f;
-            if (LOCAL) continue;
-            if (l.n > p.seg) {
-                st[ct][j] = sw[(ct * TILES + j) * 64];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (state_has(ct, j, e)) st[ct][j][e] = Hu[(size_t)tile_token(j, 4 * g + e) * s.DV + 16 * ct];
-            }
-        }
-
-    // ---- loads: rows past the last token repeat it (they do not decay, and their 2^{L_64 - L} is 0)
+    // ---- loads: rows past the last token repeat it (they do not decay, and their 2^{L_64 - L} is 0).
+    // Addresses are a chunk's (scalar) plus a lane's 32-bit offset in bytes.
+    constexpr int SZ = sizeof(TF), ROWS = 256 / CH, VROWS = 256 / (VC / 8);
+    const uint32_t skb = (uint32_t)(sk * SZ), svb = (uint32_t)(sv * SZ);
+    const int kc = WHOLE || 8 * (tid % CH) < dk ? tid % CH : 0, vc = WHOLE || 8 * (tid % (VC / 8)) < left ? tid % (VC / 8) : 0;
+    const uint32_t koff = (uint32_t)(tid / CH) * skb + 8 * SZ * kc, voff = (uint32_t)(tid / (VC / 8)) * svb + 8 * SZ * vc;
     RowPart<TF> kr[PER], qr[LOCAL ? 1 : PER], vr[VPER];
     auto fetch = [&](int chunk) {
         const int first = chunk * kChunk, most = n - 1 - first;
+        const char *k0 = reinterpret_cast<const char *>(kb) + (size_t)first * skb;
+        const char *q0 = reinterpret_cast<const char *>(qb) + (size_t)first * skb;
+        const char *v0 = reinterpret_cast<const char *>(vb) + (size_t)first * svb;
+        if (most >= kChunk - 1) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int r = min(tid / CH + 256 / CH * j, most);
-            kr[j] = row_part<WHOLE>(kb + (size_t)(first + r) * sk, tid % CH, dk);
-            if constexpr (!LOCAL) qr[j] = row_part<WHOLE>(qb + (size_t)(first + r) * sk, tid % CH, dk);
+            for (int j = 0; j < PER; ++j) {
+                kr[j].load(reinterpret_cast<const TF *>(k0 + (size_t)(ROWS * j) * skb + koff));
+                if constexpr (!LOCAL) qr[j].load(reinterpret_cast<const TF *>(q0 + (size_t)(ROWS * j) * skb + koff));
+            }
+#pragma unroll
+            for (int j = 0; j < VPER; ++j)
+                vr[j].load(reinterpret_cast<const TF *>(v0 + (size_t)(VROWS * j) * svb + voff));
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const uint32_t off = (uint32_t)min(tid / CH + ROWS * j, most) * skb + 8 * SZ * kc;
+                kr[j].load(reinterpret_cast<const TF *>(k0 + off));
+                if constexpr (!LOCAL) qr[j].load(reinterpret_cast<const TF *>(q0 + off));
+            }
+#pragma unroll
+            for (int j = 0; j < VPER; ++j)
+                vr[j].load(reinterpret_cast<const TF *>(
+                    v0 + (uint32_t)min(tid / (VC / 8) + VROWS * j, most) * svb + 8 * SZ * vc));
         }
+        if (!WHOLE) {
 #pragma unroll
-        for (int j = 0; j < VPER; ++j) {
-            const int e = tid + 256 * j, r = min(e / (VC / 8), most), c = e % (VC / 8);
-            vr[j] = row_part<WHOLE>(vb + (size_t)(first + r) * sv, c, left);
+            for (int j = 0; j < PER; ++j)
+                if (8 * (tid % CH) >= dk) {
+                    kr[j].clear();
+                    if constexpr (!LOCAL) qr[j].clear();
+                }
+#pragma unroll
+            for (int j = 0; j < VPER; ++j)
+                if (8 * (tid % (VC / 8)) >= left) vr[j].clear();
         }
     };
+    // places of operand pieces in s_k and s_q: part 4 ks + g of row tile_token(m, col), and rows
+    // 32 sb + 8 g + 4 half .. + 3 of a transposing read's part of row tile j (what is added to a row in
+    // multiples of 32 leaves its permutation)
+    int opnd[2][KS], trans[2][KS];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            opnd[x][ks] = row_at<DK>(tile_token(x, col), 4 * ks + g);
+            trans[x][ks] = row_at<DK>(8 * g + (col >> 2) + 4 * x, 4 * ks + (col & 3));
+        }
+    auto operand = [&](const __bf16 *from, int m, int ks) { return load16(from + opnd[m & 1][ks] + 32 * (m >> 1) * DK); };
     auto stage = [&]() {
         bf16x8 y[NK];
 #pragma unroll
@@ -193,37 +219,53 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
         total += all;
     };
 
+    fetch(0);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            st[ct][j] = (f32x4)0.f;
+            if (LOCAL) continue;
+            if (l.n > p.seg) {
+                st[ct][j] = sw[(ct * TILES + j) * 64];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (state_has(ct, j, e)) st[ct][j][e] = Hu[(size_t)tile_token(j, 4 * g + e) * s.DV + 16 * ct];
+            }
+        }
     float gate_next = 1.f;
     if (wave == 0) {
-        weigh(0, fetch_gate(0));
+        const float gate = fetch_gate(0);
         gate_next = fetch_gate(1);
+        weigh(0, gate);
     }
-    fetch(0);
     stage();
     lds_barrier();
     int chunk = 0;
     do {
         const float(*wt)[kChunk] = s_w[chunk & 1];
-        if (chunk + 1 < chunks) fetch(chunk + 1);
         f32x4 o[CT][4];
         if constexpr (!LOCAL) {
             // ---- P: the wavefront's row tile, as operand pieces
             const int i = tile_token(wave, col);
             const float li = wt[0][i], lr = wt[1][i];
             f32x4 pair[4];
+            bf16x8 own_q[KS][NK];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int t = 0; t < NK; ++t) own_q[ks][t] = load16(s_q[t] + row_at<DK>(i, 4 * ks + g));
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
                 pair[jt] = (f32x4)0.f;
                 if (jt >> 1 > wave >> 1) continue;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 x[NK], y[NK];
+                    bf16x8 x[NK];
 #pragma unroll
-                    for (int t = 0; t < NK; ++t) {
-                        x[t] = load16(&s_k[t][row_at<DK>(tile_token(jt, col), 4 * ks + g)]);
-                        y[t] = load16(&s_q[t][row_at<DK>(i, 4 * ks + g)]);
-                    }
-                    pair[jt] = mfma_terms(x, y, pair[jt]);
+                    for (int t = 0; t < NK; ++t) x[t] = operand(s_k[t], jt, ks);
+                    pair[jt] = mfma_terms(x, own_q[ks], pair[jt]);
                 }
                 const int j0 = tile_token(jt, 4 * g);
                 const f32x4 lj = *reinterpret_cast<const f32x4 *>(&wt[0][j0]);
@@ -255,7 +297,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
                 for (int m = 0; m < 4; ++m) {
                     bf16x8 y[NK];
 #pragma unroll
-                    for (int t = 0; t < NK; ++t) y[t] = load16(&s_q[t][row_at<DK>(tile_token(m, col), 4 * ks + g)]);
+                    for (int t = 0; t < NK; ++t) y[t] = operand(s_q[t], m, ks);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -274,39 +316,28 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
         }
         // ---- V's operand pieces: tokens 32 sb + 8 g .. + 7 of the lane's column
         const float decay = wt[2][kChunk - 1];
-        bf16x8 ev[CT][2][3];
+        bf16x8 v[CT][2][NK], ev[CT][2][3];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
-                bf16x8 v[NK];
+            for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
                 for (int t = 0; t < NK; ++t) {
                     const __bf16 *vp = &s_v[t][(32 * sb + 8 * g + (col >> 2)) * VP + c0 + 16 * ct + 4 * (col & 3)];
-                    v[t] = join(read_transposed(vp), read_transposed(vp + 4 * VP));
+                    v[ct][sb][t] = join(read_transposed(vp), read_transposed(vp + 4 * VP));
                 }
-                if constexpr (!LOCAL) {
-                    // ---- O^T += V^T P^T
-#pragma unroll
-                    for (int m = 2 * sb; m < 4; ++m) {
-                        bf16x8 y[NK];
-#pragma unroll
-                        for (int t = 0; t < NK; ++t) y[t] = load16(&s_p[t][lower_piece(m, sb)][lane][0]);
-                        o[ct][m] = mfma_terms(v, y, o[ct][m]);
-                    }
-                }
-                f32x4 lo4, hi4;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo4[e] = (float)v[0][e], hi4[e] = (float)v[0][4 + e];
-#pragma unroll
-                    for (int t = 1; t < NK; ++t) lo4[e] += (float)v[t][e], hi4[e] += (float)v[t][4 + e];
-                }
-                lo4 *= *reinterpret_cast<const f32x4 *>(&wt[3][32 * sb + 8 * g]);
-                hi4 *= *reinterpret_cast<const f32x4 *>(&wt[3][32 * sb + 8 * g + 4]);
-                split_terms8<3>(lo4, hi4, ev[ct][sb]);
-            }
         if constexpr (!LOCAL) {
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int sb = 0; sb <= m >> 1; ++sb) {
+                    bf16x8 y[NK];
+#pragma unroll
+                    for (int t = 0; t < NK; ++t) y[t] = load16(&s_p[t][lower_piece(m, sb)][lane][0]);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) o[ct][m] = mfma_terms(v[ct][sb], y, o[ct][m]);
+                }
             TF *ob = static_cast<TF *>(a.out) + row0 * sv + (size_t)h * s.DV + cg * VC + c0 + 4 * g;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -318,6 +349,22 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
                         *reinterpret_cast<tf4 *>(ob + (size_t)t * sv + 16 * ct) = __builtin_convertvector(o[ct][m], tf4);
             }
         }
+        fetch(min(chunk + 1, chunks - 1));
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+                f32x4 x[2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e >> 2][e & 3] = (float)v[ct][sb][0][e];
+#pragma unroll
+                    for (int t = 1; t < NK; ++t) x[e >> 2][e & 3] += (float)v[ct][sb][t][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x[e] *= *reinterpret_cast<const f32x4 *>(&wt[3][32 * sb + 8 * g + 4 * e]);
+                split_terms8<3>(x[0], x[1], ev[ct][sb]);
+            }
         // ---- S <- 2^{L_64} S + K^T (diag V)
 #pragma unroll
         for (int j = 0; j < TILES; ++j) {
@@ -325,12 +372,11 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : 3) void li
             for (int ct = 0; ct < CT; ++ct) st[ct][j] *= decay;
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb) {
-                const int row = 32 * sb + 8 * g + (col >> 2), c = 4 * (j >> 1) + (col & 3);
                 bf16x8 x[NK];
 #pragma unroll
                 for (int t = 0; t < NK; ++t)
-                    x[t] = join(read_transposed(&s_k[t][row_at<DK>(row, c) + 4 * (j & 1)]),
-                                read_transposed(&s_k[t][row_at<DK>(row + 4, c) + 4 * (j & 1)]));
+                    x[t] = join(read_transposed(s_k[t] + trans[0][j >> 1] + 32 * sb * DK + 4 * (j & 1)),
+                                read_transposed(s_k[t] + trans[1][j >> 1] + 32 * sb * DK + 4 * (j & 1)));
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) st[ct][j] = mfma_terms(x, ev[ct][sb], st[ct][j]);
             }
@@ -425,7 +471,7 @@ static LinearPlan plan(const bole_linear_dims_t &d) {
     const int columns = 64 * column_tiles(d);
     p.groups = (d.d_v + columns - 1) / columns;
     const int64_t chunks = (d.total_tokens + kChunk - 1) / kChunk;
-    int64_t seg = (chunks * d.heads * p.groups + 1023) / 1024;
+    int64_t seg = (chunks * d.heads * p.groups + 1535) / 1536;
     if (seg < 4) seg = 4;
     if (seg * kChunk >= d.total_tokens) seg = chunks > 0 ? chunks : 1;
     p.seg = (int)(seg * kChunk);
