@@ -472,6 +472,17 @@ def test_append(lib, shape, path):
         assert (status == 0).all()
 
 
+@pytest.mark.parametrize("shape", [(2, 128, 16, BF16), (1, 33, 8, F32), (8, 256, 64, BF16), (1, 1, 4, BF16)], ids=str)
+def test_append_many_rows(lib, shape):
+    """Row counts that take the launch for many rows; sequences that begin and end inside its blocks,
+    empty ones, more of them than a load's lanes."""
+    for sizes in ([2500, 1, 0, 700], [(5 * i) % 23 for i in range(300)], [2049]):
+        w = make_append(5, sizes, [(37 * i) % 200 for i in range(len(sizes))], *shape, path=False)
+        status = torch.full((len(sizes),), -1, dtype=torch.int32, device=dev())
+        check_append(call_append(lib, w, seq_status=status), w)
+        assert (status == 0).all()
+
+
 def test_append_contiguous_and_unaligned(lib):
     w = make_append(2, [40, 3], [10, 0], 2, 128, 16, BF16, path=False)
 

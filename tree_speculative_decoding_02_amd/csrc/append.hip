@@ -1,9 +1,9 @@
 // append.hip - new tokens into a paged cache: all rows of each sequence, or the rows of its
 // accepted path, behind its cached tokens.
 //
-// A workgroup a row: it finds the row's place, checks every page that its sequence's new tokens go
-// to (a bad sequence adds nothing, so each of its rows has to know), and copies the row of every
-// key head. Bound by the copy, or, for accepted paths, by the chain offsets - path - pages - rows.
+// A bad sequence adds nothing, so each of its rows has to know: a wavefront that finds a row's place
+// checks every page that its sequence's new tokens go to. Rows are on their way meanwhile: bound by
+// the copy, or, for accepted paths, by the chain offsets - path - pages - rows.
 #include "delta_device.h"
 #include "launch.h"
 
@@ -30,60 +30,108 @@ __device__ __forceinline__ int room_status(const AppendArgs &a, int b, int len, 
     return __any(bad) ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
 }
 
-// Packed row `row` of k and v to position `at` of sequence b, V (a power of two) bytes a thread.
-template <typename V>
-__device__ __forceinline__ void copy_row(const AppendArgs &a, int size, int b, int row, int at) {
+constexpr size_t kNowhere = ~(size_t)0;
+
+// Byte offset in either cache of position `at` of sequence b, head 0.
+__device__ __forceinline__ size_t place_of(const AppendArgs &a, int size, int b, int at) {
     const int page = a.page_table[(size_t)b * a.max_pages + (at >> a.page_shift)];
-    const int slot = at & ((1 << a.page_shift) - 1);
-    const int per = a.D * size / (int)sizeof(V);  // pieces a head
-    const char *k = static_cast<const char *>(a.k) + (size_t)row * a.k_stride * size;
-    const char *v = static_cast<const char *>(a.v) + (size_t)row * a.v_stride * size;
-    for (int e = threadIdx.x; e < a.HK * per; e += blockDim.x) {
-        const int h = e / per, c = e - h * per;
-        const size_t to = ((((size_t)page * a.HK + h) << a.page_shift) + slot) * a.D * size + (size_t)c * sizeof(V);
-        *reinterpret_cast<V *>(static_cast<char *>(a.k_cache) + to) = reinterpret_cast<const V *>(k)[e];
-        *reinterpret_cast<V *>(static_cast<char *>(a.v_cache) + to) = reinterpret_cast<const V *>(v)[e];
-    }
+    return ((((size_t)page * a.HK) << a.page_shift) + (at & ((1 << a.page_shift) - 1))) * a.D * size;
 }
 
+// One piece, of V (a power of two) bytes, of a row's keys (the first half of 2 n pieces) or values.
 template <typename V>
-__global__ __launch_bounds__(256) void append_rows_kernel(const AppendArgs a, int size) {
-    const int row = blockIdx.x, lane = lane_id();
-    const bool first = threadIdx.x < 64;
-    const RowOwner o = owner_of(a.offsets, a.B, a.T, row);
-    if (row == 0 && first)
-        for (int b = lane; b < a.B; b += 64)
-            if (!o.ordered || a.offsets[b + 1] == a.offsets[b]) {
-                const int len = a.cache_len[b];
-                const int st = !o.ordered ? BOLE_TREE_BAD_SIZE
-                               : len < 0 || len > ((int64_t)a.max_pages << a.page_shift) ? BOLE_TREE_BAD_CACHE
-                                                                                        : BOLE_TREE_OK;
-                if (a.status) a.status[b] = st;
-                if (a.new_len) a.new_len[b] = len;
-            }
-    if (!o.found) return;
-    const int len = a.cache_len[o.b];
-    const int st = room_status(a, o.b, len, o.n);
-    if (row == o.lo && threadIdx.x == 0) {
-        if (a.status) a.status[o.b] = st;
-        if (a.new_len) a.new_len[o.b] = st == BOLE_TREE_OK ? len + o.n : len;
+struct Piece {
+    const char *from;
+    char *to;
+    size_t stride, head;  // bytes between rows; from the row's place in the cache on
+    __device__ __forceinline__ Piece(const AppendArgs &a, int size, int e, int n) {
+        const bool value = e >= n;
+        e -= value ? n : 0;
+        const int per = a.D * size / (int)sizeof(V), h = e / per, c = e - h * per;
+        from = static_cast<const char *>(value ? a.v : a.k) + (size_t)e * sizeof(V);
+        to = static_cast<char *>(value ? a.v_cache : a.k_cache);
+        stride = (size_t)(value ? a.v_stride : a.k_stride) * size;
+        head = (((size_t)h << a.page_shift) * a.D) * size + (size_t)c * sizeof(V);
     }
-    if (st == BOLE_TREE_OK) copy_row<V>(a, size, o.b, row, len + row - o.lo);
+    __device__ __forceinline__ V load(int row) const { return *reinterpret_cast<const V *>(from + row * stride); }
+    __device__ __forceinline__ void store(size_t place, V x) const { *reinterpret_cast<V *>(to + place + head) = x; }
+};
+
+// A workgroup ROWS neighbouring rows. Eight for many rows: one 8192-row call of two sequences 42.9 us
+// with one.
+template <typename V, int ROWS>
+__global__ __launch_bounds__(256) void append_rows_kernel(const AppendArgs a, int size) {
+    __shared__ size_t s_place[ROWS];
+    const int row0 = blockIdx.x * ROWS, rows = min(ROWS, a.T - row0), lane = lane_id(), wave = threadIdx.x >> 6;
+    const int n = a.HK * (a.D * size / (int)sizeof(V));
+    V x[ROWS];
+    if (rows > 0) {
+        const Piece<V> p(a, size, min((int)threadIdx.x, 2 * n - 1), n);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) x[r] = p.load(row0 + min(r, rows - 1));
+    }
+    constexpr int EACH = (ROWS + 3) / 4;
+    RowOwner o = {false, true, -1, 0, 0};
+    int len = 0, st = BOLE_TREE_OK;
+    for (int i = 0; i < EACH; ++i) {
+        const int r = wave * EACH + i, row = row0 + r;
+        if (r >= ROWS || (r >= rows && row != 0)) break;
+        if (!o.found || row >= o.lo + o.n) {
+            o = owner_of(a.offsets, a.B, a.T, row);
+            if (o.found) {
+                len = a.cache_len[o.b];
+                st = room_status(a, o.b, len, o.n);
+            }
+        }
+        if (row == 0)  // sequences without rows, and all of them if offsets are unordered
+            for (int b = lane; b < a.B; b += 64)
+                if (!o.ordered || a.offsets[b + 1] == a.offsets[b]) {
+                    const int have = a.cache_len[b];
+                    const int bad = !o.ordered ? BOLE_TREE_BAD_SIZE
+                                    : have < 0 || have > ((int64_t)a.max_pages << a.page_shift) ? BOLE_TREE_BAD_CACHE
+                                                                                              : BOLE_TREE_OK;
+                    if (a.status) a.status[b] = bad;
+                    if (a.new_len) a.new_len[b] = have;
+                }
+        if (o.found && row == o.lo && lane == 0) {
+            if (a.status) a.status[o.b] = st;
+            if (a.new_len) a.new_len[o.b] = st == BOLE_TREE_OK ? len + o.n : len;
+        }
+        if (lane == 0)
+            s_place[r] = o.found && r < rows && st == BOLE_TREE_OK ? place_of(a, size, o.b, len + row - o.lo) : kNowhere;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * n; e += 256) {
+        const Piece<V> p(a, size, e, n);
+        if (e != (int)threadIdx.x) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) x[r] = p.load(row0 + min(r, rows - 1));
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (r < rows && s_place[r] != kNowhere) p.store(s_place[r], x[r]);
+    }
 }
 
+// A workgroup a node of an accepted path.
 template <typename V>
 __global__ __launch_bounds__(256) void append_path_kernel(const AppendArgs a, int size) {
     const int b = blockIdx.x, m = blockIdx.y;
-    const WavePath p = wave_path(a.parent, a.offsets, a.accepted_idx, a.accepted_len, b, a.T, a.max_path);
+    const WavePath w = wave_path(a.parent, a.offsets, a.accepted_idx, a.accepted_len, b, a.T, a.max_path);
     const int len = a.cache_len[b];
-    int st = p.status;
-    if (st == BOLE_TREE_OK) st = room_status(a, b, len, p.len);
+    int st = w.status;
+    if (st == BOLE_TREE_OK) st = room_status(a, b, len, w.len);
     if (m == 0 && threadIdx.x == 0) {
         if (a.status) a.status[b] = st;
-        if (a.new_len) a.new_len[b] = st == BOLE_TREE_OK ? len + p.len : len;
+        if (a.new_len) a.new_len[b] = st == BOLE_TREE_OK ? len + w.len : len;
     }
-    if (st == BOLE_TREE_OK && m < p.len)
-        copy_row<V>(a, size, b, __builtin_amdgcn_readlane(p.row, m), len + m);
+    if (st != BOLE_TREE_OK || m >= w.len) return;
+    const int row = __builtin_amdgcn_readlane(w.row, m), n = a.HK * (a.D * size / (int)sizeof(V));
+    const size_t place = place_of(a, size, b, len + m);
+    for (int e = threadIdx.x; e < 2 * n; e += 256) {
+        const Piece<V> p(a, size, e, n);
+        p.store(place, p.load(row));
+    }
 }
 
 template <typename V>
@@ -92,7 +140,8 @@ static hipError_t launch_pieces(const AppendArgs &a, int size, hipStream_t strea
         const dim3 grid((unsigned)a.B, (unsigned)(a.max_path > 0 ? a.max_path : 1));
         append_path_kernel<V><<<grid, dim3(256), 0, stream>>>(a, size);
     } else {
-        append_rows_kernel<V><<<dim3((unsigned)(a.T > 0 ? a.T : 1)), dim3(256), 0, stream>>>(a, size);
+        if (a.T >= 2048) append_rows_kernel<V, 8><<<dim3((unsigned)((a.T + 7) / 8)), dim3(256), 0, stream>>>(a, size);
+        else append_rows_kernel<V, 1><<<dim3((unsigned)(a.T > 0 ? a.T : 1)), dim3(256), 0, stream>>>(a, size);
     }
     return hipGetLastError();
 }
