@@ -80,12 +80,13 @@ __global__ __launch_bounds__(256, 2) void prefix_kernel(const PrefixArgs p, cons
                                                       : (kRowsLds<D> > kTokensLds<D> ? kRowsLds<D> : kTokensLds<D>);
     __shared__ __align__(16) char s_mem[LDS];
     const int HK = p.w.s.HK;
-    if ((int)blockIdx.x < parts.shared_blocks) {
-        const int per = parts.shared_slots * HK, part = uniform(blockIdx.x / per), block = blockIdx.x - part * per;
+    const int bx = blockIdx.x;
+    if (bx < parts.shared_blocks) {
+        const int per = parts.shared_slots * HK, part = uniform(bx / per), block = bx - part * per;
         if constexpr (SHARED_TOKENS) tokens_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
         else rows_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
     } else {
-        const int x = blockIdx.x - parts.shared_blocks, per = parts.own_slots * HK;
+        const int x = bx - parts.shared_blocks, per = parts.own_slots * HK;
         const int part = uniform(x / per), block = x - part * per;
         if constexpr (OWN_TOKENS) tokens_body<D>(OwnKeys{p}, parts.own, parts.own_slots, block, part, s_mem);
         else rows_body<D>(OwnKeys{p}, parts.own, parts.own_slots, block, part, s_mem);
@@ -106,13 +107,25 @@ __global__ __launch_bounds__(256, 2) void prefix_f32_kernel(const PrefixArgs p, 
 }
 
 // Joins the parts of a row and head (at most 64), a wavefront each, in a fixed order; a lane has
-// D / 64 dimensions (96: two of three lanes' worth).
-template <typename T, int D>
+// D / 64 dimensions (96: two of three lanes' worth). What the parts hold is loaded before it is known
+// whether the row is anybody's: it only has to be there. AHEAD of them at once, as many as there are.
+template <typename T, int D, int AHEAD>
 __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, const PrefixParts parts) {
+    constexpr int E = D == 64 ? 1 : 2;
+    typedef float wide __attribute__((ext_vector_type(E)));
     const WindowArgs &a = p.w;
     const WindowShape &s = a.s;
-    const int lane = lane_id();
+    const int lane = lane_id(), n_own = parts.own.n, n_all = n_own + parts.shared.n;
     const int64_t at = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6), all = (int64_t)s.T * s.H;
+    const bool line = at < all, has = lane * E < D;
+    const float *src = parts.own.o + (line ? at : 0) * D + (has ? lane * E : 0);
+    float2 x = {-INFINITY, 0.f};
+    wide v[AHEAD];
+    if (line) {
+        if (lane < n_all) x = *reinterpret_cast<const float2 *>(parts.own.ml + (lane * all + at) * 2);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) v[i] = *reinterpret_cast<const wide *>(src + min(i, n_all - 1) * all * D);
+    }
     const bool ordered = offsets_ordered(a.offsets, s.B, s.T) &&
                          (p.groups == 0 || offsets_ordered(p.group_offsets, p.groups, s.B));
     if (!ordered) {
@@ -120,18 +133,12 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, co
             for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
         return;
     }
-    if (at >= all) return;
+    if (!line) return;
     const int row = uniform((int)(at / s.H)), h = (int)(at - (int64_t)row * s.H);
     if (row < a.offsets[0] || row >= a.offsets[s.B]) return;
-    int n = parts.own.n;
-    if (p.groups > 0 && row >= a.offsets[p.group_offsets[0]] && row < a.offsets[p.group_offsets[p.groups]])
-        n += parts.shared.n;
-    const int64_t stride = all;  // (own parts, then shared ones)
-    float m = -INFINITY, l = 0.f;
-    if (lane < n) {
-        const float2 x = *reinterpret_cast<const float2 *>(parts.own.ml + (lane * stride + at) * 2);
-        m = x.x, l = x.y;
-    }
+    int n = n_own;
+    if (p.groups > 0 && row >= a.offsets[p.group_offsets[0]] && row < a.offsets[p.group_offsets[p.groups]]) n = n_all;
+    const float m = lane < n ? x.x : -INFINITY, l = lane < n ? x.y : 0.f;
     const float own = readlane_f(l, 0), shared = readlane_f(l, n - 1);  // (all parts of a bad list say the same)
     if (own == kLeftRow) return;
     T *out = static_cast<T *>(a.out) + at * D;
@@ -143,20 +150,15 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, co
     float top = m;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    const float f = __builtin_amdgcn_exp2f(m - top);
+    const float f = lane < n ? __builtin_amdgcn_exp2f(m - top) : 0.f;
     float sum = f * l;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-    constexpr int E = D == 64 ? 1 : 2;
-    const bool has = lane * E < D;
-    const float *src = parts.own.o + at * D + (has ? lane * E : 0);
-    float o[E] = {};
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float fi = readlane_f(f, i);
+    wide o = (wide)0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(fi, src[i * stride * D + e], o[e]);
-    }
+    for (int i = 0; i < AHEAD; ++i)
+        if (i < n) o += readlane_f(f, i) * v[i];
+    for (int i = AHEAD; i < n; ++i) o += readlane_f(f, i) * *reinterpret_cast<const wide *>(src + i * all * D);
     if (has) {
 #pragma unroll
         for (int e = 0; e < E; ++e) out[lane * E + e] = (T)(o[e] / sum);
@@ -170,15 +172,20 @@ static bool covers(const bole_prefix_dims_t &d) {
            (d.head_dim == 64 || d.head_dim == 96 || d.head_dim == 128) && d.batch > 0;
 }
 
-static int parts_for(int64_t workgroups, int64_t keys, int most) {
-    int64_t n = (512 + workgroups - 1) / workgroups;
+// Parts so that `wanted` workgroups run, no more than one for each 256 keys begun, nor than `most`.
+static int parts_for(int64_t workgroups, int64_t keys, int wanted, int most) {
+    int64_t n = (wanted + workgroups - 1) / workgroups;
     if (n > (keys + 255) / 256) n = (keys + 255) / 256;
     return (int)(n > most ? most : n < 1 ? 1 : n);
 }
 
-// From a call's sizes alone, by windowed attention's rules (window_mfma.hip): the tokens form for up
-// to one of its tiles a list on average, parts so that 512 workgroups run on either kind of list, but
-// no more than one for each 256 keys begun. Lengths are not known here: the lists' longest count.
+// From a call's sizes alone: the tokens form for up to one of its tiles a list on average, as windowed
+// attention's rule; of own lists parts so that 512 workgroups run, of prefixes 256, one a CU with the
+// own lists' beside them, as a part's sums are written and read again (64 tokens over 16384: 51 us,
+// with 384 or 512 workgroups 59 and 64; 128 tokens 65, 66 and 69). Where that is three parts or fewer
+// it would leave some CUs two workgroups and others one: 512 (trees over one prefix of 8192 tokens 105
+// and 108 us in four and five parts, 113 in three; over four prefixes of up to 8192 81 us in five parts,
+// 88 in four). Lengths are not known here: the longest count.
 static PrefixPlan plan(const bole_prefix_dims_t &d) {
     PrefixPlan p;
     const int64_t G = d.heads / d.kv_heads, rows = d.total_rows * G;
@@ -188,13 +195,14 @@ static PrefixPlan plan(const bole_prefix_dims_t &d) {
     const int own = p.f32 ? kF32Tile : p.own_tokens ? kTokenTile : kRowTile;
     const int shared = p.f32 ? kF32Tile : p.shared_tokens ? kTokenTile : kRowTile;
     p.own_slots = (int)(rows / own + d.batch);
-    p.own_parts = parts_for((int64_t)p.own_slots * d.kv_heads, (int64_t)d.max_pages * d.page_size + 1, 16);
+    p.own_parts = parts_for((int64_t)p.own_slots * d.kv_heads, (int64_t)d.max_pages * d.page_size + 1, 512, 16);
     p.shared_slots = (int)(d.groups == 1 ? (rows > 0 ? (rows + shared - 1) / shared : 1) : rows / shared + d.groups);
-    p.shared_parts = 0;
-    if (d.groups > 0)
-        p.shared_parts = parts_for((int64_t)p.shared_slots * d.kv_heads, (int64_t)d.max_prefix_pages * d.page_size, 48);
-    else
-        p.shared_slots = 0;
+    if (d.groups > 0) {
+        const int64_t blocks = (int64_t)p.shared_slots * d.kv_heads;
+        p.shared_parts = parts_for(blocks, (int64_t)d.max_prefix_pages * d.page_size, blocks > 85 ? 512 : 256, 48);
+    } else {
+        p.shared_slots = p.shared_parts = 0;
+    }
     return p;
 }
 
@@ -211,6 +219,17 @@ bool prefix_mfma_applies(const bole_prefix_dims_t &d, const PrefixArgs &a) {
     return covers(d) && bits % 16 == 0;
 }
 
+template <typename T, int D>
+static hipError_t launch_join(const PrefixArgs &a, const PrefixParts &parts, hipStream_t stream) {
+    const int64_t lines = (int64_t)a.w.s.T * a.w.s.H;
+    const dim3 grid((unsigned)(lines > 0 ? (lines + 3) / 4 : 1)), block(256);
+    const int n = parts.own.n + parts.shared.n;
+    if (n <= 3) prefix_join_kernel<T, D, 3><<<grid, block, 0, stream>>>(a, parts);
+    else if (n <= 8) prefix_join_kernel<T, D, 8><<<grid, block, 0, stream>>>(a, parts);
+    else prefix_join_kernel<T, D, 16><<<grid, block, 0, stream>>>(a, parts);
+    return hipGetLastError();
+}
+
 template <int D>
 static hipError_t launch_width(const PrefixArgs &a, const PrefixPlan &p, const PrefixParts &parts, hipStream_t stream) {
     const int64_t HK = a.w.s.HK;
@@ -221,11 +240,7 @@ static hipError_t launch_width(const PrefixArgs &a, const PrefixPlan &p, const P
     else prefix_kernel<D, false, false><<<grid, block, 0, stream>>>(a, parts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t lines = (int64_t)a.w.s.T * a.w.s.H;
-    const dim3 join((unsigned)(lines > 0 ? (lines + 3) / 4 : 1));
-    if (p.f32) prefix_join_kernel<float, D><<<join, block, 0, stream>>>(a, parts);
-    else prefix_join_kernel<__bf16, D><<<join, block, 0, stream>>>(a, parts);
-    return hipGetLastError();
+    return p.f32 ? launch_join<float, D>(a, parts, stream) : launch_join<__bf16, D>(a, parts, stream);
 }
 
 hipError_t launch_prefix_mfma(const PrefixArgs &a, const bole_prefix_dims_t &d, void *workspace, hipStream_t stream) {
