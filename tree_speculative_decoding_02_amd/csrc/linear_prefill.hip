@@ -59,6 +59,19 @@ __device__ __forceinline__ double scan_f64(double x) {
     return x;
 }
 
+// A workgroup's slot, head and column group. Of each slot's heads and groups every XCD (workgroups are
+// dealt to the eight in turn) has an eighth, neighbours, as those that share keys read the same lines;
+// the spare slots, the last ones, are spread over all.
+__device__ __forceinline__ void unit_of(const LinearPlan &p, int H, int &slot, int &h, int &cg) {
+    const int each = H * p.groups;  // units of a slot
+    int unit = blockIdx.x;
+    slot = unit / each;
+    unit -= slot * each;
+    if (each % 8 == 0) unit = (unit % 8) * (each / 8) + unit / 8;
+    h = unit / p.groups;
+    cg = unit - h * p.groups;
+}
+
 template <int DK>
 __device__ __forceinline__ int row_at(int row, int c) {  // as delta_prefill.hip's K
     return row * DK + 8 * (c ^ (DK == 128 ? ((row & 3) << 2 | ((row >> 2) & 3))
@@ -83,13 +96,9 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
     __shared__ __align__(16) __bf16 s_p[LOCAL ? 1 : NK][6][64][8];
     __shared__ __align__(16) float s_w[2][4][kChunk];  // L in two terms, 2^L, 2^{L_64 - L}
     const DeltaShape &s = a.s;
-    // the units of one XCD (workgroups are dealt to the eight in turn) are neighbours: heads that
-    // share keys, and column groups, read the same lines
-    const int units = p.slots * s.H * p.groups, per = (units + 7) / 8;
-    const int unit = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-    if ((int)(blockIdx.x / 8) >= per || unit >= units) return;
-    const int slot = unit / (s.H * p.groups), rest = unit - slot * s.H * p.groups;
-    const int h = rest / p.groups, cg = rest - h * p.groups, hk = h / (s.H / s.HK);
+    int slot, h, cg;
+    unit_of(p, s.H, slot, h, cg);
+    const int hk = h / (s.H / s.HK);
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
     const Located l = locate(a.offsets, s.B, s.T, p.seg, slot);
@@ -466,13 +475,22 @@ static int column_tiles(const bole_linear_dims_t &d) {
     return d.factor_dtype == BOLE_DTYPE_BF16 && d.d_v > 64 ? 2 : 1;
 }
 
+// From a call's sizes alone. Segments so that 512 workgroups run, of at least four chunks, since each
+// costs a state's way through memory, and K and V are read twice (one 32768-token prompt of 32 heads
+// 240 us, with 256 workgroups 369, with 768 241; eight of up to 2048 tokens 115, 135 and 107; two of up
+// to 4096 58, 72 and 68). Where the sequences alone give 512, they are cut only from four times their
+// average length on (32 of up to 2048 tokens 215 us whole, 293 cut at twice the average).
 static LinearPlan plan(const bole_linear_dims_t &d) {
     LinearPlan p;
     const int columns = 64 * column_tiles(d);
     p.groups = (d.d_v + columns - 1) / columns;
-    const int64_t chunks = (d.total_tokens + kChunk - 1) / kChunk;
-    int64_t seg = (chunks * d.heads * p.groups + 1535) / 1536;
+    const int64_t chunks = (d.total_tokens + kChunk - 1) / kChunk, units = (int64_t)d.heads * p.groups;
+    int64_t seg = (chunks * units + 511) / 512;
     if (seg < 4) seg = 4;
+    if (d.batch * units >= 512) {
+        const int64_t most = 4 * ((chunks + d.batch - 1) / d.batch);
+        if (seg < most) seg = most;
+    }
     if (seg * kChunk >= d.total_tokens) seg = chunks > 0 ? chunks : 1;
     p.seg = (int)(seg * kChunk);
     p.slots = d.total_tokens / p.seg + d.batch;
@@ -496,7 +514,7 @@ template <typename TF, int DK, int CT, bool WHOLE>
 static hipError_t launch_shape(const LinearArgs &a, const LinearPlan &p, const LinearSpace &w, bool cut,
                                hipStream_t stream) {
     const int64_t units = (int64_t)p.slots * a.s.H * p.groups;
-    const dim3 grid((unsigned)((units + 7) / 8 * 8)), block(256);
+    const dim3 grid((unsigned)units), block(256);
     if (cut) {
         linear_chunk_kernel<TF, DK, CT, WHOLE, true><<<grid, block, 0, stream>>>(a, p, w);
         hipError_t e = hipGetLastError();
