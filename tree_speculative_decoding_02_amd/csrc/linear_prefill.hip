@@ -31,15 +31,12 @@ struct LinearPlan {
     int seg, slots, groups;
 };
 
-// Workspace: of each sequence of more than one segment, from slot 2 floor(first row / seg) on (a
-// sequence of n > seg rows has at most 2 floor(n / seg) segments, so they do not meet), [slot][head]:
-// the state in the order of the accumulators, then its decay.
+// Workspace (space_slot, linear_device.h), [slot][head]: the state in the order of the accumulators,
+// then its decay.
 struct LinearSpace {
     f32x4 *s;      // [slot][H][column tile][row tile][64]
     float *decay;  // [slot][H]
 };
-
-__device__ __forceinline__ size_t space_slot(int lo, int seg, int i) { return 2 * (size_t)(lo / seg) + i; }
 
 // Inclusive sum over lanes 0 .. lane, in fp64, by moves within the vector registers.
 template <int CTRL, int ROWS>
@@ -497,17 +494,15 @@ static LinearPlan plan(const bole_linear_dims_t &d) {
     return p;
 }
 
-static size_t spaces(const bole_linear_dims_t &d, const LinearPlan &p) {
-    return d.total_tokens > p.seg ? 2 * (size_t)(d.total_tokens / p.seg) : 0;
-}
-
 static int row_width(const bole_linear_dims_t &d) { return d.d_k <= 64 ? 64 : 128; }
 
 size_t linear_prefill_workspace(const bole_linear_dims_t &d) {
-    if (!chunked(d)) return 0;
+    const size_t walk = linear_walk_workspace(d);  // (of rows that are not on 16-byte addresses too)
+    if (!chunked(d)) return walk;
     const LinearPlan p = plan(d);
     const size_t state = (size_t)p.groups * 64 * column_tiles(d) * row_width(d) + 4;  // (and its decay)
-    return spaces(d, p) * d.heads * state * sizeof(float);
+    const size_t need = space_slots(d.total_tokens, p.seg) * d.heads * state * sizeof(float);
+    return need > walk ? need : walk;
 }
 
 template <typename TF, int DK, int CT, bool WHOLE>
@@ -546,9 +541,9 @@ hipError_t launch_linear_prefill(float *H0, const void *q, const void *k, const 
     const LinearArgs a = {H0, q, k, v, gate, seq_offsets, out, seq_status, shape(d)};
     const uintptr_t rows = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
                            reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(out);
-    if (!chunked(d) || rows % 16 != 0) return launch_linear_walk(a, d, true, stream);
+    if (!chunked(d) || rows % 16 != 0) return launch_linear_walk(a, d, workspace, stream);
     const LinearPlan p = plan(d);
-    const size_t n = spaces(d, p) * d.heads;
+    const size_t n = space_slots(d.total_tokens, p.seg) * d.heads;
     const LinearSpace w = {static_cast<f32x4 *>(workspace),
                            static_cast<float *>(workspace) + n * p.groups * 64 * column_tiles(d) * row_width(d)};
     if (d.factor_dtype == BOLE_DTYPE_F32) return launch_width<float, 1>(a, p, w, n > 0, stream);
@@ -560,7 +555,7 @@ hipError_t launch_linear_step(float *H0, const void *q, const void *k, const voi
                               const float *gate, void *out, const bole_linear_dims_t &d,
                               hipStream_t stream) {
     const LinearArgs a = {H0, q, k, v, gate, nullptr, out, nullptr, shape(d)};
-    return launch_linear_walk(a, d, false, stream);
+    return launch_linear_step_walk(a, d, stream);
 }
 
 }  // namespace bole
