@@ -134,33 +134,24 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
     constexpr int SZ = sizeof(TF), ROWS = 256 / CH, VROWS = 256 / (VC / 8);
     const uint32_t skb = (uint32_t)(sk * SZ), svb = (uint32_t)(sv * SZ);
     const int kc = WHOLE || 8 * (tid % CH) < dk ? tid % CH : 0, vc = WHOLE || 8 * (tid % (VC / 8)) < left ? tid % (VC / 8) : 0;
-    const uint32_t koff = (uint32_t)(tid / CH) * skb + 8 * SZ * kc, voff = (uint32_t)(tid / (VC / 8)) * svb + 8 * SZ * vc;
+    const uint32_t krow = (uint32_t)(tid / CH) * skb, vrow = (uint32_t)(tid / (VC / 8)) * svb;
     RowPart<TF> kr[PER], qr[LOCAL ? 1 : PER], vr[VPER];
     auto fetch = [&](int chunk) {
-        const int first = chunk * kChunk, most = n - 1 - first;
+        const int first = chunk * kChunk;
+        const uint32_t most = min(n - 1 - first, kChunk - 1);
         const char *k0 = reinterpret_cast<const char *>(kb) + (size_t)first * skb;
         const char *q0 = reinterpret_cast<const char *>(qb) + (size_t)first * skb;
         const char *v0 = reinterpret_cast<const char *>(vb) + (size_t)first * svb;
-        if (most >= kChunk - 1) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                kr[j].load(reinterpret_cast<const TF *>(k0 + (size_t)(ROWS * j) * skb + koff));
-                if constexpr (!LOCAL) qr[j].load(reinterpret_cast<const TF *>(q0 + (size_t)(ROWS * j) * skb + koff));
-            }
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t off = min(krow + ROWS * j * skb, most * skb) + 8 * SZ * kc;
+            kr[j].load(reinterpret_cast<const TF *>(k0 + off));
+            if constexpr (!LOCAL) qr[j].load(reinterpret_cast<const TF *>(q0 + off));
+        }
 #pragma unroll
-            for (int j = 0; j < VPER; ++j)
-                vr[j].load(reinterpret_cast<const TF *>(v0 + (size_t)(VROWS * j) * svb + voff));
-        } else {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const uint32_t off = (uint32_t)min(tid / CH + ROWS * j, most) * skb + 8 * SZ * kc;
-                kr[j].load(reinterpret_cast<const TF *>(k0 + off));
-                if constexpr (!LOCAL) qr[j].load(reinterpret_cast<const TF *>(q0 + off));
-            }
-#pragma unroll
-            for (int j = 0; j < VPER; ++j)
-                vr[j].load(reinterpret_cast<const TF *>(
-                    v0 + (uint32_t)min(tid / (VC / 8) + VROWS * j, most) * svb + 8 * SZ * vc));
+        for (int j = 0; j < VPER; ++j) {
+            const uint32_t off = min(vrow + VROWS * j * svb, most * svb) + 8 * SZ * vc;
+            vr[j].load(reinterpret_cast<const TF *>(v0 + off));
         }
         if (!WHOLE) {
 #pragma unroll
@@ -174,23 +165,23 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
                 if (8 * (tid % (VC / 8)) >= left) vr[j].clear();
         }
     };
-    // places of operand pieces in s_k and s_q: part 4 ks + g of row tile_token(m, col), and rows
-    // 32 sb + 8 g + 4 half .. + 3 of a transposing read's part of row tile j (what is added to a row in
-    // multiples of 32 leaves its permutation)
-    int opnd[2][KS], trans[2][KS];
+    // Places of operand pieces in s_k and s_q: part 4 ks + g of row tile_token(m, col), and rows
+    // 32 sb + 8 g + 4 half .. + 3 of a transposing read's part of row tile j. What is added to a row in
+    // multiples of 32 leaves its permutation, and a step of ks flips bits of the place: two places each,
+    // as all sixteen would take registers that prefetched rows need.
+    int opnd[2], trans[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            opnd[x][ks] = row_at<DK>(tile_token(x, col), 4 * ks + g);
-            trans[x][ks] = row_at<DK>(8 * g + (col >> 2) + 4 * x, 4 * ks + (col & 3));
-        }
-    auto operand = [&](const __bf16 *from, int m, int ks) { return load16(from + opnd[m & 1][ks] + 32 * (m >> 1) * DK); };
+    for (int x = 0; x < 2; ++x) {
+        opnd[x] = row_at<DK>(tile_token(x, col), g);
+        trans[x] = row_at<DK>(8 * g + (col >> 2) + 4 * x, col & 3);
+    }
+    auto operand = [&](const __bf16 *from, int m, int ks) { return load16(from + (opnd[m & 1] ^ 32 * ks) + 32 * (m >> 1) * DK); };
     auto stage = [&]() {
         bf16x8 y[NK];
+        static_assert(ROWS % 16 == 0, "rows that keep their permutation");
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int at = row_at<DK>(tid / CH + 256 / CH * j, tid % CH);
+            const int at = row_at<DK>(tid / CH, tid % CH) + ROWS * j * DK;
             kr[j].terms(y);
 #pragma unroll
             for (int i = 0; i < NK; ++i) *reinterpret_cast<bf16x8 *>(&s_k[i][at]) = y[i];
@@ -248,20 +239,24 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
     }
     stage();
     lds_barrier();
+    char *ob = reinterpret_cast<char *>(static_cast<TF *>(a.out) + row0 * sv + (size_t)h * s.DV + cg * VC);
+    const uint32_t ooff = (uint32_t)tile_token(0, col) * svb + (c0 + 4 * g) * SZ;
     int chunk = 0;
     do {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) asm volatile("" : "+v"(opnd[x]), "+v"(trans[x]));  // (worked out anew in each turn)
         const float(*wt)[kChunk] = s_w[chunk & 1];
         f32x4 o[CT][4];
         if constexpr (!LOCAL) {
             // ---- P: the wavefront's row tile, as operand pieces
-            const int i = tile_token(wave, col);
+            const int i = tile_token(wave, col), above = i - 8 * g;  // j <= i in each lane's own numbers
             const float li = wt[0][i], lr = wt[1][i];
             f32x4 pair[4];
             bf16x8 own_q[KS][NK];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int t = 0; t < NK; ++t) own_q[ks][t] = load16(s_q[t] + row_at<DK>(i, 4 * ks + g));
+                for (int t = 0; t < NK; ++t) own_q[ks][t] = load16(s_q[t] + ((wave & 1 ? opnd[1] : opnd[0]) ^ 32 * ks) + 32 * (wave >> 1) * DK);
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
                 pair[jt] = (f32x4)0.f;
@@ -278,7 +273,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
                 const f32x4 ljr = *reinterpret_cast<const f32x4 *>(&wt[1][j0]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    pair[jt][r] *= j0 + r <= i ? __builtin_amdgcn_exp2f((li - lj[r]) + (lr - ljr[r])) : 0.f;
+                    pair[jt][r] *= tile_token(jt, 0) + r <= above ? __builtin_amdgcn_exp2f((li - lj[r]) + (lr - ljr[r])) : 0.f;
             }
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb) {
@@ -344,18 +339,20 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) o[ct][m] = mfma_terms(v[ct][sb], y, o[ct][m]);
                 }
-            TF *ob = static_cast<TF *>(a.out) + row0 * sv + (size_t)h * s.DV + cg * VC + c0 + 4 * g;
+            char *o0 = ob + (size_t)(chunk * kChunk) * svb;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const int t = chunk * kChunk + tile_token(m, col);
-                if (t >= n) continue;
+                const int token = 32 * (m >> 1) + 4 * (m & 1);  // of the lane's first one
+                if (tile_token(0, col) + token >= n - chunk * kChunk) continue;
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
                     if (WHOLE || c0 + 16 * ct + 4 * g < left)
-                        *reinterpret_cast<tf4 *>(ob + (size_t)t * sv + 16 * ct) = __builtin_convertvector(o[ct][m], tf4);
+                        *reinterpret_cast<tf4 *>(o0 + (size_t)token * svb + (ooff + 16 * SZ * ct)) =
+                            __builtin_convertvector(o[ct][m], tf4);
             }
         }
         fetch(min(chunk + 1, chunks - 1));
+        __builtin_amdgcn_sched_barrier(0);  // (they would sink to behind the products)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -381,8 +378,8 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
                 bf16x8 x[NK];
 #pragma unroll
                 for (int t = 0; t < NK; ++t)
-                    x[t] = join(read_transposed(s_k[t] + trans[0][j >> 1] + 32 * sb * DK + 4 * (j & 1)),
-                                read_transposed(s_k[t] + trans[1][j >> 1] + 32 * sb * DK + 4 * (j & 1)));
+                    x[t] = join(read_transposed(s_k[t] + (trans[0] ^ 32 * (j >> 1)) + 32 * sb * DK + 4 * (j & 1)),
+                                read_transposed(s_k[t] + (trans[1] ^ 32 * (j >> 1)) + 32 * sb * DK + 4 * (j & 1)));
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) st[ct][j] = mfma_terms(x, ev[ct][sb], st[ct][j]);
             }
@@ -463,8 +460,10 @@ static DeltaShape shape(const bole_linear_dims_t &d) {
 }
 
 static bool chunked(const bole_linear_dims_t &d) {
+    // row offsets within a chunk are 32-bit
+    const int64_t row = (int64_t)d.heads * (d.d_v > d.d_k ? d.d_v : d.d_k) * (d.factor_dtype == BOLE_DTYPE_F32 ? 4 : 2);
     return !(d.flags & BOLE_FLAG_FORCE_GENERIC) && d.gate_kind == BOLE_GATE_SCALAR && d.d_k <= 128 &&
-           d.d_k % 8 == 0 && d.d_v % 8 == 0 && d.batch > 0;
+           d.d_k % 8 == 0 && d.d_v % 8 == 0 && d.batch > 0 && row * kChunk <= 0x7fffffffLL;
 }
 
 // Column tiles a wavefront: two from 65 columns on in bf16 (K's and Q's reads from LDS then serve both).
