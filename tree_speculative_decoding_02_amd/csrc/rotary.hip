@@ -4,7 +4,8 @@
 //
 // A row's angles are the same for all of its heads: they are taken once, in fp64, reduced to one
 // turn, and their sines and cosines kept in LDS (an fp32 angle at position 2^20 is off by 2^-5).
-// Bound by the rows' way through HBM: 2 bytes read and 2 written an element in bf16.
+// Bound by the rows' way through HBM, 2 bytes read and 2 written an element in bf16: two prompts of 8192
+// tokens, 32 query and 8 key heads of 128, 71 us (4.7 TB/s); 64 single tokens 4.8 us, launch and chain.
 #include <cmath>
 
 #include "delta_device.h"
@@ -114,8 +115,8 @@ __global__ __launch_bounds__(256) void rotary_generic_kernel(const RotaryArgs a,
 // Heads whose lanes hold 8 consecutive elements each: LP lanes a head (8 LP >= d), 256 / LP heads at
 // a time, of ROWS neighbouring rows. The other half of a pair (j, j + half) is another lane's.
 //
-// With ROWS 1 the heads are dealt to gridDim.y workgroups, so that a row is one pass: for few rows,
-// where the chain of loads behind a row's position is what takes time.
+// With ROWS 1 the heads of few rows are dealt to gridDim.y workgroups: what takes time there is the
+// chain of loads behind a row's position.
 template <typename T> struct Eight;  // 8 elements as loaded
 template <> struct Eight<__bf16> {
     uint4 x;
@@ -172,111 +173,114 @@ __device__ __forceinline__ float sum_lanes(float x) {
     return x;
 }
 
+// What multiplies an element and its pair's other one, for each row: weight times cosine and, with
+// its sign, the other's weight times sine. So a head costs three operations an element (with both
+// weights and the angle apart it was bound by the vector units: two prompts of 8192 tokens 84 us).
+// Element 8 c + i of a head at [i / 4][c][i % 4], so that neighbouring lanes read 16-byte neighbours.
+template <int LP, int ROWS>
+struct RotaryTables {
+    float own[ROWS][2][8 * LP], other[ROWS][2][8 * LP];  // [row][query or key]
+    int pos[ROWS];
+    static __device__ __forceinline__ int at(int e) { return ((e >> 2) & 1) * 4 * LP + (e >> 3) * 4 + (e & 3); }
+};
+
 template <typename T, int LP, bool INTER, int ROWS>
 __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
-    __shared__ __align__(16) float s_cos[ROWS][kMaxPairs], s_sin[ROWS][kMaxPairs];
-    __shared__ int s_pos[ROWS];
+    __shared__ __align__(16) RotaryTables<LP, ROWS> t;
     const int tid = threadIdx.x, wave = tid >> 6, row0 = blockIdx.x * ROWS, P = a.R / 2;
-    const int heads = a.H + a.HK, rows = min(ROWS, a.T - row0), items = rows * heads;
+    const int rows = min(ROWS, a.T - row0);
     const int c = tid % LP, part = 8 * c;               // the lane's elements of its head
-    const bool in = part < a.D, turned = part < a.R;
+    const bool in = part < a.D;
     const int half = P / 8;                             // pairs (j, j + half): the other's lane
-    const bool second = c >= half;
-    const int other = (tid & 63) + (second ? -half : half);
-    struct Item {
-        int r, h;
-        bool key, live;
-        Eight<T> x;
-    };
-    auto fetch = [&](int first) {
-        Item t;
-        const int i = min(first + tid / LP, items - 1);
-        t.live = in && first + tid / LP < items;
-        t.r = ROWS == 1 ? 0 : i / heads;
-        t.h = i - t.r * heads;
-        t.key = t.h >= a.H;
-        t.h -= t.key ? a.H : 0;
-        const T *x = static_cast<const T *>(t.key ? a.k : a.q) +
-                     (size_t)(row0 + t.r) * (t.key ? a.k_stride : a.q_stride) + t.h * a.D + (in ? part : 0);
-        t.x.load(x);
-        return t;
-    };
+    const int from = (tid & 63) + (c >= half ? -half : half);
     constexpr int STEP = 256 / LP;
-    int first = blockIdx.y * STEP;
-    if (a.T == 0 || first >= items) {
+    // a pass takes STEP heads of the rows' queries, then of their keys
+    const int q_passes = (rows * a.H + STEP - 1) / STEP, passes = q_passes + (rows * a.HK + STEP - 1) / STEP;
+    int pass = blockIdx.y;
+    if (a.T == 0 || pass >= passes) {
         if (a.T == 0 && wave == 0) row_position(a, 0);  // reports sequences without rows
         return;
     }
-    Item t = fetch(first);
+    struct Item {
+        int r, h;
+        bool live;
+        Eight<T> x;
+    };
+    auto fetch = [&](int p) {
+        const bool key = p >= q_passes;
+        const int heads = key ? a.HK : a.H, i = (key ? p - q_passes : p) * STEP + tid / LP;
+        const T *x = static_cast<const T *>(key ? a.k : a.q);
+        const int64_t stride = key ? a.k_stride : a.q_stride;
+        Item y;
+        y.live = in && i < rows * heads;
+        // (exact: below 2^19 halves and whole numbers lie apart in fp32 by more than the product's error)
+        y.r = ROWS == 1 ? 0 : min((int)(((float)i + 0.5f) * (1.f / (float)heads)), rows - 1);
+        y.h = min(i - y.r * heads, heads - 1);
+        y.x.load(x + (size_t)row0 * stride + (size_t)y.r * stride + (uint32_t)(y.h * a.D + (in ? part : 0)));
+        return y;
+    };
+    Item y = fetch(pass);
     // every wavefront (ROWS 1), or wavefront w for row w
     int pos = kNoRow;
     if (ROWS == 1 || wave < rows) {
         pos = row_position(a, row0 + (ROWS == 1 ? 0 : wave));
-        if (ROWS > 1 && lane_id() == 0) s_pos[wave] = pos;
+        if (ROWS > 1 && lane_id() == 0) t.pos[wave] = pos;
     }
     if constexpr (ROWS > 1) __syncthreads();
-    for (int i = tid; i < rows * P; i += 256) {
-        const int r = ROWS == 1 ? 0 : i / P, j = i - r * P;
-        const int at = ROWS == 1 ? pos : s_pos[r];
-        if (at < 0) continue;
-        const float2 y = turn_of(at, a.inv_freq[j]);
-        s_cos[r][j] = y.x, s_sin[r][j] = y.y;
+    for (int k = tid; k < rows * (a.D - P); k += 256) {  // pairs, then elements that are not turned
+        const int r = ROWS == 1 ? 0 : k / (a.D - P), j = k - r * (a.D - P);
+        const int at = ROWS == 1 ? pos : t.pos[r];
+        if (at == kNoRow) continue;
+        const bool pair = j < P;
+        const int ea = !pair ? j + P : INTER ? 2 * j : j, eb = INTER ? 2 * j + 1 : j + P;
+        const float2 turn = pair && at >= 0 ? turn_of(at, a.inv_freq[j]) : float2{1.f, 0.f};
+        const float bad = at == kNanRowAt ? __builtin_nanf("") : 1.f;
+#pragma unroll
+        for (int key = 0; key < 2; ++key) {
+            const T *w = static_cast<const T *>(key ? a.k_weight : a.q_weight);
+            const float wa = w ? to_f32(w[ea]) : 1.f, wb = w && pair ? to_f32(w[eb]) : 1.f;
+            t.own[r][key][t.at(ea)] = bad * wa * turn.x;
+            t.other[r][key][t.at(ea)] = -wb * turn.y;
+            if (pair) {
+                t.own[r][key][t.at(eb)] = bad * wb * turn.x;
+                t.other[r][key][t.at(eb)] = wa * turn.y;
+            }
+        }
     }
     __syncthreads();
-    for (; first < items; first += STEP * gridDim.y) {
-        Item next = t;
-        if (first + STEP * (int)gridDim.y < items) next = fetch(first + STEP * gridDim.y);
-        const T *w = static_cast<const T *>(t.key ? a.k_weight : a.q_weight);
-        float v[8], u[8], sum = 0.f;
+    const float inv_d = 1.f / (float)a.D;
+    for (; pass < passes; pass += gridDim.y) {
+        Item next = y;
+        if (pass + (int)gridDim.y < passes) next = fetch(pass + gridDim.y);
+        const bool key = pass >= q_passes;
+        float v[8], u[8], sum = 0.f, scale = 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = t.x.get(e);
-            sum = fmaf(in ? v[e] : 0.f, v[e], sum);
+        for (int e = 0; e < 8; ++e) v[e] = y.x.get(e);
+        if (key ? a.k_weight != nullptr : a.q_weight != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+            const float mean = fmaf(sum_lanes<LP>(in ? sum : 0.f), inv_d, a.eps);
+            const bool tiny = mean < 0x1p-100f;  // (the instruction takes no denormals)
+            scale = __builtin_amdgcn_rsqf(tiny ? mean * 0x1p64f : mean) * (tiny ? 0x1p32f : 1.f);
         }
-        sum = sum_lanes<LP>(in ? sum : 0.f);
-        Eight<T> x2 = t.x, w1, w2;
-        if (!INTER && P > 0) x2 = t.x.from(other);
-        const int at = ROWS == 1 ? pos : s_pos[t.r];
-        if (w) {
-            const float scale = 1.f / sqrtf(sum / a.D + a.eps);
-            w1.load(w + (in ? part : 0));
-            w2 = w1;
-            if (!INTER && turned) w2.load(w + part + (second ? -P : P));
+        if constexpr (INTER) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = v[e] * scale * w1.get(e);
-                u[e] = x2.get(e) * scale * w2.get(e);
-            }
+            for (int e = 0; e < 8; ++e) u[e] = part < a.R ? v[e ^ 1] : 0.f;
         } else {
+            Eight<T> z = y.x;
+            if (P > 0) z = y.x.from(from);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = x2.get(e);
+            for (int e = 0; e < 8; ++e) u[e] = part < a.R ? z.get(e) : 0.f;
         }
-        if (turned && at >= 0) {
-            if constexpr (INTER) {
-                const f32x4 co = *reinterpret_cast<const f32x4 *>(&s_cos[t.r][part / 2]);
-                const f32x4 si = *reinterpret_cast<const f32x4 *>(&s_sin[t.r][part / 2]);
+        const f32x4 *own = reinterpret_cast<const f32x4 *>(t.own[y.r][key]) + c;
+        const f32x4 *other = reinterpret_cast<const f32x4 *>(t.other[y.r][key]) + c;
+        const f32x4 ow[2] = {own[0], own[LP]}, ot[2] = {other[0], other[LP]};
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float x = v[e], y = v[e + 1];
-                    v[e] = fmaf(-y, si[e / 2], x * co[e / 2]);
-                    v[e + 1] = fmaf(x, si[e / 2], y * co[e / 2]);
-                }
-            } else {
-                const int j = second ? part - P : part;
-                const f32x4 *co = reinterpret_cast<const f32x4 *>(&s_cos[t.r][j]), *si = reinterpret_cast<const f32x4 *>(&s_sin[t.r][j]);
-                const f32x4 cs[2] = {co[0], co[1]}, sn[2] = {si[0], si[1]};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = fmaf(second ? u[e] : -u[e], sn[e >> 2][e & 3], v[e] * cs[e >> 2][e & 3]);
-            }
-        }
-        if (at == kNanRowAt) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_nanf("");
-        }
-        if (t.live && at != kNoRow)
-            Eight<T>::store(static_cast<T *>(t.key ? a.k_out : a.q_out) +
-                            ((size_t)(row0 + t.r) * (t.key ? a.HK : a.H) + t.h) * a.D + part, v);
-        t = next;
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(u[e], ot[e >> 2][e & 3], v[e] * ow[e >> 2][e & 3]) * scale;
+        if (y.live && (ROWS == 1 ? pos : t.pos[y.r]) != kNoRow)
+            Eight<T>::store(static_cast<T *>(key ? a.k_out : a.q_out) +
+                            ((size_t)(row0 + y.r) * (key ? a.HK : a.H) + y.h) * a.D + part, v);
+        y = next;
     }
 }
 
@@ -284,12 +288,14 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
 
 template <typename T, int LP, bool INTER>
 static hipError_t launch_lanes(const RotaryArgs &a, hipStream_t stream) {
-    // four rows a workgroup once that leaves every CU two of them
-    if (a.T >= 2048) {
+    // Four rows a workgroup from 4096 rows on (2000 rows of 40 heads 13.5 us, one row each 10.7), one
+    // from 512 on, and two passes of one below (500 rows 6.4 us, one pass 7.2, whole rows 6.7).
+    if (a.T >= 4096) {
         rotary_kernel<T, LP, INTER, 4><<<dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, stream>>>(a);
     } else {
-        const int passes = ((a.H + a.HK) * LP + 255) / 256;
-        rotary_kernel<T, LP, INTER, 1><<<dim3((unsigned)(a.T > 0 ? a.T : 1), (unsigned)passes), dim3(256), 0, stream>>>(a);
+        const int passes = (a.H * LP + 255) / 256 + (a.HK * LP + 255) / 256;
+        const dim3 grid((unsigned)(a.T > 0 ? a.T : 1), a.T >= 512 ? 1u : (unsigned)(passes + 1) / 2);
+        rotary_kernel<T, LP, INTER, 1><<<grid, dim3(256), 0, stream>>>(a);
     }
     return hipGetLastError();
 }
