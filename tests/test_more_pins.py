@@ -141,6 +141,9 @@ def test_prefix_dims():
             ("flags", 2, 1), ("scale", float("nan"), 1), ("scale", 2.0 ** 127, 1), ("head_dim", 257, 2), ("page_size", 2048, 2),
             ("total_rows", 1 << 26, 2), ("max_pages", 1 << 27, 2), ("max_prefix_pages", 1 << 27, 2), ("groups", 1 << 24, 2)])
     d = base()
+    d.max_prefix_pages = (1 << 27) - 64       # its positions alone would do, a row's place behind them does not
+    assert bole.lib.bole_prefix_check_dims(ctypes.byref(d)) == 2
+    d = base()
     need = bole.lib.bole_prefix_workspace_size(ctypes.byref(d))
     P = [0x1000 * (i + 1) for i in range(13)]
     for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 11, 12):

@@ -259,7 +259,7 @@ hipError_t launch_linear_step_walk(const LinearArgs &a, const bole_linear_dims_t
 static int walk_segment(const bole_linear_dims_t &d) {
     const int64_t blocks = d.d_v % 4 == 0 ? (d.d_v + 31) / 32 : (d.d_v + 7) / 8;
     if ((int64_t)d.batch * d.heads * blocks >= 2048) return 0;
-    int64_t seg = (d.total_tokens * d.heads * blocks + 2047) / 2048;
+    int64_t seg = ((int64_t)d.total_tokens * d.heads * blocks + 2047) / 2048;
     if (seg < 16) seg = 16;
     return seg < d.total_tokens ? (int)seg : 0;
 }

@@ -133,7 +133,7 @@ bole_status_t bole_prefix_check_dims(const bole_prefix_dims_t *d) {
     // for each 16 rows a key head packs and up to three times a sequence or group (of few rows).
     const int64_t rows = d->total_rows, lists = (int64_t)d->batch + d->groups;
     if ((int64_t)d->max_pages * d->page_size + rows > (1LL << 31) - 1024 ||
-        (int64_t)d->max_prefix_pages * d->page_size > (1LL << 31) - 1024 ||
+        (int64_t)d->max_prefix_pages * d->page_size + rows > (1LL << 31) - 1024 ||
         lists * d->heads > 0x7fffffffLL || rows * d->heads >= 1LL << 26 ||
         rows * d->heads / 16 + 3 * lists * d->kv_heads >= 1LL << 24)
         return BOLE_ERR_UNSUPPORTED;
