@@ -9,6 +9,8 @@ magnitudes, an output by that and d_k 2^-24 more. With bf16 factors an output al
 before its 64 tokens as two bf16 terms (2^-17), the weights of those tokens rounded (half a step,
 2^-8), and is itself rounded.
 """
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -146,6 +148,20 @@ def test_long_prompts(lib, shape):
         w.gate.copy_(w.gate ** 0.02)  # decays near one: states that remember
         t = on_gpu(w)
         check(lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets)), t["H0"], w, w.offsets)
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 128, 128, BF16), (64, 32, 64, 128, BF16), (64, 16, 72, 136, BF16), (64, 16, 16, 72, BF16)], ids=str)
+def test_long_prompts_of_many_heads(lib, shape):
+    """The form with 128 columns a workgroup, cut and whole sequences; some heads against the oracle."""
+    w = make(18, [2160, 90], shape, gate_value=None)
+    w.gate.copy_(w.gate ** 0.02)
+    t = on_gpu(w)
+    out = lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets))
+    heads = [0, 3, 37, 63]
+    keys = [h // (shape[0] // shape[1]) for h in heads]
+    part = SimpleNamespace(H0=w.H0[:, heads], q=w.q[:, keys], k=w.k[:, keys], v=w.v[:, heads], gate=w.gate[:, heads],
+                           offsets=w.offsets)
+    check(out[:, heads], t["H0"][:, heads], part, w.offsets)
 
 
 def test_many_sequences(lib):

@@ -3,7 +3,7 @@
 //
 // A bad sequence adds nothing, so each of its rows has to know: a wavefront that finds a row's place
 // checks every page that its sequence's new tokens go to. Rows are on their way meanwhile: bound by
-// the copy, or, for accepted paths, by the chain offsets - path - pages - rows.
+// the copy, or, for accepted paths, by the chain offsets - path - pages - rows (64 of them 4.9 us).
 #include "delta_device.h"
 #include "launch.h"
 
@@ -57,8 +57,9 @@ struct Piece {
     __device__ __forceinline__ void store(size_t place, V x) const { *reinterpret_cast<V *>(to + place + head) = x; }
 };
 
-// A workgroup ROWS neighbouring rows. Eight for many rows: one 8192-row call of two sequences 42.9 us
-// with one.
+// A workgroup ROWS neighbouring rows: eight from 2048 rows on, whose loads are in flight together while
+// their places are found (8 heads of 128 in bf16: 16384 rows 28.4 us, 4.7 TB/s, with one row each 34.9; 4096
+// 8.8 and 9.2; 2048 5.7 and 5.5). Fewer rows take one each, so that more CUs have work.
 template <typename V, int ROWS>
 __global__ __launch_bounds__(256) void append_rows_kernel(const AppendArgs a, int size) {
     __shared__ size_t s_place[ROWS];

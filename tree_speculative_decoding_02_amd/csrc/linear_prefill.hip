@@ -19,6 +19,13 @@
 // terms (2^-25 left). What only the output sees may be rounded harder: S in two terms, P in one (half
 // a step of bf16 of each pair weight, once, before an output that is rounded to bf16 itself). With
 // fp32 factors K, Q, V, P and S are three terms each.
+//
+// Measured, 32 heads of 128 x 64 states, bf16: eight prompts of up to 2048 tokens (9412 in all) 115 us
+// (33 the first kernel, 11 the second, 73 the third; 2.2 TB/s of what the call cannot do without), one
+// prompt of 32768 tokens and 8 key heads 241 us (72, 8 and 161; 1.7 TB/s). What bounds the third is
+// issue: a wavefront's chunk is some 510 vector instructions and 102 matrix ones, three workgroups a
+// CU, and the one kind hardly runs beside the other. With registers for two workgroups and the next
+// chunk's loads earlier it took 208 us for the long prompt, with three and no rows ahead 171.
 #include "delta_mfma.h"
 #include "linear_device.h"
 #include "launch.h"
@@ -466,9 +473,16 @@ static bool chunked(const bole_linear_dims_t &d) {
            d.d_k % 8 == 0 && d.d_v % 8 == 0 && d.batch > 0 && row * kChunk <= 0x7fffffffLL;
 }
 
-// Column tiles a wavefront: two from 65 columns on in bf16 (K's and Q's reads from LDS then serve both).
+// Column tiles a wavefront: two, in bf16 from 65 columns on, where the call is cut into segments anyway
+// and has four chunks for each of 512 such workgroups: K's and Q's reads from LDS, and P, serve both then
+// (32 heads of 128 x 128: one 32768-token prompt 380 us, 448 with one tile; four of up to 2048 106 and
+// 121). One otherwise, for twice the workgroups and three of them a CU in place of two (eight of up to
+// 2048 148, 175 with two; 16 of them 187 and 239; one of 300 tokens 32 and 40).
 static int column_tiles(const bole_linear_dims_t &d) {
-    return d.factor_dtype == BOLE_DTYPE_BF16 && d.d_v > 64 ? 2 : 1;
+    if (d.factor_dtype != BOLE_DTYPE_BF16 || d.d_v <= 64) return 1;
+    const int64_t chunks = ((int64_t)d.total_tokens + kChunk - 1) / kChunk;
+    const int64_t one = (int64_t)d.heads * ((d.d_v + 63) / 64), two = (int64_t)d.heads * ((d.d_v + 127) / 128);
+    return d.batch * one < 512 && chunks * two >= 4 * 512 ? 2 : 1;
 }
 
 // From a call's sizes alone. Segments so that 512 workgroups run, of at least four chunks, since each

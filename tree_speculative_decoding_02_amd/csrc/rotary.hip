@@ -288,8 +288,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
 
 template <typename T, int LP, bool INTER>
 static hipError_t launch_lanes(const RotaryArgs &a, hipStream_t stream) {
-    // Four rows a workgroup from 4096 rows on (2000 rows of 40 heads 13.5 us, one row each 10.7), one
-    // from 512 on, and two passes of one below (500 rows 6.4 us, one pass 7.2, whole rows 6.7).
+    // Four rows a workgroup from 4096 rows on (40 heads of 128: 16384 rows 71 us, 77 with one row each, 4096
+    // 19.9 and 19.8, 2048 13.9 and 11.0), one from 512 on, and two passes of one below (500 rows 6.4 us, one
+    // pass 7.2, whole rows 6.7).
     if (a.T >= 4096) {
         rotary_kernel<T, LP, INTER, 4><<<dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, stream>>>(a);
     } else {
