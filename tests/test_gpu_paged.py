@@ -323,6 +323,20 @@ def test_prefix_bad_sequences(lib, force):
             assert status.tolist() == [BAD_SIZE] * 7 and (out == -7.0).all()
 
 
+@pytest.mark.parametrize("force", [False, True], ids=["fast", "generic"])
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[4]], ids=[IDS[0], IDS[4]])
+def test_one_bad_page_of_a_long_prefix(lib, shape, force):
+    """A page that does not exist, wherever it lies in a prefix that many workgroups share, is every row's."""
+    w = make(47, [1, 1, 2, 1], [3, 0, 70, 9], ([2100, 1500], [0, 2, 3]), shape)
+    for at in (0, 64, 131):
+        t = on_gpu(w)
+        t["prefix_table"][0, at] = w.k_cache.shape[0]
+        status = i32([-1] * 4)
+        out = lib.bole_prefix_attention(**t, seq_status=status, force_generic=force)
+        assert status.tolist() == [BAD_CACHE, BAD_CACHE, 0, 0]
+        assert torch.isnan(out[:2]).all() and not torch.isnan(out[2:]).any()
+
+
 def oracle_of_ok(w, parent, keep):
     """{b: (out, limit)} of the sequences `keep`, each as a batch of its own."""
     got = {}

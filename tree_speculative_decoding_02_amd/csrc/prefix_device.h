@@ -27,15 +27,21 @@ __device__ __forceinline__ Group group_of(const PrefixArgs &a, int b) {
     return x;
 }
 
+// Whether the pages of positions x0 .. x1 - 1 of prefix g exist. One wavefront.
+__device__ __forceinline__ int prefix_pages_status(const PrefixArgs &a, int g, int x0, int x1) {
+    const int shift = a.w.s.page_shift;
+    const int32_t *table = a.prefix_table + (size_t)g * a.max_prefix_pages;
+    bool bad = false;
+    if (x0 < x1)
+        for (int i = (x0 >> shift) + lane_id(); i <= (x1 - 1) >> shift; i += 64)
+            bad |= (unsigned)table[i] >= (unsigned)a.w.s.pages;
+    return __any(bad) ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
+}
+
 // Whether prefix g of len tokens lies in pages that exist. One wavefront.
 __device__ __forceinline__ int prefix_status(const PrefixArgs &a, int g, int len) {
-    const int shift = a.w.s.page_shift;
-    if (len < 0 || len > ((int64_t)a.max_prefix_pages << shift)) return BOLE_TREE_BAD_CACHE;
-    const int32_t *table = a.prefix_table + (size_t)g * a.max_prefix_pages;
-    const int pages = (int)(((int64_t)len + (1 << shift) - 1) >> shift);
-    bool bad = false;
-    for (int i = lane_id(); i < pages; i += 64) bad |= (unsigned)table[i] >= (unsigned)a.w.s.pages;
-    return __any(bad) ? BOLE_TREE_BAD_CACHE : BOLE_TREE_OK;
+    if (len < 0 || len > ((int64_t)a.max_prefix_pages << a.w.s.page_shift)) return BOLE_TREE_BAD_CACHE;
+    return prefix_pages_status(a, g, 0, len);
 }
 
 // The matrix-core kernels (prefix_mfma.hip).

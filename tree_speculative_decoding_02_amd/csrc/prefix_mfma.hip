@@ -33,7 +33,7 @@ struct OwnKeys {
         return find_tile<MT>(p.w, G, slot, report, t, mask, depth);
     }
     __device__ __forceinline__ const int32_t *table(int b) const { return p.w.page_table + (size_t)b * p.w.s.max_pages; }
-    __device__ __forceinline__ int pages_status(int b, int len) const { return bole::pages_status(p.w, b, len); }
+    __device__ __forceinline__ int pages_status(const RowTile &t, int, int) const { return bole::pages_status(p.w, t.b, t.len); }
 };
 
 struct GroupRanges {
@@ -68,7 +68,10 @@ struct SharedKeys {
         return true;
     }
     __device__ __forceinline__ const int32_t *table(int g) const { return p.prefix_table + (size_t)g * p.max_prefix_pages; }
-    __device__ __forceinline__ int pages_status(int g, int len) const { return prefix_status(p, g, len); }
+    // (each part its own keys' pages: the join asks all of them)
+    __device__ __forceinline__ int pages_status(const RowTile &t, int x0, int x1) const {
+        return prefix_pages_status(p, t.b, x0, min(x1, t.len));
+    }
 };
 
 // How a call runs: form, row tiles (slots) and parts of either kind of key list.
@@ -148,10 +151,10 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, co
     int n = n_own;
     if (p.groups > 0 && row >= a.offsets[p.group_offsets[0]] && row < a.offsets[p.group_offsets[p.groups]]) n = n_all;
     const float m = lane < n ? x.x : -INFINITY, l = lane < n ? x.y : 0.f;
-    const float own = readlane_f(l, 0), shared = readlane_f(l, n - 1);  // (all parts of a bad list say the same)
+    const float own = readlane_f(l, 0);  // (all parts of a bad sequence say the same, of a bad prefix some)
     if (own == kLeftRow) return;
     T *out = static_cast<T *>(a.out) + at * D;
-    if (own == kNanRow || shared == kNanRow) {
+    if (__any(l == kNanRow)) {
         if (own != kNanRow && h == 0 && lane == 0 && a.status) a.status[sequence_of(a.offsets, s.B, row)] = BOLE_TREE_BAD_CACHE;
         for (int e = lane; e < D; e += 64) out[e] = (T)__builtin_nanf("");
         return;

@@ -2,7 +2,8 @@
 // for windowed attention and for attention behind shared prefixes. Which rows a workgroup has and
 // which keys they see is `Keys`:
 //   args(), find<MT>(..) (the row tile of a slot and its key list), table(b) (its pages),
-//   pages_status(b, len);  kOwnRows: the rows' own sequences and what they see beyond the shared
+//   pages_status(t, x0, x1) (whether the pages of its keys exist, at least of entries x0 .. x1 - 1 of
+//   the list);  kOwnRows: the rows' own sequences and what they see beyond the shared
 //   prefix;  kSplit: results always go to the parts, [part][row][head], for another kernel to join.
 #pragma once
 
@@ -144,7 +145,7 @@ __device__ __forceinline__ void rows_body(const Keys &keys, const WindowParts &p
         fetch(first);
         find_rows(min(first + 1, last - 1));
     }
-    t.status = keys.pages_status(t.b, t.len);
+    t.status = keys.pages_status(t, part_edge(tiles, part, parts.n) * kKeys, part_edge(tiles, part + 1, parts.n) * kKeys);
     if (report) a.status[t.b] = t.status;
     if (t.status != BOLE_TREE_OK) {
         give_up();
@@ -350,7 +351,7 @@ __device__ __forceinline__ void tokens_body(const Keys &keys, const WindowParts 
         fetch(first);
         page = key_page(s, table, t, (first + 4) * kKeys);
     }
-    t.status = keys.pages_status(t.b, t.len);
+    t.status = keys.pages_status(t, part_edge(tiles, part, parts.n) * kKeys, part_edge(tiles, part + 1, parts.n) * kKeys);
     if (report) a.status[t.b] = t.status;
     if (t.status != BOLE_TREE_OK) {
         give_up();

@@ -94,7 +94,7 @@ __device__ __forceinline__ void f32_body(const Keys &keys, const WindowParts &pa
         fetch(first);
         page = key_page(s, table, t, (first + 1) * kKeys);
     }
-    t.status = keys.pages_status(t.b, t.len);
+    t.status = keys.pages_status(t, first * kKeys, last * kKeys);
     if (report) a.status[t.b] = t.status;
     if (t.status != BOLE_TREE_OK) {
         give_up();

@@ -253,7 +253,7 @@ struct WindowKeys {
         return find_tile<MT>(a, G, slot, report, t, mask, depth);
     }
     __device__ __forceinline__ const int32_t *table(int b) const { return a.page_table + (size_t)b * a.s.max_pages; }
-    __device__ __forceinline__ int pages_status(int b, int len) const { return bole::pages_status(a, b, len); }
+    __device__ __forceinline__ int pages_status(const RowTile &t, int, int) const { return bole::pages_status(a, t.b, t.len); }
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
