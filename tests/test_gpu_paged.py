@@ -251,6 +251,21 @@ def test_long_prefixes(lib, shape, kind):
         check_attention(out, oracle_of(w, kind == "trees", rows=rows), w, 6200)
 
 
+@pytest.mark.parametrize("kind", ["tokens", "trees"])
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[4], (8, 8, 64, 64, BF16)], ids=[IDS[0], IDS[4], "8-8-64-64-bf16"])
+def test_prefixes_of_unequal_length(lib, shape, kind):
+    """One long prefix beside short and empty ones, more of them than a load's lanes."""
+    lens = [6000, 0, 64, 700] + [(13 * i) % 90 for i in range(70)]
+    ends = [0, 3, 4, 9, 10] + list(range(11, 81))
+    sizes = [1 if kind == "tokens" else 1 + (11 * i) % 40 if i < 10 else i % 3 for i in range(82)]
+    for groups in ((lens[:4], ends[:5]), (lens, ends)):
+        w = make(48, sizes, [(29 * i) % 100 for i in range(82)], groups, shape)
+        out = lib.bole_prefix_attention(**on_gpu(w), parent=g(w.parent) if kind == "trees" else None)
+        T = int(w.offsets[-1])
+        rows = set(range(0, T, max(1, T // 24))) | {T - 1}
+        check_attention(out, oracle_of(w, kind == "trees", rows=rows), w, 6200)
+
+
 def test_prefix_equals_one_cache(lib):
     """The same keys as windowed attention's own cache: equal within both calls' limits, and equal
     bits whether a sequence's neighbours share its prefix or not is not asked for."""

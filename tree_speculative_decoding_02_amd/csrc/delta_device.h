@@ -144,6 +144,24 @@ __device__ __forceinline__ double wave_sum_up_f64(double x) {
     return x;
 }
 
+// Inclusive sum over lanes 0 .. lane, in fp64, by moves within the vector registers.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double x) {
+    const long long v = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+    return __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
+}
+__device__ __forceinline__ double scan_f64(double x) {
+    x += dpp_f64<0x111, 0xf>(x);  // from 1, 2, 4 and 8 lanes before, within rows of 16
+    x += dpp_f64<0x112, 0xf>(x);
+    x += dpp_f64<0x114, 0xf>(x);
+    x += dpp_f64<0x118, 0xf>(x);
+    x += dpp_f64<0x142, 0xa>(x);  // a row's last lane to the next row,
+    x += dpp_f64<0x143, 0xc>(x);  // lane 31 to the upper half
+    return x;
+}
+
 // Inclusive sum over lanes 0 .. lane.
 __device__ __forceinline__ int wave_sum_up(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // from 1, 2, 4 and 8 lanes before,

@@ -11,11 +11,11 @@
 // Measured, 32 query heads over 8 key heads of 128, bf16: 64 single tokens behind one prefix of 16384,
 // with up to 512 cached of their own, 50 us (45 and 7 for the join; 2.6 TB/s of the bytes that each
 // have to be read once, 350 TFLOP/s); 50 trees of up to 16 nodes, four prefixes of up to 8192 among
-// them, 78 us (69 and 12; 306 TFLOP/s); 4 tokens behind 1000 11.7 us, two launches and the chains
-// within. The larger two are bound by the prefix's workgroups, two a CU at most and of one form: each
-// has 64 keys at a time through registers to LDS, then products and exponentials behind a barrier.
-// Tried: the own tokens' workgroups first (59 against 45), touching the rows three tiles ahead (52),
-// parts of equal length in place of equal number for prefixes of unequal length (87 against 78).
+// them, 74 to 80 us (68 and 12), 62 without tokens of their own; 4 tokens behind 1000 12 us, two launches
+// and the chains within. The larger two are bound by the prefix's workgroups, two a CU at most and of
+// one form: each has 64 keys at a time through registers to LDS, then products and exponentials behind
+// a barrier. Tried: the own tokens' workgroups first (59 against 45), touching the rows three tiles
+// ahead (52).
 #include "prefix_device.h"
 #include "window_rows.h"
 #include "window_rows_f32.h"
@@ -38,7 +38,6 @@ struct OwnKeys {
 
 struct GroupRanges {
     const PrefixArgs &p;
-    __device__ __forceinline__ int count() const { return p.groups; }
     __device__ __forceinline__ void load(int x, int &lo, int &hi, int &len, bool &bad) const {
         const int b0 = p.group_offsets[x], b1 = p.group_offsets[x + 1], B = p.w.s.B;
         bad |= b0 < 0 || b1 < b0 || b1 > B;
@@ -46,15 +45,97 @@ struct GroupRanges {
     }
 };
 
+// Which part of which of the prefixes' row tiles item x of a key head is. One prefix is in `most` parts.
+// Several are cut, once their lengths are known, into parts of a like number of key tiles, so that there
+// are `items` at most, and `most` of a prefix (64 tokens over five prefixes of up to 16384: 64 us, with
+// as many parts of each, whatever its length, 86).
+struct Deal {
+    Slot tile;
+    int slot, part, parts;
+};
+
+template <int MT>
+__device__ __forceinline__ Deal deal(const PrefixArgs &p, int G, int x, int items, int most) {
+    const GroupRanges ranges{p};
+    const int lane = lane_id(), T = p.w.s.T;
+    Deal r = {{false, true, 0, 0, 0, 0, 0}, 0, 0, 1};
+    if (p.groups == 1) {  // as many parts as the call's sizes say
+        bool bad = false;
+        int lo, hi, len;
+        ranges.load(0, lo, hi, len, bad);
+        bad |= lo < 0 || hi < lo || hi > T;
+        const int tiles = max(1, uniform((int)(((uint32_t)(hi - lo) * G + MT - 1) / MT)));
+        r.part = uniform(x / tiles), r.slot = x - r.part * tiles, r.parts = most;
+        r.tile = {!bad && r.part < most, !bad, 0, lo, hi - lo, 0, len};
+        return r;
+    }
+    const int longest = (int)min(((int64_t)p.max_prefix_pages << p.w.s.page_shift), (int64_t)0x7fffffff);
+    bool bad = false;
+    int lo, hi, len, tiles, keys;  // of a group a lane: its rows and tokens, and both in tiles
+    auto load = [&](int c) {
+        ranges.load(min(c + lane, p.groups - 1), lo, hi, len, bad);
+        bad |= lo < 0 || hi < lo || hi > T;
+        const bool there = c + lane < p.groups;
+        tiles = there ? max(1, (int)(((uint32_t)(hi - lo) * G + MT - 1) / MT)) : 0;
+        keys = there && len >= 0 && len <= longest ? (len + kKeys - 1) / kKeys : 0;
+    };
+    load(0);
+    auto total = [&](auto &&f) {  // over all groups
+        int sum = 0;
+        for (int c = 0; c < p.groups; c += 64) {
+            if (p.groups > 64) load(c);
+            sum += __builtin_amdgcn_readlane(wave_sum_up(f()), 63);
+        }
+        return sum;
+    };
+    double products = 0.0;
+    for (int c = 0; c < p.groups; c += 64) {
+        if (p.groups > 64) load(c);
+        products += (double)tiles * keys;
+    }
+    const float work = readlane_f((float)scan_f64(products), 63);
+    // Key tiles a part. Parts as if row tiles had no ends are tried first; with the other step they fit for
+    // certain (fp32's rounding allowed for), as each row tile may end in a part of less.
+    int step = 4;
+    auto count = [&]() { return tiles > 0 ? min(most, max(1, (keys + step - 1) / step)) : 0; };
+    step = max(step, (int)ceilf(work / (float)items));
+    if (total([&]() { return tiles * count(); }) > items) {
+        const float spare = (float)max(1, items - total([&]() { return tiles; }));
+        step = max(step, (int)ceilf(work / spare * (1.f + 0x1p-16f)));
+    }
+    int before = 0, slots = 0;
+    for (int c = 0; c < p.groups; c += 64) {
+        if (p.groups > 64) load(c);
+        const int n = count(), own = tiles * n, end = before + wave_sum_up(own), slot = slots + wave_sum_up(tiles);
+        const int at = (int)__popcll(__ballot(c + lane < p.groups && end <= x));
+        if (!r.tile.found && at < min(64, p.groups - c)) {
+            r.tile.found = true;
+            r.tile.b = c + at;
+            r.tile.lo = __builtin_amdgcn_readlane(lo, at);
+            r.tile.n = __builtin_amdgcn_readlane(hi, at) - r.tile.lo;
+            r.tile.slot0 = __builtin_amdgcn_readlane(slot - tiles, at);
+            r.tile.per = __builtin_amdgcn_readlane(len, at);
+            r.parts = __builtin_amdgcn_readlane(n, at);
+            const int i = x - __builtin_amdgcn_readlane(end - own, at), nt = __builtin_amdgcn_readlane(tiles, at);
+            r.part = uniform(i / nt);
+            r.slot = r.tile.slot0 + i - r.part * nt;
+        }
+        before = __builtin_amdgcn_readlane(end, 63);
+        slots = __builtin_amdgcn_readlane(slot, 63);
+    }
+    r.tile.ordered = !__any(bad);
+    r.tile.found = r.tile.found && r.tile.ordered;
+    return r;
+}
+
 // A group's prefix: rows of all its sequences, cached keys alone. `b` of the tile is the group.
 struct SharedKeys {
     const PrefixArgs &p;
+    const Slot &l;
     static constexpr bool kOwnRows = false, kSplit = true;
     __device__ __forceinline__ const WindowArgs &args() const { return p.w; }
     template <int MT>
     __device__ __forceinline__ bool find(int G, int slot, bool, RowTile &t, uint64_t &, int &) const {
-        const Slot l = find_slot<MT>(GroupRanges{p}, p.w.s.T, G, slot);
-        if (!l.found) return false;
         t.b = l.b, t.lo = l.lo, t.n = l.n, t.slot0 = l.slot0, t.len = l.per;
         t.tile = slot - t.slot0;
         if (t.tile * MT >= t.n * G) return false;
@@ -77,13 +158,34 @@ struct SharedKeys {
 // How a call runs: form, row tiles (slots) and parts of either kind of key list.
 struct PrefixPlan {
     bool f32, own_tokens, shared_tokens;
-    int own_slots, own_parts, shared_slots, shared_parts;
+    int own_slots, own_parts, shared_slots, shared_items, shared_parts;
 };
 
 struct PrefixParts {
     WindowParts own, shared;
-    int own_slots, shared_slots, shared_blocks;
+    int own_slots, shared_slots, shared_items, shared_blocks;
 };
+
+// An item of the prefixes: its part, and, with the last one, marks where parts of others would be.
+template <int MT, class Body>
+__device__ __forceinline__ void shared_item(const PrefixArgs &p, const PrefixParts &parts, int block, Body &&body) {
+    const WindowShape &s = p.w.s;
+    const int x = uniform(block / s.HK), hk = block - x * s.HK, G = s.H / s.HK;
+    const Deal d = deal<MT>(p, G, x, parts.shared_items, parts.shared.n);
+    if (!d.tile.found) return;
+    WindowParts mine = parts.shared;
+    mine.n = d.parts;
+    if (d.part == d.parts - 1) {
+        const int r0 = (d.slot - d.tile.slot0) * MT, rows = min(MT, d.tile.n * G - r0);
+        for (int i = threadIdx.x; i < rows * (parts.shared.n - d.parts); i += 256) {
+            const int part = i / rows, R = r0 + i - part * rows, row = R / G;
+            const size_t at = (size_t)(d.parts + part) * s.T * s.H + (size_t)(d.tile.lo + row) * s.H + hk * G + (R - row * G);
+            mine.ml[at * 2] = -INFINITY;
+            mine.ml[at * 2 + 1] = 0.f;
+        }
+    }
+    body(SharedKeys{p, d.tile}, mine, d.slot * s.HK + hk, d.part);
+}
 
 // The workgroups of the prefixes come first: theirs is the most work.
 template <int D, bool OWN_TOKENS, bool SHARED_TOKENS>
@@ -94,9 +196,11 @@ __global__ __launch_bounds__(256, 2) void prefix_kernel(const PrefixArgs p, cons
     const int HK = p.w.s.HK;
     const int bx = blockIdx.x;
     if (bx < parts.shared_blocks) {
-        const int per = parts.shared_slots * HK, part = uniform(bx / per), block = bx - part * per;
-        if constexpr (SHARED_TOKENS) tokens_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
-        else rows_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, block, part, s_mem);
+        shared_item<SHARED_TOKENS ? kTokenTile : kRowTile>(
+            p, parts, bx, [&](const SharedKeys &keys, const WindowParts &mine, int block, int part) {
+                if constexpr (SHARED_TOKENS) tokens_body<D>(keys, mine, parts.shared_slots, block, part, s_mem);
+                else rows_body<D>(keys, mine, parts.shared_slots, block, part, s_mem);
+            });
     } else {
         const int x = bx - parts.shared_blocks, per = parts.own_slots * HK;
         const int part = uniform(x / per), block = x - part * per;
@@ -110,8 +214,9 @@ __global__ __launch_bounds__(256, 2) void prefix_f32_kernel(const PrefixArgs p, 
     __shared__ __align__(16) char s_mem[kF32Lds<D>];
     const int HK = p.w.s.HK;
     if ((int)blockIdx.x < parts.shared_blocks) {
-        const int per = parts.shared_slots * HK, part = uniform(blockIdx.x / per);
-        f32_body<D>(SharedKeys{p}, parts.shared, parts.shared_slots, blockIdx.x - part * per, part, s_mem);
+        shared_item<kF32Tile>(p, parts, blockIdx.x, [&](const SharedKeys &keys, const WindowParts &mine, int block, int part) {
+            f32_body<D>(keys, mine, parts.shared_slots, block, part, s_mem);
+        });
     } else {
         const int x = blockIdx.x - parts.shared_blocks, per = parts.own_slots * HK, part = uniform(x / per);
         f32_body<D>(OwnKeys{p}, parts.own, parts.own_slots, x - part * per, part, s_mem);
@@ -119,9 +224,10 @@ __global__ __launch_bounds__(256, 2) void prefix_f32_kernel(const PrefixArgs p, 
 }
 
 // Joins the parts of a row and head (at most 64), a wavefront each, in a fixed order; a lane has
-// D / 64 dimensions (96: two of three lanes' worth). What the parts hold is loaded before it is known
-// whether the row is anybody's: it only has to be there. AHEAD of them at once, as many as there are.
-template <typename T, int D, int AHEAD>
+// D / 64 dimensions (96: two of three lanes' worth). KNOWN: what the first AHEAD parts hold is loaded
+// before it is known whether the row is anybody's and which of its parts there are: it only has to be
+// there. Otherwise AHEAD at once of those that there are.
+template <typename T, int D, int AHEAD, bool KNOWN>
 __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, const PrefixParts parts) {
     constexpr int E = D == 64 ? 1 : 2;
     typedef float wide __attribute__((ext_vector_type(E)));
@@ -135,8 +241,10 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, co
     wide v[AHEAD];
     if (line) {
         if (lane < n_all) x = *reinterpret_cast<const float2 *>(parts.own.ml + (lane * all + at) * 2);
+        if constexpr (KNOWN) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) v[i] = *reinterpret_cast<const wide *>(src + min(i, n_all - 1) * all * D);
+            for (int i = 0; i < AHEAD; ++i) v[i] = *reinterpret_cast<const wide *>(src + min(i, n_all - 1) * all * D);
+        }
     }
     const bool ordered = offsets_ordered(a.offsets, s.B, s.T) &&
                          (p.groups == 0 || offsets_ordered(p.group_offsets, p.groups, s.B));
@@ -167,10 +275,26 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const PrefixArgs p, co
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
     wide o = (wide)0.f;
+    uint64_t live = __ballot(lane < n && l != 0.f);  // (a part without keys has no sums)
+    if constexpr (KNOWN) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (i < n) o += readlane_f(f, i) * v[i];
-    for (int i = AHEAD; i < n; ++i) o += readlane_f(f, i) * *reinterpret_cast<const wide *>(src + i * all * D);
+        for (int i = 0; i < AHEAD; ++i)
+            if ((live >> i) & 1) o += readlane_f(f, i) * v[i];
+        live = AHEAD < 64 ? live >> AHEAD << AHEAD : 0;
+    }
+    while (live) {
+        float w[AHEAD];
+        int at_part = 0;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            w[i] = 0.f;
+            if (live) at_part = __builtin_ctzll(live), w[i] = readlane_f(f, at_part);
+            live &= live - 1;
+            v[i] = *reinterpret_cast<const wide *>(src + at_part * all * D);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) o += w[i] * v[i];
+    }
     if (has) {
 #pragma unroll
         for (int e = 0; e < E; ++e) out[lane * E + e] = (T)(o[e] / sum);
@@ -196,8 +320,10 @@ static int parts_for(int64_t workgroups, int64_t keys, int wanted, int most) {
 // own lists' beside them, as a part's sums are written and read again (64 tokens over 16384: 51 us,
 // with 384 or 512 workgroups 59 and 64; 128 tokens 65, 66 and 69). Where that is three parts or fewer
 // it would leave some CUs two workgroups and others one: 512 (trees over one prefix of 8192 tokens 105
-// and 108 us in four and five parts, 113 in three; over four prefixes of up to 8192 81 us in five parts,
-// 88 in four). Lengths are not known here: the longest count.
+// and 108 us in four and five parts, 113 in three), or 400 of several prefixes, whose parts are of like
+// length (50 trees over four prefixes of up to 8192: 81 us, with 256, 320 and 512 87, 82 and 84; 64 larger
+// ones 146, 208, 212 and 148). Of several prefixes one may have three times the average's parts. Lengths
+// are not known here: the longest count.
 static PrefixPlan plan(const bole_prefix_dims_t &d) {
     PrefixPlan p;
     const int64_t G = d.heads / d.kv_heads, rows = d.total_rows * G;
@@ -210,10 +336,14 @@ static PrefixPlan plan(const bole_prefix_dims_t &d) {
     p.own_parts = parts_for((int64_t)p.own_slots * d.kv_heads, (int64_t)d.max_pages * d.page_size + 1, 512, 16);
     p.shared_slots = (int)(d.groups == 1 ? (rows > 0 ? (rows + shared - 1) / shared : 1) : rows / shared + d.groups);
     if (d.groups > 0) {
-        const int64_t blocks = (int64_t)p.shared_slots * d.kv_heads;
-        p.shared_parts = parts_for(blocks, (int64_t)d.max_prefix_pages * d.page_size, blocks > 85 ? 512 : 256, 48);
+        const int64_t blocks = (int64_t)p.shared_slots * d.kv_heads, keys = (int64_t)d.max_prefix_pages * d.page_size;
+        const int wanted = blocks <= 85 ? 256 : d.groups == 1 ? 512 : 400;
+        const int64_t items = wanted / d.kv_heads;  // of a key head
+        p.shared_parts = parts_for(d.groups == 1 ? blocks : (blocks + 2) / 3, keys, wanted, 48);
+        p.shared_items = (int)(items > p.shared_slots + 1 ? items : p.shared_slots + 1);
+        if (d.groups == 1) p.shared_items = p.shared_slots * p.shared_parts;
     } else {
-        p.shared_slots = p.shared_parts = 0;
+        p.shared_slots = p.shared_items = p.shared_parts = 0;
     }
     return p;
 }
@@ -235,10 +365,13 @@ template <typename T, int D>
 static hipError_t launch_join(const PrefixArgs &a, const PrefixParts &parts, hipStream_t stream) {
     const int64_t lines = (int64_t)a.w.s.T * a.w.s.H;
     const dim3 grid((unsigned)(lines > 0 ? (lines + 3) / 4 : 1)), block(256);
+    // Few parts, and all of one prefix's, are there for most rows and loaded ahead; of several prefixes
+    // most rows have fewer than the longest's.
     const int n = parts.own.n + parts.shared.n;
-    if (n <= 3) prefix_join_kernel<T, D, 3><<<grid, block, 0, stream>>>(a, parts);
-    else if (n <= 8) prefix_join_kernel<T, D, 8><<<grid, block, 0, stream>>>(a, parts);
-    else prefix_join_kernel<T, D, 16><<<grid, block, 0, stream>>>(a, parts);
+    if (n <= 3) prefix_join_kernel<T, D, 3, true><<<grid, block, 0, stream>>>(a, parts);
+    else if (n <= 8) prefix_join_kernel<T, D, 8, true><<<grid, block, 0, stream>>>(a, parts);
+    else if (a.groups <= 1) prefix_join_kernel<T, D, 16, true><<<grid, block, 0, stream>>>(a, parts);
+    else prefix_join_kernel<T, D, 8, false><<<grid, block, 0, stream>>>(a, parts);
     return hipGetLastError();
 }
 
@@ -264,7 +397,8 @@ hipError_t launch_prefix_mfma(const PrefixArgs &a, const bole_prefix_dims_t &d, 
     parts.shared = {o + p.own_parts * lines * d.head_dim, ml + p.own_parts * lines * 2, p.shared_parts};
     parts.own_slots = p.own_slots;
     parts.shared_slots = p.shared_slots;
-    parts.shared_blocks = p.shared_slots * d.kv_heads * p.shared_parts;
+    parts.shared_items = p.shared_items;
+    parts.shared_blocks = p.shared_items * d.kv_heads;
     switch (d.head_dim) {
         case 64: return launch_width<64>(a, p, parts, stream);
         case 96: return launch_width<96>(a, p, parts, stream);
