@@ -512,6 +512,24 @@ def test_append_many_rows(lib, shape):
         assert (status == 0).all()
 
 
+@pytest.mark.parametrize("shape", [(16, 128, 16, BF16), (5, 33, 8, F32), (6, 129, 4, BF16), (1, 1, 4, BF16)], ids=str)
+def test_append_without_rows(lib, shape):
+    """No rows at all, of more than one load a thread and of few: only statuses and lengths, without
+    and with a row's memory behind k and v."""
+    HK, d, ps, dt = shape
+    for path in (False, True):
+        w = make_append(6, [0, 0, 0], [0, 5, 3], *shape, spare=0, path=path)
+        w["cached"][2] = -1
+        none = torch.empty(0, HK, d, dtype=dt, device=dev())
+        some = torch.full((1, HK, d), 7.0, dtype=dt, device=dev())[:0]
+        for x in (none, some):
+            status = i32([-1] * 3)
+            kc, vc, ln = call_append(lib, w, k=x, v=x, seq_status=status)
+            torch.cuda.synchronize()
+            assert status.tolist() == [0, 0, BAD_CACHE] and ln.tolist() == [0, 5, -1]
+            assert torch.equal(kc, g(w["kc"])) and torch.equal(vc, g(w["vc"]))
+
+
 def test_append_contiguous_and_unaligned(lib):
     w = make_append(2, [40, 3], [10, 0], 2, 128, 16, BF16, path=False)
 

@@ -101,6 +101,7 @@ __global__ __launch_bounds__(256) void append_rows_kernel(const AppendArgs a, in
         if (lane == 0)
             s_place[r] = o.found && r < rows && st == BOLE_TREE_OK ? place_of(a, size, o.b, len + row - o.lo) : kNowhere;
     }
+    if (rows <= 0) return;  // (a call without rows only reports)
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * n; e += 256) {
         const Piece<V> p(a, size, e, n);
