@@ -651,7 +651,9 @@ BOLE_API bole_status_t bole_window_attention(const void *q, const void *k, const
  * prompt's outputs see the state before their 64 tokens as two bf16 terms (2^-17 left), and the
  * weights D_{j->i} (q_i . k_j) of tokens of the same 64 rounded to bf16 (half a step of that term
  * of the output's sum). BOLE_FLAG_FORCE_GENERIC walks a prompt's tokens in fp32, as do prompts
- * with BOLE_GATE_VECTOR.
+ * with BOLE_GATE_VECTOR. Products of decays below 2^-126 may count as 0. Decays above 1 may grow past
+ * fp32 on the way as long as states and outputs do not; prompts in which the ones above 1 among 64
+ * tokens multiply to more than 2^64 are walked in part, and as slow as that.
  * Values must be finite: a NaN or an infinity in one token may reach every token of its sequence
  * (its head alone), earlier ones of the same 64 tokens among them. Gates are not checked. Buffers
  * that a call writes must not overlap any other buffer of that call. Rows that belong to no

@@ -15,6 +15,12 @@
 // LDS, the next chunk in registers meanwhile; P's row tiles are formed by a wavefront each and
 // exchanged.
 //
+// Products of decays above 1 may leave fp32 where what they scale is small or zero. A segment with a chunk
+// whose decays above 1 multiply to more than 2^64 is taken once more, token by token (H <- a H + k v^T,
+// o = H^T q, in the same accumulators), when its chunks are through; others have half of fp32's range for
+// what decays scale. (A way out of the chunks' loop, or a test within it, cost all prompts 3 to 12 %, as the
+// compiler then orders the loop's reads and products less well.)
+//
 // The state is kept to fp32: K is exact in bf16, and diag(2^{L_64 - L}) V is taken as three bf16
 // terms (2^-25 left). What only the output sees may be rounded harder: S in two terms, P in one (half
 // a step of bf16 of each pair weight, once, before an output that is rounded to bf16 itself). With
@@ -42,7 +48,7 @@ struct LinearPlan {
 // then its decay.
 struct LinearSpace {
     f32x4 *s;      // [slot][H][column tile][row tile][64]
-    float *decay;  // [slot][H]
+    float *decay;  // [slot][H]: its log2
 };
 
 // A workgroup's slot, head and column group. Of each slot's heads and groups every XCD (workgroups are
@@ -56,6 +62,22 @@ __device__ __forceinline__ void unit_of(const LinearPlan &p, int H, int &slot, i
     if (each % 8 == 0) unit = (unit % 8) * (each / 8) + unit / 8;
     h = unit / p.groups;
     cg = unit - h * p.groups;
+}
+
+// Product of the values above 1 of a wavefront.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float times_dpp(float x) {
+    return x * __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(1.f), __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float product_above(float x) {
+    x = x > 1.f ? x : 1.f;
+    x = times_dpp<0x111, 0xf>(x);  // as scan_f64
+    x = times_dpp<0x112, 0xf>(x);
+    x = times_dpp<0x114, 0xf>(x);
+    x = times_dpp<0x118, 0xf>(x);
+    x = times_dpp<0x142, 0xa>(x);
+    x = times_dpp<0x143, 0xc>(x);
+    return readlane_f(x, 63);
 }
 
 template <int DK>
@@ -81,6 +103,7 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
     __shared__ __align__(16) __bf16 s_v[NK][kChunk * VP];
     __shared__ __align__(16) __bf16 s_p[LOCAL ? 1 : NK][6][64][8];
     __shared__ __align__(16) float s_w[2][4][kChunk];  // L in two terms, 2^L, 2^{L_64 - L}
+    __shared__ int s_grows;                            // whether some chunk's decays are too large for that
     const DeltaShape &s = a.s;
     int slot, h, cg;
     unit_of(p, s.H, slot, h, cg);
@@ -202,28 +225,33 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
         to[1][lane] = (float)(L - (double)(float)L);
         to[2][lane] = __builtin_amdgcn_exp2f((float)L);
         to[3][lane] = chunk * kChunk + lane < n ? __builtin_amdgcn_exp2f((float)(all - L)) : 0.f;
+        if (__any(gate > 1.f) && product_above(gate) > 0x1p64f) s_grows = 1;
         total += all;
     };
 
-    fetch(0);
+    auto first_state = [&]() {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-            st[ct][j] = (f32x4)0.f;
-            if (LOCAL) continue;
-            if (l.n > p.seg) {
-                st[ct][j] = sw[(ct * TILES + j) * 64];
-            } else {
+            for (int j = 0; j < TILES; ++j) {
+                st[ct][j] = (f32x4)0.f;
+                if (LOCAL) continue;
+                if (l.n > p.seg) {
+                    st[ct][j] = sw[(ct * TILES + j) * 64];
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (state_has(ct, j, e)) st[ct][j][e] = Hu[(size_t)tile_token(j, 4 * g + e) * s.DV + 16 * ct];
+                    for (int e = 0; e < 4; ++e)
+                        if (state_has(ct, j, e)) st[ct][j][e] = Hu[(size_t)tile_token(j, 4 * g + e) * s.DV + 16 * ct];
+                }
             }
-        }
+    };
+    fetch(0);
+    first_state();
     float gate_next = 1.f;
     if (wave == 0) {
         const float gate = fetch_gate(0);
         gate_next = fetch_gate(1);
+        s_grows = 0;
         weigh(0, gate);
     }
     stage();
@@ -384,12 +412,52 @@ __global__ __launch_bounds__(256, sizeof(TF) == 4 ? 1 : CT == 2 ? 2 : LOCAL ? 4 
         }
     } while (++chunk < chunks);
 
+    if (__builtin_amdgcn_readfirstlane(s_grows)) {  // ---- once more, token by token
+        first_state();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the outputs written above come before these
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            const float decay = gb[(size_t)t * s.H];
+            const TF *k = kb + (size_t)t * sk, *q = qb + (size_t)t * sk;
+            float v[CT], z[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int c = c0 + 16 * ct + col;
+                v[ct] = WHOLE || c < left ? to_f32(vb[(size_t)t * sv + c]) : 0.f;
+                z[ct] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) {
+                asm volatile("" ::: "memory");  // (all rows' loads at once would take more registers than the loop above)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = tile_token(j, 4 * g + e);
+                    const bool in = WHOLE || row < dk;
+                    const float kr = in ? to_f32(k[row]) : 0.f, qr = !LOCAL && in ? to_f32(q[row]) : 0.f;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        st[ct][j][e] = fmaf(kr, v[ct], decay * st[ct][j][e]);
+                        z[ct] = fmaf(st[ct][j][e], qr, z[ct]);
+                    }
+                }
+            }
+            if constexpr (!LOCAL) {
+                TF *o = static_cast<TF *>(a.out) + (row0 + t) * sv + (size_t)h * s.DV + cg * VC + c0 + col;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const float y = sum32(sum16(z[ct]));
+                    if (g == 0 && (WHOLE || c0 + 16 * ct + col < left)) o[16 * ct] = (TF)y;
+                }
+            }
+        }
+    }
+
     if (LOCAL) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int j = 0; j < TILES; ++j) sw[(ct * TILES + j) * 64] = st[ct][j];
-        if (tid == 0 && cg == 0) w.decay[at_ws] = __builtin_amdgcn_exp2f((float)total);
+        if (tid == 0 && cg == 0) w.decay[at_ws] = (float)total;
     } else if (last_seg) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
@@ -437,7 +505,11 @@ __global__ __launch_bounds__(256) void linear_carry_kernel(const LinearArgs a, c
         for (int k = 0; k < 8; ++k) {
             if (i + k >= count) break;
             x[(i + k) * step] = S;
-            S = S * decay[k] + own[k];
+            // (past fp32's range as two roots, and no infinity, so that what is zero stays zero)
+            const bool far = fabsf(decay[k]) > 126.f;
+            const float by = __builtin_amdgcn_exp2f(far ? fminf(0.5f * decay[k], 127.9f) : decay[k]);
+            if (far) S *= by;
+            S = S * by + own[k];
         }
     }
 }
