@@ -10,10 +10,9 @@ at most the sum A of |log2 gate|, and n tokens have at most n / 64 + 1 chunks an
 """
 import numpy as np
 import pytest
-import torch
 
 from oracle import linear as O
-from test_gpu_linear import BF16, F32, dev, g, lib, make, on_gpu  # noqa: F401 (lib: the fixture)
+from test_gpu_linear import BF16, F32, g, lib, make, on_gpu  # noqa: F401 (lib: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +90,12 @@ def test_chunked(lib, shape, case):  # noqa: F811
     w = case(shape)
     t = on_gpu(w)
     check(lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets)), t["H0"], w, True)
+
+
+@pytest.mark.parametrize("channel", [False, True], ids=["head", "channel"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: c.__name__)
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_walked(lib, shape, case, channel):  # noqa: F811
+    w = case(shape, channel=channel)
+    t = on_gpu(w)
+    check(lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets), force_generic=True), t["H0"], w, False)

@@ -22,11 +22,21 @@ namespace bole {
 // segment from nothing, a second runs over a sequence's segments and leaves the state that each starts
 // from, a third walks them again, with outputs. (Two prompts of up to 600 tokens, 32 heads of 128 x 64
 // states, decays a channel: 88 us, 490 in one chain.)
+//
+// A segment's decays are multiplied in fp64, as their products may leave fp32 where what they scale is
+// small or zero, and kept below infinity, as zero has to stay that. A product in fp32's range goes on as
+// it is, one above or below as its root with a minus sign.
 struct WalkSpace {
     float *s;      // [slot][H][d_k][d_v]
     float *decay;  // [slot][H], or [slot][H][d_k]
     int seg;       // tokens a segment; 0: whole sequences
 };
+
+__device__ __forceinline__ float kept_decay(double x) {
+    if (x == 0.0 || (x >= 0x1p-126 && x <= 0x1p126)) return (float)x;
+    const double root = sqrt(x);
+    return root > 0x1p127 ? -0x1p127f : -(float)root;
+}
 
 enum { kWalkStep = 0, kWalkLocal = 1, kWalkMain = 2 };
 
@@ -90,18 +100,22 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
     const TF *q = static_cast<const TF *>(a.q), *k = static_cast<const TF *>(a.k),
              *v = static_cast<const TF *>(a.v);
     const size_t sk = (size_t)a.s.HK * DK, sv = (size_t)H * DV;
+    // Decays that the lane multiplies up: the head's, or its share of the row group's.
+    constexpr int SHARE = CHANNEL ? RPL / 8 : 1;
+    const int s0 = CHANNEL ? r0 + (lane & 7) * SHARE : 0;
     struct Token {
         RowPiece<TF, RPL, ROW> k, q;
         RowPiece<float, CHANNEL ? RPL : 1, CHANNEL ? ROW : kAnyRow> g;
         float v[CPL];
+        float share[SHARE];
     };
     // this token and the next one: with three or four the registers leave fewer wavefronts (7000 tokens of
     // 32 heads with decays a channel 0.84 ms, 1.24 and 1.33)
     constexpr int AHEAD = MODE == kWalkStep ? 1 : 2;
     Token x[AHEAD];
-    float all[CHANNEL ? RPL : 1];
+    double all[SHARE];
 #pragma unroll
-    for (int i = 0; i < (CHANNEL ? RPL : 1); ++i) all[i] = 1.f;
+    for (int i = 0; i < SHARE; ++i) all[i] = 1.0;
     auto fetch = [&](int t, Token &y) {
         const size_t row = (size_t)lo + min(t, n - 1);
         y.k.load(k + row * sk + (size_t)hk * DK, r0, DK);
@@ -111,6 +125,11 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
             y.v[c] = live ? to_f32(v[row * sv + (size_t)h * DV + c0 + c]) : 0.f;
         if constexpr (CHANNEL) y.g.load(a.gate + (row * H + h) * DK, r0, DK);
         else y.g.x[0] = a.gate[row * H + h];
+        if constexpr (!OUT) {
+#pragma unroll
+            for (int i = 0; i < SHARE; ++i)
+                y.share[i] = !CHANNEL ? y.g.x[0] : ROW == kExact || s0 + i < DK ? a.gate[(row * H + h) * DK + s0 + i] : 1.f;
+        }
     };
     auto token = [&](int t, const Token &y) {
         float z[CPL];
@@ -118,7 +137,7 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
         for (int c = 0; c < CPL; ++c) z[c] = 0.f;
         if constexpr (!OUT) {
 #pragma unroll
-            for (int i = 0; i < (CHANNEL ? RPL : 1); ++i) all[i] *= y.g.x[i];
+            for (int i = 0; i < SHARE; ++i) all[i] *= (double)y.share[i];
         }
 #pragma unroll
         for (int i = 0; i < RPL; ++i) {
@@ -146,6 +165,11 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
     } else {
         int t = 0;
         for (; t + AHEAD <= n; t += AHEAD) {
+            if constexpr (!OUT) {  // (two decays more stay below infinity)
+                static_assert(AHEAD == 2, "range");
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i) all[i] = all[i] > 0x1p700 ? 0x1p700 : all[i];
+            }
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 token(t + u, x[u]);
@@ -163,13 +187,13 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
                 __builtin_nontemporal_store(hr[i], reinterpret_cast<hvec *>(to + c0 + (size_t)(r0 + i) * DV));
     }
     if constexpr (!OUT) {
-        if (cb == 0 && (lane & 7) == 0) {
+        if (cb == 0) {
             if constexpr (CHANNEL) {
 #pragma unroll
-                for (int i = 0; i < RPL; ++i)
-                    if (r0 + i < DK) w.decay[space * DK + r0 + i] = all[i];
-            } else if (rg == 0) {
-                w.decay[space] = all[0];
+                for (int i = 0; i < SHARE; ++i)
+                    if (s0 + i < DK) w.decay[space * DK + s0 + i] = kept_decay(all[i]);
+            } else if (lane == 0) {
+                w.decay[space] = kept_decay(all[0]);
             }
         }
     }
@@ -201,7 +225,8 @@ __global__ __launch_bounds__(256) void linear_walk_carry_kernel(const LinearArgs
         for (int k = 0; k < 8; ++k) {
             if (i + k >= count) break;
             x[(i + k) * step] = S;
-            S = fmaf(S, decay[k], own[k]);
+            const float by = fabsf(decay[k]);
+            S = fmaf(decay[k] < 0.f ? S * by : S, by, own[k]);
         }
     }
 }
