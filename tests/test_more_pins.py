@@ -175,3 +175,16 @@ def test_append_dims():
     a[6] = None
     d.batch = 0
     assert call(a, d) == bole.BOLE_OK
+
+
+def test_prefix_rows_that_fill_a_launch():
+    """The join has a wavefront a row and head, four to 256 threads, and fewer than 2^32 threads in all:
+    at most 2^26 - 4 rows and heads, as four workgroups' worth more would round up past it."""
+    check = bole.lib.bole_prefix_check_dims
+    dims = lambda rows, heads: bole.bole_prefix_dims_t(1, heads, heads, 64, rows, 10, 16, 5, 0, 0, 0, 0, 0.1)
+    for rows, heads, want in ((2**26 - 4, 1, bole.BOLE_OK), (2**26 - 3, 1, 2), (2**26 - 1, 1, 2), (2**25 - 2, 2, bole.BOLE_OK),
+                              (2**25 - 1, 2, 2), ((2**26 - 1) // 3, 3, 2), ((2**26 - 4) // 3, 3, bole.BOLE_OK)):
+        d = dims(rows, heads)
+        assert check(ctypes.byref(d)) == want, (rows, heads)
+        if want == bole.BOLE_OK:
+            assert (rows * heads + 3) // 4 * 256 < 2**32

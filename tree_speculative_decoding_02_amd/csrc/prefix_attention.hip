@@ -129,12 +129,12 @@ bole_status_t bole_prefix_check_dims(const bole_prefix_dims_t *d) {
     if (d->flags & ~BOLE_FLAG_FORCE_GENERIC) return BOLE_ERR_INVALID_VALUE;
     if (d->head_dim > 256 || d->page_size > 1024 || d->heads > 65535) return BOLE_ERR_UNSUPPORTED;
     // Positions, those of the next few key tiles behind the last among them, and (sequences +
-    // groups) x heads fit 31 bits, and a launch has fewer than 2^32 threads: 64 a row and head, or 256
-    // for each 16 rows a key head packs and up to three times a sequence or group (of few rows).
+    // groups) x heads fit 31 bits, and a launch has fewer than 2^32 threads: 64 a row and head (in
+    // fours), or 256 for each 16 rows a key head packs and up to three times a sequence or group (of few rows).
     const int64_t rows = d->total_rows, lists = (int64_t)d->batch + d->groups;
     if ((int64_t)d->max_pages * d->page_size + rows > (1LL << 31) - 1024 ||
         (int64_t)d->max_prefix_pages * d->page_size + rows > (1LL << 31) - 1024 ||
-        lists * d->heads > 0x7fffffffLL || rows * d->heads >= 1LL << 26 ||
+        lists * d->heads > 0x7fffffffLL || rows * d->heads + 3 >= 1LL << 26 ||
         rows * d->heads / 16 + 3 * lists * d->kv_heads >= 1LL << 24)
         return BOLE_ERR_UNSUPPORTED;
     return BOLE_OK;
