@@ -98,10 +98,13 @@ __device__ __forceinline__ Deal deal(const PrefixArgs &p, int G, int x, int item
     // certain (fp32's rounding allowed for), as each row tile may end in a part of less.
     int step = 4;
     auto count = [&]() { return tiles > 0 ? min(most, max(1, (keys + step - 1) / step)) : 0; };
-    step = max(step, (int)ceilf(work / (float)items));
+    // (a step of 2^30 is longer than any list: more, from hundreds of thousands of row tiles over long
+    // prefixes or from bad offsets, would not be an int)
+    auto whole = [](float x) { return (int)fminf(ceilf(x), 0x1p30f); };
+    step = max(step, whole(work / (float)items));
     if (total([&]() { return tiles * count(); }) > items) {
         const float spare = (float)max(1, items - total([&]() { return tiles; }));
-        step = max(step, (int)ceilf(work / spare * (1.f + 0x1p-16f)));
+        step = max(step, whole(work / spare * (1.f + 0x1p-16f)));
     }
     int before = 0, slots = 0;
     for (int c = 0; c < p.groups; c += 64) {
