@@ -11,7 +11,7 @@ struct PrefixArgs {
     int groups, max_prefix_pages;
 };
 
-// Sequences [b0, b1) of group g share the prefix of len tokens; found: the sequence has one.
+// The prefix of a sequence: group g's, of len tokens; found: it has one.
 struct Group {
     bool found;
     int g, len;

@@ -67,18 +67,9 @@ struct Slot {
     int b, lo, n, slot0, per;       // sequence, its rows, its first slot
 };
 
-// Ranges: B of them; load(x, ..) gives the x-th's rows [lo, hi) and tokens, and whether it is bad.
-struct SequenceRanges {
-    const WindowArgs &a;
-    __device__ __forceinline__ int count() const { return a.s.B; }
-    __device__ __forceinline__ void load(int x, int &lo, int &hi, int &len, bool &) const {
-        lo = a.offsets[x], hi = a.offsets[x + 1], len = a.cache_len[x];
-    }
-};
-
-template <int MT, class Ranges>
-__device__ __forceinline__ Slot find_slot(const Ranges &ranges, int T, int G, int slot) {
-    const int B = ranges.count();
+template <int MT>
+__device__ __forceinline__ Slot find_slot(const WindowArgs &a, int G, int slot) {
+    const int B = a.s.B;
     bool bad = false;
     Slot l = {false, true, 0, 0, 0, 0, 0};
     int before = 0;
@@ -87,13 +78,13 @@ __device__ __forceinline__ Slot find_slot(const Ranges &ranges, int T, int G, in
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int x = min(c0 + 64 * j + lane_id(), B - 1);
-            ranges.load(x, lo[j], hi[j], len[j], bad);
+            lo[j] = a.offsets[x], hi[j] = a.offsets[x + 1], len[j] = a.cache_len[x];
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int c = c0 + 64 * j;
             if (c >= B) break;
-            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > T;
+            bad |= lo[j] < 0 || hi[j] < lo[j] || hi[j] > a.s.T;
             const int own = c + lane_id() < B ? max(1, (int)(((uint32_t)(hi[j] - lo[j]) * G + MT - 1) / MT)) : 0;
             const int end = before + wave_sum_up(own);
             const int at = uniform((int)__popcll(__ballot(c + lane_id() < B && end <= slot)));
@@ -122,7 +113,7 @@ __device__ __forceinline__ bool find_tile(const WindowArgs &a, int G, int slot, 
     const WindowShape &s = a.s;
     const int lane = lane_id();
     t.status = BOLE_TREE_OK;
-    const Slot l = find_slot<MT>(SequenceRanges{a}, s.T, G, slot);
+    const Slot l = find_slot<MT>(a, G, slot);
     if (!l.found) {
         if (!l.ordered && report && slot == 0 && a.status)
             for (int b = lane; b < s.B; b += 64) a.status[b] = BOLE_TREE_BAD_SIZE;
@@ -269,7 +260,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     const size_t stride = (size_t)slots * s.HK * MT, at = (size_t)blockIdx.x * MT + r;
     // every part's maximum and sum, a part a lane (the rows of unused tiles are never read)
-    const Slot t = find_slot<MT>(SequenceRanges{a}, s.T, G, slot);
+    const Slot t = find_slot<MT>(a, G, slot);
     const int R = (slot - t.slot0) * MT + r;
     if (!t.found || R >= t.n * G) return;
     float m = -INFINITY, l = 0.f;
