@@ -492,6 +492,9 @@ BOLE_API bole_status_t bole_tree_accept(const float *p_ctx, const float *p_node,
  * updates and the pair weights D_{j->i} (q_i . k_j) as two bf16 terms (2^-17 left); by prompts
  * the first two so, and each pair weight, of tokens of the same 64, rounded to bf16 (half a step
  * of that term of the output's sum). BOLE_FLAG_FORCE_GENERIC walks a prompt's tokens in fp32.
+ * Of gates above 1, the product of any run within 64 tokens of a prompt, or along a tree's path,
+ * has to stay below 2^127 (walked prompts and steps: what it makes of the state alone); products
+ * below 2^-126 may count as 0.
  * Values must be finite: a NaN or an infinity in one token reaches every token of its
  * sequence (its head alone), earlier ones of the same 64 tokens among them. Gates are not
  * checked. Buffers that a call writes must not overlap any other buffer of that call.
@@ -712,7 +715,10 @@ BOLE_API bole_status_t bole_linear_step(float *H0, const void *q, const void *k,
  *   first_position int32 [B], >= 0;   node_offsets int32 [B + 1]
  *   q_out, k_out  [T][heads][d] and [T][kv_heads][d], dtype; may be q and k themselves where
  *                 those are contiguous, and must not overlap any other buffer of the call
- * Sums, norms and rotations are fp32; outputs are rounded once. A NaN stays in its own head.
+ * Sums, norms and rotations are fp32; outputs are rounded once. The squares of a head, and their
+ * sum, have to stay in fp32's range where they matter beside eps: values up to 1e18 in size, and,
+ * with an eps of 0, some value above 1e-18 or a head of zeros (which becomes NaN, as 0 / 0 is). A NaN
+ * stays in its own head.
  * Statuses and errors follow bole_window_attention: BOLE_TREE_BAD_SIZE leaves the rows untouched,
  * rows of a bad-parent tree, and of a sequence whose first_position is negative or so large that
  * first_position + rows - 1 passes 2^31 - 1 (BOLE_TREE_BAD_CACHE), become NaN.
