@@ -2,7 +2,8 @@
 test_gpu_linear.py and test_gpu_paged.py, whose limits' derivations hold here: prompts that are walked
 though their sizes fit the chunked form (the limits without that form's roundings), walked prompts in
 segments of hundreds of tokens, a prefix against windowed attention over the same keys in one table,
-calls without rows.
+calls without rows, more query heads than a tile's rows, many trees, caches filled to the end, and calls
+captured once and replayed on other lengths.
 """
 from types import SimpleNamespace
 
@@ -111,3 +112,104 @@ def test_prefix_is_windowed_attention_over_one_table(lib, shape, kind):  # noqa:
     alg = (half if w.q.dtype == BF16 else 0.0) + 2 * (w.q.shape[2] + 2) * 2.0 ** -24 * reach + keys * 2.0 ** -24 + 2.0 ** -20
     lim = 2 * (half * np.abs(out) + alg[:, :, None] * mag)
     assert (np.abs(got.double().cpu().numpy() - whole.double().cpu().numpy()) <= lim).all()
+
+
+@pytest.mark.parametrize("kind", ["tokens", "trees"])
+@pytest.mark.parametrize("shape", [(32, 1, 128, 16, BF16), (40, 2, 64, 8, BF16), (24, 1, 96, 32, F32)], ids=str)
+def test_prefix_of_more_query_heads_than_a_tile_has_rows(lib, shape, kind):  # noqa: F811
+    sizes, cached = paged.CALLS[kind]
+    w = paged.make(75, sizes, cached, ([200, 77], [0, 4, 6]), shape)
+    tree = kind == "trees"
+    out = lib.bole_prefix_attention(**paged.on_gpu(w), parent=g(w.parent) if tree else None)
+    check_attention(out, paged.oracle_of(w, tree), w, 900)
+
+
+@pytest.mark.parametrize("shape", [paged.ROTARY[0], paged.ROTARY[3], paged.ROTARY[9]], ids=str)
+def test_rotation_of_many_trees(lib, shape):  # noqa: F811
+    """Trees in the launch for many rows, among them ones of one node, of none, and bad ones."""
+    sizes = [(17 * i) % 65 for i in range(150)]
+    first = [(97 * i) % 5000 for i in range(150)]
+    w = paged.make_rotary(76, sizes, first, shape, tree=True)
+    assert w["offs"][-1] >= 4096
+    at = {t: p for t, p in P.positions(w["first"], w["offs"], w["parent"]).items()}
+    bad = [7, 90]
+    for b in bad:
+        w["parent"][w["offs"][b] + 1] = 1  # its own
+    status = torch.full((150,), -1, dtype=torch.int32, device=dev())
+    got = paged.call_rotary(lib, w, seq_status=status)
+    assert status.tolist() == [paged.BAD_PARENT if b in bad else 0 for b in range(150)]
+    rows = {b: range(w["offs"][b], w["offs"][b + 1]) for b in bad}
+    for b in bad:
+        assert all(torch.isnan(y[list(rows[b])]).all() for y in got)
+    gone = {t for b in bad for t in rows[b]}
+    paged.check_rotary(got, w, at={t: at[t] for t in sorted(at)[::7] if t not in gone})
+
+
+def test_append_to_the_last_position_and_paths_of_none(lib):  # noqa: F811
+    for path in (False, True):
+        w = paged.make_append(77, [5, 3, 0, 6], [11, 0, 16, 10], 2, 64, 8, BF16, path=path)
+        if path:
+            w["idx"], w["len"] = w["idx"][:, :0].copy(), np.zeros(4, np.int32)
+        else:
+            w["table"] = w["table"][:, :2].copy()  # 16 positions: 11 + 5, 16 + 0 and 10 + 6 are the last
+        status = torch.full((4,), -1, dtype=torch.int32, device=dev())
+        paged.check_append(paged.call_append(lib, w, seq_status=status), w)
+        assert (status == 0).all()
+
+
+def replays(call, settings, results):
+    """call(), captured once, replayed on each setting of its inputs (functions that write them), with
+    eager work between, against the eager call on the same inputs, bit for bit."""
+    settings[0]()
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for setting in settings[1:] + settings[:1]:
+        got = []
+        for run in (call, graph.replay):
+            for x in results:
+                x.fill_(-3)  # (rows of no sequence keep that)
+            setting()
+            torch.cuda.synchronize()
+            run()
+            torch.randn(1 << 16, device=dev()).mul_(2.0)
+            torch.cuda.synchronize()
+            got.append([x.clone() for x in results])
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
+def test_captured_prompts_of_other_lengths(lib):  # noqa: F811
+    """Offsets are read on the GPU: one capture serves prompts of other lengths in as many rows."""
+    for shape, channel in (((4, 2, 128, 64, BF16), False), ((4, 2, 128, 64, BF16), True), ((2, 2, 64, 32, F32), False)):
+        w = make(78, [700, 200, 0], shape, channel=channel)
+        t = on_gpu(w)
+        H, out, offs = t["H0"].clone(), torch.zeros_like(t["v"]), g(w.offsets).clone()
+        call = lib.bind_linear_prefill(**dict(t, H0=H), seq_offsets=offs, out=out)
+
+        def lengths(*ends):
+            def setting():
+                H.copy_(t["H0"])
+                offs.copy_(torch.tensor([0, *ends], dtype=torch.int32))
+            return setting
+        replays(call, [lengths(700, 900, 900), lengths(1, 2, 900), lengths(900, 900, 900), lengths(300, 600, 880)], [out, H])
+
+
+def test_captured_prefix_attention_of_other_lengths(lib):  # noqa: F811
+    for shape in ((8, 2, 128, 16, BF16), (4, 2, 96, 16, F32)):
+        w = paged.make(79, [1] * 9, [40] * 9, ([1500, 200, 64], [0, 4, 7, 9]), shape)
+        t = paged.on_gpu(w)
+        plen, groups, clen = t["prefix_len"].clone(), t["group_offsets"].clone(), t["cache_len"].clone()
+        out = torch.zeros_like(t["q"])
+        call = lib.bind_prefix_attention(**dict(t, prefix_len=plen, group_offsets=groups, cache_len=clen), out=out)
+
+        def lengths(prefix, ends, cached):
+            def setting():
+                plen.copy_(torch.tensor(prefix, dtype=torch.int32))
+                groups.copy_(torch.tensor(ends, dtype=torch.int32))
+                clen.fill_(cached)
+            return setting
+        replays(call, [lengths([1500, 200, 64], [0, 4, 7, 9], 40), lengths([3, 0, 64], [0, 1, 7, 9], 7),
+                       lengths([1500, 1, 1], [0, 9, 9, 9], 0), lengths([0, 200, 0], [2, 2, 5, 6], 33)], [out])
