@@ -26,12 +26,14 @@
 // a step of bf16 of each pair weight, once, before an output that is rounded to bf16 itself). With
 // fp32 factors K, Q, V, P and S are three terms each.
 //
-// Measured, 32 heads of 128 x 64 states, bf16: eight prompts of up to 2048 tokens (9412 in all) 115 us
-// (33 the first kernel, 11 the second, 73 the third; 2.2 TB/s of what the call cannot do without), one
-// prompt of 32768 tokens and 8 key heads 241 us (72, 8 and 161; 1.7 TB/s). What bounds the third is
-// issue: a wavefront's chunk is some 510 vector instructions and 102 matrix ones, three workgroups a
-// CU, and the one kind hardly runs beside the other. With registers for two workgroups and the next
-// chunk's loads earlier it took 208 us for the long prompt, with three and no rows ahead 171.
+// Measured, 32 heads of 128 x 64 states, bf16: eight prompts of up to 2048 tokens (9412 in all) 116 us
+// (31 the first kernel, 10 the second, 71 the third; 2.2 TB/s of what the call cannot do without), one
+// prompt of 32768 tokens and 8 key heads 248 us (73, 8 and 163 to 171; 1.7 TB/s). In fp32 eight of up to
+// 1000 tokens take 155 us (38, 10 and 102), one workgroup a CU, as K, Q and V are three terms each in LDS.
+// What bounds the third is issue: a wavefront's chunk is some 510 vector instructions, about 200 of them
+// the splits of S and of the weighed V, and 102 matrix ones, three workgroups a CU, and the one kind
+// hardly runs beside the other. With registers for two workgroups and the next chunk's loads earlier it
+// took 208 us for the long prompt, with three and no rows ahead 171, when it took 161 as it is.
 #include "delta_mfma.h"
 #include "linear_device.h"
 #include "launch.h"
@@ -529,9 +531,9 @@ static bool chunked(const bole_linear_dims_t &d) {
 
 // Column tiles a wavefront: two, in bf16 from 65 columns on, where the call is cut into segments anyway
 // and has four chunks for each of 512 such workgroups: K's and Q's reads from LDS, and P, serve both then
-// (32 heads of 128 x 128: one 32768-token prompt 380 us, 448 with one tile; four of up to 2048 106 and
+// (32 heads of 128 x 128: one 32768-token prompt 389 us, 454 with one tile; four of up to 2048 106 and
 // 121). One otherwise, for twice the workgroups and three of them a CU in place of two (eight of up to
-// 2048 148, 175 with two; 16 of them 187 and 239; one of 300 tokens 32 and 40).
+// 2048 142, 173 with two; 16 of them 190 and 239; one of 300 tokens 32 and 40).
 static int column_tiles(const bole_linear_dims_t &d) {
     if (d.factor_dtype != BOLE_DTYPE_BF16 || d.d_v <= 64) return 1;
     const int64_t chunks = ((int64_t)d.total_tokens + kChunk - 1) / kChunk;
@@ -541,9 +543,9 @@ static int column_tiles(const bole_linear_dims_t &d) {
 
 // From a call's sizes alone. Segments so that 512 workgroups run, of at least four chunks, since each
 // costs a state's way through memory, and K and V are read twice (one 32768-token prompt of 32 heads
-// 240 us, with 256 workgroups 369, with 768 241; eight of up to 2048 tokens 115, 135 and 107; two of up
-// to 4096 58, 72 and 68). Where the sequences alone give 512, they are cut only from four times their
-// average length on (32 of up to 2048 tokens 215 us whole, 293 cut at twice the average).
+// 249 us, with 256 workgroups 359, with 768 238; eight of up to 2048 tokens 116, 132 and 103; two of up
+// to 4096 58, 69 and 66). Where the sequences alone give 512, they are cut only from four times their
+// average length on (32 of up to 2048 tokens 210 us whole, 291 cut at twice the average).
 static LinearPlan plan(const bole_linear_dims_t &d) {
     LinearPlan p;
     const int columns = 64 * column_tiles(d);

@@ -21,7 +21,7 @@ namespace bole {
 // prompt by the chain of its tokens, so prompts are cut into segments: a first kernel walks each
 // segment from nothing, a second runs over a sequence's segments and leaves the state that each starts
 // from, a third walks them again, with outputs. (Two prompts of up to 600 tokens, 32 heads of 128 x 64
-// states, decays a channel: 88 us, 490 in one chain.)
+// states, decays a channel: 86 to 89 us - 26, 20 and 39 - and 606 in one chain.)
 //
 // A segment's decays are multiplied in fp64, as their products may leave fp32 where what they scale is
 // small or zero, and kept below infinity, as zero has to stay that. A product in fp32's range goes on as
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(const LinearArgs a, co
         float share[SHARE];
     };
     // this token and the next one: with three or four the registers leave fewer wavefronts (7000 tokens of
-    // 32 heads with decays a channel 0.84 ms, 1.24 and 1.33)
+    // 32 heads with decays a channel 0.60 ms, 0.98 and 1.01)
     constexpr int AHEAD = MODE == kWalkStep ? 1 : 2;
     Token x[AHEAD];
     double all[SHARE];
@@ -283,7 +283,7 @@ hipError_t launch_linear_step_walk(const LinearArgs &a, const bole_linear_dims_t
 
 // Tokens a segment (0: sequences stay whole), from a call's sizes alone: segments so that 2048
 // wavefronts run, of at least 16 tokens, since each costs a state's way through memory (two prompts of
-// up to 600 tokens 88 us, with at least 32 104; four heads' 47 and 67).
+// up to 600 tokens 86 us, with at least 32 103; four heads' 46 and 67).
 static int walk_segment(const bole_linear_dims_t &d) {
     const int64_t blocks = d.d_v % 4 == 0 ? (d.d_v + 31) / 32 : (d.d_v + 7) / 8;
     if ((int64_t)d.batch * d.heads * blocks >= 2048) return 0;

@@ -9,13 +9,14 @@
 // [part][row][head], and a second kernel joins a row's parts.
 //
 // Measured, 32 query heads over 8 key heads of 128, bf16: 64 single tokens behind one prefix of 16384,
-// with up to 512 cached of their own, 50 us (45 and 7 for the join; 2.6 TB/s of the bytes that each
+// with up to 512 cached of their own, 50 us (40 to 45, and 7 for the join; 2.6 TB/s of the bytes that each
 // have to be read once, 350 TFLOP/s); 50 trees of up to 16 nodes, four prefixes of up to 8192 among
-// them, 74 to 80 us (68 and 12), 62 without tokens of their own; 4 tokens behind 1000 12 us, two launches
-// and the chains within. The larger two are bound by the prefix's workgroups, two a CU at most and of
-// one form: each has 64 keys at a time through registers to LDS, then products and exponentials behind
-// a barrier. Tried: the own tokens' workgroups first (59 against 45), touching the rows three tiles
-// ahead (52).
+// them, 74 us (63 and 12), 79 to 82 where three batches take turns, and 63 then without tokens of their
+// own; 4 tokens behind 1000 12 us, two launches and the chains within; two prompts of 8192 rows behind 8192
+// 3.9 ms (850 TFLOP/s), 315 us of it the join, as their sums pass through memory like all others. Tokens
+// and trees are bound by the prefix's workgroups, two a CU at most and of one form: each has 64 keys at a
+// time through registers to LDS, then products and exponentials behind a barrier. Tried: the own tokens'
+// workgroups first (59 against 45), touching the rows three tiles ahead (52).
 #include "prefix_device.h"
 #include "window_rows.h"
 #include "window_rows_f32.h"
@@ -320,12 +321,13 @@ static int parts_for(int64_t workgroups, int64_t keys, int wanted, int most) {
 
 // From a call's sizes alone: the tokens form for up to one of its tiles a list on average, as windowed
 // attention's rule; of own lists parts so that 512 workgroups run, of prefixes 256, one a CU with the
-// own lists' beside them, as a part's sums are written and read again (64 tokens over 16384: 51 us,
-// with 384 or 512 workgroups 59 and 64; 128 tokens 65, 66 and 69). Where that is three parts or fewer
-// it would leave some CUs two workgroups and others one: 512 (trees over one prefix of 8192 tokens 105
-// and 108 us in four and five parts, 113 in three), or 400 of several prefixes, whose parts are of like
-// length (50 trees over four prefixes of up to 8192: 81 us, with 256, 320 and 512 87, 82 and 84; 64 larger
-// ones 146, 208, 212 and 148). Of several prefixes one may have three times the average's parts. Lengths
+// own lists' beside them, as a part's sums are written and read again (three batches in turn: 64
+// tokens over 16384 50 us, with 384 or 512 workgroups 55 and 61; 128 tokens 77, 86 and 91). Where that is
+// three parts or fewer it would leave some CUs two workgroups and others one: 512 (trees of up to 64
+// nodes over one prefix of 8192, 24 of them 150 us, with 256 workgroups 157, 48 276 and 303; 64 of up to
+// 16 nodes, just past the edge, 140 and 128), or 400 of several prefixes, whose parts are of like length
+// (50 trees over four prefixes of up to 8192: 81 us, with 256, 320 and 512 87, 81 and 86; 64 larger ones
+// 146, 209, 212 and 146). Of several prefixes one may have three times the average's parts. Lengths
 // are not known here: the longest count.
 static PrefixPlan plan(const bole_prefix_dims_t &d) {
     PrefixPlan p;
