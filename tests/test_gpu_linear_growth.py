@@ -8,6 +8,8 @@ has both roots' two steps and a rounding more, 5 2^-24. Over a prompt the argume
 at most the sum A of |log2 gate|, and n tokens have at most n / 64 + 1 chunks and as many segments: A +
 10 (n / 64 + 1) steps of 2^-24 of the terms' magnitudes more.
 """
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 
@@ -99,3 +101,22 @@ def test_walked(lib, shape, case, channel):  # noqa: F811
     w = case(shape, channel=channel)
     t = on_gpu(w)
     check(lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets), force_generic=True), t["H0"], w, False)
+
+
+@pytest.mark.parametrize("shape", [(64, 32, 128, 128, BF16), (64, 32, 64, 128, BF16), (64, 16, 72, 136, BF16)], ids=str)
+def test_chunked_in_128_columns(lib, shape):  # noqa: F811
+    """The form with 128 columns a workgroup, where one segment of many grows; some heads against the oracle."""
+    w = make(55, [2160, 90], shape, gate_value=None)
+    w.gate.copy_(w.gate ** 0.02)
+    for at in (700, 2200):
+        lo = 0 if at < 2160 else 2160
+        w.H0[int(lo > 0)] *= 1e-30
+        w.v[lo:at + 2] *= 1e-30
+        w.gate[at:at + 2], w.gate[at + 2:at + 4] = 1e20, 1e-20
+    t = on_gpu(w)
+    out = lib.bole_linear_prefill(**t, seq_offsets=g(w.offsets))
+    heads = [0, 37, 63]
+    keys = [h // (shape[0] // shape[1]) for h in heads]
+    part = SimpleNamespace(H0=w.H0[:, heads], q=w.q[:, keys], k=w.k[:, keys], v=w.v[:, heads], gate=w.gate[:, heads],
+                           offsets=w.offsets)
+    check(out[:, heads], t["H0"][:, heads], part, True)
